@@ -314,6 +314,60 @@ SV_API sv_status_t spec_token_likelihood(const sv_shape_t* shape,
                               size_t* workspace_bytes,
                               hipStream_t stream);
 
+/*
+ * Beam search's selection, the counterpart of spec_draft_sample for callers
+ * that follow the best continuations instead of drawing one ("Text Generation
+ * via Speculative Sampling, KV Caching, and OpenVINO", section "Prepare
+ * autoregressive sampling", decodes by the argmax, the selection of one beam).
+ * A group (one request) has `beams` hypotheses; row g * beams + w of `logits`
+ * holds beam w's next-token logits.  Candidate (w, v) extends beam w by token
+ * v and scores
+ *     s(w, v) = scores[w] + logits[w, v] / T - log sum_u exp(logits[w, u] / T).
+ * The num_select candidates of largest s are written in falling order, equal
+ * scores in rising order of w * vocab + v.  The order is that of the scores in
+ * fp64, formed as (scores[w] - log S_w) + (l - m_w) / T with m_w the row's
+ * largest logit and S_w = sum_u exp((l_u - m_w) / T).
+ *   A finished beam (finished[row] != 0) has one candidate, pad_token at its
+ *   own score; its logits are not read.  A beam whose score is not finite (a
+ *   place not yet in use has -inf) and a row with no finite logit, or with a
+ *   NaN or +inf logit, have none.  A logit of -inf is no candidate.
+ * Arguments
+ *   logits [groups * beams, row_stride] in shape->dtype; scores float
+ *   [groups * beams]; finished (nullable) one byte [groups * beams].
+ *   temperature as for spec_verify_sample; pad_token in [0, vocab).
+ *   out_scores float, out_tokens int32 and out_parents int32
+ *   [groups * num_select]: the candidate's score, its token, and the beam it
+ *   extends (0 .. beams - 1, within its group).  Places that no candidate
+ *   fills hold -inf, -1, -1.
+ *   1 <= beams <= SV_MAX_BEAMS, 1 <= num_select <= SV_MAX_SELECT.
+ * Outputs may not overlap inputs.  Memory, execution, workspace and errors as
+ * for spec_verify_sample.
+ */
+#define SV_MAX_BEAMS 64
+#define SV_MAX_SELECT 128
+
+typedef struct {
+    int32_t groups;     /* G >= 1                                 */
+    int32_t beams;      /* W: hypotheses per group                */
+    int32_t vocab;      /* V >= 1                                 */
+    int32_t num_select; /* candidates to keep per group           */
+    sv_dtype_t dtype;   /* element type of the logits             */
+    int64_t row_stride; /* elements between logit rows, >= V      */
+} sv_beam_shape_t;
+
+SV_API sv_status_t spec_beam_select(const sv_beam_shape_t* shape,
+                              const void* logits,
+                              const float* scores,
+                              const uint8_t* finished,
+                              float temperature,
+                              int32_t pad_token,
+                              float* out_scores,
+                              int32_t* out_tokens,
+                              int32_t* out_parents,
+                              void* workspace,
+                              size_t* workspace_bytes,
+                              hipStream_t stream);
+
 /* A static, human-readable name for a status code. */
 SV_API const char* spec_verify_status_string(sv_status_t status);
 

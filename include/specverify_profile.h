@@ -62,6 +62,12 @@ SV_API sv_status_t spec_token_likelihood_profiled(const sv_profile_events_t* eve
                                                   float top_p, float* out_terms, float* out_beta, double* out_nll,
                                                   void* workspace, size_t* workspace_bytes, hipStream_t stream);
 
+SV_API sv_status_t spec_beam_select_profiled(const sv_profile_events_t* events, const sv_beam_shape_t* shape,
+                                             const void* logits, const float* scores, const uint8_t* finished,
+                                             float temperature, int32_t pad_token, float* out_scores,
+                                             int32_t* out_tokens, int32_t* out_parents, void* workspace,
+                                             size_t* workspace_bytes, hipStream_t stream);
+
 /*
  * A plain streaming read, the practical roof the streaming passes are
  * measured against: every 16-byte block of [data, data + bytes) is loaded

@@ -22,3 +22,7 @@ from .binding import (  # noqa: F401
     verify_sample_noalloc,
     workspace_bytes,
 )
+from .beam import (  # noqa: F401
+    BeamSelectPlan,
+    beam_select,
+)

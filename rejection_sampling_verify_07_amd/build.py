@@ -2,14 +2,17 @@
 import os
 import shutil
 import subprocess
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libspecverify.so")
+SOURCES = ("specverify.hip", "beam.hip")
 
 HIPCC_FLAGS = [
-    "-O3", "-std=c++17", "--offload-arch=gfx950", "-fPIC", "-shared",
+    "-O3", "-std=c++17", "--offload-arch=gfx950", "-fPIC",
     "-Wall", "-Wno-unused-result",
     # keep the compiler from emitting packed-fp32 VALU instructions
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
@@ -34,14 +37,22 @@ def build(verbose: bool = False, out: str = LIB, defines=(), host_sanitize: bool
     """Compile the HIP sources into rejection_sampling_verify_07_amd/libspecverify.so
     (or `out`, with extra -D defines, for tuning builds; host_sanitize: a host
     ASan/UBSan build for the CPU tests of the argument checks)."""
-    src = os.path.join(CSRC, "specverify.hip")
     tmp = out + ".tmp"
     extra = HOST_SANITIZE_FLAGS if host_sanitize else []
-    cmd = [hipcc_path(), *HIPCC_FLAGS, *extra, *[f"-D{d}" for d in defines], "-I", os.path.join(ROOT, "include"),
-           "-I", CSRC, src, "-o", tmp]
-    if verbose:
-        print(" ".join(cmd))
-    subprocess.run(cmd, check=True)
+    flags = [*HIPCC_FLAGS, *extra, *[f"-D{d}" for d in defines], "-I", os.path.join(ROOT, "include"), "-I", CSRC]
+
+    def run(cmd):
+        if verbose:
+            print(" ".join(cmd))
+        subprocess.run(cmd, check=True)
+
+    # one object per source, compiled side by side
+    with tempfile.TemporaryDirectory() as objdir:
+        objs = [os.path.join(objdir, os.path.splitext(src)[0] + ".o") for src in SOURCES]
+        with ThreadPoolExecutor(len(SOURCES)) as pool:
+            list(pool.map(lambda so: run([hipcc_path(), *flags, "-c", os.path.join(CSRC, so[0]), "-o", so[1]]),
+                          zip(SOURCES, objs)))
+        run([hipcc_path(), *HIPCC_FLAGS, "-shared", *extra, *objs, "-o", tmp])
     os.replace(tmp, out)
     return out
 

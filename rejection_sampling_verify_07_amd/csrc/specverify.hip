@@ -13,6 +13,7 @@
 #include <type_traits>
 
 #include "sv_common.hpp"
+#include "sv_host.hpp"
 #include "sv_stats.hpp"
 #include "sv_topk.hpp"
 #include "sv_select.hpp"
@@ -79,7 +80,6 @@ int32_t split_groups(int32_t batch, int32_t vocab)
     return g < 2 ? 1 : g;
 }
 constexpr int32_t kDraftSmallRowsMin = 512;  // draft rows from which full-row draft draws use smaller workgroups
-constexpr size_t kAlign = 256;
 // XCDs of an MI355X: workgroups are dealt to them in turn, workgroup g to XCD g mod 8
 #ifndef SV_XCDS
 #define SV_XCDS 8
@@ -105,55 +105,6 @@ struct Plan {
     size_t off_partials, off_counts, off_bounds, off_cands, off_descs, off_kept, off_pair, off_segsum, off_tickets,
         bytes;
 };
-
-size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
-
-int vec_of(sv_dtype_t dt) { return dt == SV_DTYPE_F32 ? 4 : 8; }
-size_t esize_of(sv_dtype_t dt) { return dt == SV_DTYPE_F32 ? 4 : 2; }
-
-// Calls fn with std::integral_constant<int, DT> for the element type
-// (the shape check has already rejected any other value).
-template <class F>
-sv_status_t by_dtype(sv_dtype_t dt, F&& fn)
-{
-    switch (dt) {
-        case SV_DTYPE_F32: return fn(std::integral_constant<int, sv::DT_F32>{});
-        case SV_DTYPE_BF16: return fn(std::integral_constant<int, sv::DT_BF16>{});
-        case SV_DTYPE_F16: return fn(std::integral_constant<int, sv::DT_F16>{});
-    }
-    return SV_ERR_INVALID_ARGUMENT;
-}
-
-// Chunks per row of the streaming passes: a row with start misalignment up
-// to VEC-1 elements touches at most ceil((V + VEC - 1) / VEC) blocks.
-int32_t chunks_for(int32_t vocab, int vec, int loads)
-{
-    const int64_t nblk = ((int64_t)vocab + 2 * vec - 2) / vec;
-    const int64_t per = (int64_t)sv::kThreads * loads;
-    return (int32_t)((nblk + per - 1) / per);
-}
-
-// Launch a streaming-pass kernel, one tile per workgroup.  With `prof`
-// (the benchmark entry points), the launch itself records the caller's
-// events right before and after the kernel on the call's stream.
-template <class K, class... Args>
-void launch_stream_nt(const sv_profile_events_t* prof, K kernel, uint32_t ntiles, uint32_t nt, hipStream_t s,
-                      Args... args)
-{
-    if (prof != nullptr) {
-        hipExtLaunchKernelGGL(kernel, dim3(ntiles), dim3(nt), 0, s, prof->start, prof->stop, 0, args...);
-    } else {
-        hipLaunchKernelGGL(kernel, dim3(ntiles), dim3(nt), 0, s, args...);
-    }
-}
-
-template <class K, class... Args>
-void launch_stream(const sv_profile_events_t* prof, K kernel, uint32_t ntiles, hipStream_t s, Args... args)
-{
-    launch_stream_nt(prof, kernel, ntiles, sv::kThreads, s, args...);
-}
-
-bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
 
 // The caller's dtype field as an integer.  A C caller may store any int in
 // it; reading a value outside the enumerators through the C++ enum type is
@@ -272,18 +223,6 @@ Plan make_plan(const sv_shape_t* sh, CallKind kind, int32_t top_k, float top_p =
     }
     p.bytes = off == 0 ? kAlign : off;
     return p;
-}
-
-template <class T>
-T* ws_at(void* ws, size_t off)
-{
-    return reinterpret_cast<T*>(static_cast<char*>(ws) + off);
-}
-
-sv_status_t launch_status()
-{
-    const hipError_t e = hipGetLastError();
-    return e == hipSuccess ? SV_OK : SV_ERR_HIP;
 }
 
 // The streaming pass and, with top-k, the per-row select over the rows of rs:
@@ -544,9 +483,6 @@ sv_status_t run_greedy(const sv_shape_t* sh, const Plan& p, const void* tgt, con
                        stream, ga);
     return launch_status();
 }
-
-// c = fl32(log2(e) / T): the softmax's exp(l / T) is computed as exp2(l * c).
-float scale_of(float temperature) { return (float)(1.4426950408889634 / (double)temperature); }
 
 // Temperature, top-k and top-p arguments shared by the sampling calls.  A
 // temperature so small that c overflows fp32 (T below about 4.2e-39) is

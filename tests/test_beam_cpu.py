@@ -1,0 +1,92 @@
+"""Argument checks of the beam-decoding calls: no GPU is needed, nothing here
+reaches a launch."""
+import ctypes as C
+
+import pytest
+import torch
+
+FAKE = 1 << 40  # never dereferenced
+
+
+@pytest.fixture(scope="module")
+def B():
+    import os
+
+    from rejection_sampling_verify_07_amd import beam, binding
+
+    if not os.path.exists(binding.LIB_PATH):
+        from rejection_sampling_verify_07_amd import build
+
+        build.build()
+    binding.load_library()
+    return beam
+
+
+@pytest.fixture(scope="module")
+def lib(B):
+    return B.load_library()
+
+
+def _beam_shape(B, **kw):
+    d = dict(groups=2, beams=4, vocab=1000, num_select=8, dtype=1, row_stride=1000)
+    d.update(kw)
+    return B.BeamShapeT(**d)
+
+
+def _select(lib, sh, T=1.0, pad=0, logits=FAKE, scores=FAKE, fin=None, o=(FAKE, FAKE, FAKE), ws=None, have=0):
+    n = C.c_size_t(have)
+    st = lib.spec_beam_select(C.byref(sh) if sh is not None else None, logits, scores, fin, T, pad, *o, ws,
+                              C.byref(n), None)
+    return st, n.value
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(), 0), (dict(groups=0), 1), (dict(beams=0), 1), (dict(vocab=0), 1), (dict(num_select=0), 1),
+    (dict(row_stride=999), 1), (dict(dtype=3), 1), (dict(dtype=-1), 1), (dict(beams=64, num_select=128), 0),
+    (dict(beams=65), 2), (dict(num_select=129), 2),
+    (dict(vocab=(1 << 20) + 1, row_stride=1 << 21), 2), (dict(vocab=1 << 20, row_stride=1 << 20), 0),
+    (dict(groups=1 << 30), 2), (dict(groups=1 << 24, row_stride=1 << 40), 2)])
+def test_select_shapes(B, lib, kw, code):
+    st, n = _select(lib, _beam_shape(B, **kw))
+    assert st == code
+    if code == 0:
+        assert n > 0 and n % 256 == 0
+
+
+@pytest.mark.parametrize("T,pad,code", [(0.0, 0, 1), (-1.0, 0, 1), (float("nan"), 0, 1), (float("inf"), 0, 1),
+                                        (1e-39, 0, 1), (4.3e-39, 0, 0), (1.0, -1, 1), (1.0, 1000, 1), (1.0, 999, 0)])
+def test_select_arguments(B, lib, T, pad, code):
+    assert _select(lib, _beam_shape(B), T, pad)[0] == code
+
+
+def test_select_pointers(B, lib):
+    sh = _beam_shape(B)
+    need = _select(lib, sh)[1]
+    ok = dict(ws=FAKE, have=need)
+    for bad in (dict(logits=None), dict(logits=FAKE + 1), dict(scores=None), dict(scores=FAKE + 2),
+                dict(o=(None, FAKE, FAKE)), dict(o=(FAKE, None, FAKE)), dict(o=(FAKE, FAKE, None)),
+                dict(o=(FAKE + 1, FAKE, FAKE)), dict(o=(FAKE, FAKE + 2, FAKE)), dict(o=(FAKE, FAKE, FAKE + 3)),
+                dict(ws=FAKE + 128)):
+        assert _select(lib, sh, **{**ok, **bad})[0] == 1, bad
+    assert _select(lib, sh, ws=FAKE, have=need - 1)[0] == 3
+    assert _select(lib, None)[0] == 1
+    assert lib.spec_beam_select(C.byref(sh), FAKE, FAKE, None, 1.0, 0, FAKE, FAKE, FAKE, FAKE, None, None) == 1
+    # the benchmark form checks alike
+    n = C.c_size_t(0)
+    assert lib.spec_beam_select_profiled(None, C.byref(sh), None, None, None, 1.0, 0, None, None, None, None,
+                                         C.byref(n), None) == 0
+    assert n.value == need
+
+
+def test_select_binding_refusals(B):
+    x, s = torch.zeros(8, 100), torch.zeros(8)
+    with pytest.raises(ValueError, match="multiple of beams"):
+        B.beam_select(x, s, 3)
+    with pytest.raises(ValueError, match="2-D"):
+        B.beam_select(x[0], s, 1)
+    with pytest.raises(TypeError, match="logits must be"):
+        B.beam_select(x.double(), s, 4)
+    with pytest.raises(ValueError, match="num_select"):
+        B.beam_select(x, s, 4, 0)
+    with pytest.raises(ValueError, match="GPU"):
+        B.beam_select(x, s, 4)
