@@ -368,6 +368,51 @@ SV_API sv_status_t spec_beam_select(const sv_beam_shape_t* shape,
                               size_t* workspace_bytes,
                               hipStream_t stream);
 
+/*
+ * Reorder of beam states, in place, the step after a selection: place w of
+ * group g takes the state of beam parents[g * beams + w] of the same group.
+ * A state is a cache of keys or values, a token history or anything else that
+ * is indexed by beam; its bytes are moved as they are.  The tensor is
+ *     states[slab][g * beams + w][head][position][0 .. row_bytes)
+ * with any strides whose places are distinct.  A cache [layers, batch,
+ * positions, heads * dim] has heads = 1 and one slab per layer (keys and
+ * values in one allocation: two); [layers, batch, heads, positions, dim] has
+ * its heads; a state with no position has positions = 1.
+ *   Only positions below the parent's length move: place w receives positions
+ *   0 .. lengths[g * beams + parent] - 1 and keeps its others.  lengths
+ *   (nullable: every beam holds all positions) is read, not reordered.
+ *   A parent outside [0, beams), as spec_beam_select's -1, and a parent equal
+ *   to w leave the place as it was.  A length below 0 counts as 0, one above
+ *   `positions` as `positions`.
+ * Arguments
+ *   states: device memory, read and written; parents int32 [groups * beams];
+ *   lengths int32 [groups * beams] or NULL.  Strides are in bytes.
+ * Errors: SV_ERR_INVALID_ARGUMENT (null or misaligned pointer, a count < 1,
+ * positions, row_bytes or a stride < 0, places that overlap),
+ * SV_ERR_UNSUPPORTED (beams > SV_MAX_BEAMS, or one slab and head of a beam of
+ * more than 2^31 - 1 pieces, a piece being 16, 4, 2 or 1 bytes as the
+ * alignment of states, row_bytes and the strides allows), SV_ERR_HIP.  Execution as for
+ * spec_verify_sample; no workspace.
+ */
+typedef struct {
+    int32_t slabs;           /* >= 1: layers, or layers * 2                  */
+    int32_t groups;          /* G >= 1                                       */
+    int32_t beams;           /* W: places per group                          */
+    int32_t heads;           /* >= 1                                         */
+    int32_t positions;       /* >= 0                                         */
+    int64_t row_bytes;       /* contiguous bytes per position (and head)     */
+    int64_t slab_stride;     /* bytes                                        */
+    int64_t beam_stride;     /* bytes; beam w of group g is row g * W + w     */
+    int64_t head_stride;     /* bytes                                        */
+    int64_t position_stride; /* bytes                                        */
+} sv_state_shape_t;
+
+SV_API sv_status_t spec_state_reorder(const sv_state_shape_t* shape,
+                                void* states,
+                                const int32_t* parents,
+                                const int32_t* lengths,
+                                hipStream_t stream);
+
 /* A static, human-readable name for a status code. */
 SV_API const char* spec_verify_status_string(sv_status_t status);
 

@@ -68,6 +68,10 @@ SV_API sv_status_t spec_beam_select_profiled(const sv_profile_events_t* events, 
                                              int32_t* out_tokens, int32_t* out_parents, void* workspace,
                                              size_t* workspace_bytes, hipStream_t stream);
 
+SV_API sv_status_t spec_state_reorder_profiled(const sv_profile_events_t* events, const sv_state_shape_t* shape,
+                                               void* states, const int32_t* parents, const int32_t* lengths,
+                                               hipStream_t stream);
+
 /*
  * A plain streaming read, the practical roof the streaming passes are
  * measured against: every 16-byte block of [data, data + bytes) is loaded

@@ -24,5 +24,7 @@ from .binding import (  # noqa: F401
 )
 from .beam import (  # noqa: F401
     BeamSelectPlan,
+    StateReorderPlan,
     beam_select,
+    reorder_states,
 )

@@ -24,6 +24,13 @@ class BeamShapeT(C.Structure):
                 ("dtype", C.c_int32), ("row_stride", C.c_int64)]
 
 
+class StateShapeT(C.Structure):
+    """sv_state_shape_t."""
+    _fields_ = [("slabs", C.c_int32), ("groups", C.c_int32), ("beams", C.c_int32), ("heads", C.c_int32),
+                ("positions", C.c_int32), ("row_bytes", C.c_int64), ("slab_stride", C.c_int64),
+                ("beam_stride", C.c_int64), ("head_stride", C.c_int64), ("position_stride", C.c_int64)]
+
+
 def _on(dev, stream):
     """A context in which `dev` is the current device and `stream` (default:
     the device's current one) its current stream, and that stream."""
@@ -140,3 +147,61 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, beams: int, num_sele
     """
     return BeamSelectPlan(logits, scores, beams, num_select, temperature, finished, pad_token, out, workspace,
                           stream)()
+
+
+class StateReorderPlan(_DevicePlan):
+    """spec_state_reorder with every argument marshalled once: __call__
+    enqueues one reorder and returns `states`.  See reorder_states."""
+
+    name = "spec_state_reorder"
+
+    def __init__(self, states, parents, beams, lengths=None, stream=None):
+        lib = load_library()
+        beams = int(beams)
+        if states.dim() not in (2, 3, 4, 5):
+            raise ValueError("states must be [batch, row], [batch, positions, row], [slabs, batch, positions, row] or "
+                             "[slabs, batch, heads, positions, row]")
+        if states.device.type != "cuda":
+            raise ValueError("states must be on a GPU")
+        # every form as [slabs, batch, heads, positions, row]
+        v = states
+        if v.dim() == 2:
+            v = v[None, :, None, None, :]
+        elif v.dim() == 3:
+            v = v[None, :, None, :, :]
+        elif v.dim() == 4:
+            v = v[:, :, None, :, :]
+        slabs, batch, heads, positions, row = v.shape
+        if beams < 1 or batch < 1 or batch % beams != 0:
+            raise ValueError(f"states holds {batch} beams; a multiple of beams = {beams} is needed")
+        if slabs < 1 or heads < 1:
+            raise ValueError("states needs at least one slab and one head")
+        if row > 1 and v.stride(4) != 1:
+            raise ValueError("states must have unit stride in its last dimension")
+        dev = states.device
+        es = states.element_size()
+        shape = StateShapeT(slabs, batch // beams, beams, heads, positions, row * es,
+                            *(v.stride(i) * es for i in range(4)))
+        ctx, s = _on(dev, stream)
+        self.out, self.dev, self.shape = states, dev, shape
+        self._keep = (parents, lengths, s)
+        self.args = (C.byref(shape), C.c_void_p(states.data_ptr()),
+                     _vector(parents, "parents", batch, torch.int32, dev),
+                     None if lengths is None else _vector(lengths, "lengths", batch, torch.int32, dev),
+                     C.c_void_p(s.cuda_stream))
+        self.fn, self.fn_profiled = lib.spec_state_reorder, lib.spec_state_reorder_profiled
+
+
+def reorder_states(states: torch.Tensor, parents: torch.Tensor, beams: int, lengths: Optional[torch.Tensor] = None,
+                   stream=None) -> torch.Tensor:
+    """Beam states put in the order of their parents, in place, on the GPU
+    (spec_state_reorder).
+
+    states: any dtype, [batch, row], [batch, positions, row], [slabs, batch,
+    positions, row] or [slabs, batch, heads, positions, row], batch = groups *
+    beams, any strides without overlap (last dimension contiguous); parents int32
+    [groups * beams] or [groups, beams], as beam_select returns them; lengths
+    int32, the positions that each beam holds (as before the reorder).
+    Returns `states`.
+    """
+    return StateReorderPlan(states, parents, beams, lengths, stream)()

@@ -43,3 +43,17 @@ def select_ref(logits, scores, beams, n, T=1.0, finished=None, pad_token=0):
 def widen(t):
     """A tensor's values as float64 on the host (exact for the 16-bit types)."""
     return t.detach().cpu().double().numpy()
+
+
+def reorder_ref(states, parents, beams, lengths=None):
+    """The reorder of a host tensor [slabs, batch, heads, positions, row], out of place."""
+    out = states.clone()
+    _, batch, _, positions, _ = states.shape
+    for b in range(batch):
+        g, q = b // beams, int(parents[b])
+        if q < 0 or q >= beams:
+            continue
+        src = g * beams + q
+        n = positions if lengths is None else max(0, min(positions, int(lengths[src])))
+        out[:, b, :, :n] = states[:, src, :, :n]
+    return out

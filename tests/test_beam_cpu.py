@@ -90,3 +90,47 @@ def test_select_binding_refusals(B):
         B.beam_select(x, s, 4, 0)
     with pytest.raises(ValueError, match="GPU"):
         B.beam_select(x, s, 4)
+
+
+# ---- spec_state_reorder
+def _state_shape(B, **kw):
+    d = dict(slabs=2, groups=2, beams=4, heads=3, positions=10, row_bytes=32, slab_stride=8 * 960, beam_stride=960,
+             head_stride=320, position_stride=32)
+    d.update(kw)
+    return B.StateShapeT(**d)
+
+
+def _reorder(lib, sh, states=FAKE, parents=FAKE, lengths=None):
+    return lib.spec_state_reorder(C.byref(sh) if sh is not None else None, states, parents, lengths, None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(slabs=0), 1), (dict(groups=0), 1), (dict(beams=0), 1), (dict(heads=0), 1), (dict(positions=-1), 1),
+    (dict(row_bytes=-1), 1), (dict(beams=65), 2), (dict(slab_stride=-1), 1), (dict(beam_stride=-960), 1),
+    (dict(position_stride=31), 1), (dict(head_stride=319), 1), (dict(beam_stride=0), 1), (dict(slab_stride=7679), 1),
+    (dict(position_stride=0), 1), (dict(beam_stride=1 << 62), 1),
+    (dict(slabs=1, groups=1, beams=2, heads=1, positions=2, row_bytes=1 << 36, beam_stride=1 << 38,
+          position_stride=1 << 36), 2),
+    (dict(slabs=1 << 24, groups=1 << 8, beams=4, heads=3, slab_stride=960 << 10), 2)])
+def test_reorder_shapes(B, lib, kw, code):
+    assert _reorder(lib, _state_shape(B, **kw)) == code
+
+
+def test_reorder_pointers(B, lib):
+    sh = _state_shape(B)
+    assert _reorder(lib, None) == 1
+    assert _reorder(lib, sh, states=None) == 1
+    assert _reorder(lib, sh, parents=None) == 1
+    assert _reorder(lib, sh, parents=FAKE + 2) == 1
+    assert _reorder(lib, sh, lengths=FAKE + 2) == 1
+    # no position, no bytes: nothing to move, nothing launched
+    assert _reorder(lib, _state_shape(B, positions=0), states=None) == 0
+    assert _reorder(lib, _state_shape(B, row_bytes=0), states=None) == 0
+
+
+def test_reorder_binding_refusals(B):
+    par = torch.zeros(8, dtype=torch.int32)
+    with pytest.raises(ValueError, match="states must be"):
+        B.reorder_states(torch.zeros(8), par, 4)
+    with pytest.raises(ValueError, match="GPU"):
+        B.reorder_states(torch.zeros(8, 3), par, 4)
