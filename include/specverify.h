@@ -413,6 +413,84 @@ SV_API sv_status_t spec_state_reorder(const sv_state_shape_t* shape,
                                 const int32_t* lengths,
                                 hipStream_t stream);
 
+/*
+ * Attention of a batch whose sequences share long prefixes: the beams of a
+ * request, several samples of one prompt, or requests under one system prompt,
+ * at a decode step or in the scoring pass that a verify judges ("Text
+ * Generation via Speculative Sampling, KV Caching, and OpenVINO", its KV
+ * caching, with the prompt's cache held and read once per group).
+ *   The batch is that of spec_verify_sample: sequence b has K_b + 1 query rows
+ *   (K_b = 0: a plain decode step), row cu_draft[b] + b + k for k = 0..K_b.
+ *   Group g holds sequences cu_groups[g] .. cu_groups[g+1] - 1 (NULL:
+ *   batch / groups each) and one prefix of prefix_lengths[g] positions; b's
+ *   own cache holds suffix_lengths[b] positions, the keys and values of its
+ *   K_b + 1 newest rows last.  Row k sees the whole prefix and the suffix
+ *   positions j with j <= suffix_lengths[b] - 1 - K_b + k:
+ *     a_j = scale * q . k_j,  lse = log sum_j exp(a_j),  out = sum_j exp(a_j - lse) v_j,
+ *   where query head h reads key/value head h / (q_heads / kv_heads).  A row
+ *   that sees nothing gets zeros and lse = -inf.
+ *   Lengths below 0 count as 0, above max_prefix / max_suffix as that; NULL
+ *   lengths are max_prefix / max_suffix.  Positions behind a length are not read.
+ * Arguments
+ *   q and out [total_draft + batch][q_heads][head_dim]; a cache is
+ *   data[group or sequence][position][head][head_dim], all of shape->dtype,
+ *   strides in elements, the last dimension contiguous.  prefix_k and
+ *   prefix_v may be NULL when max_prefix is 0, the suffix's when max_suffix is.
+ *   q and the caches lie on 16-byte places (pointers, and strides of a
+ *   multiple of 8 elements), out on 8-byte ones.
+ *   out_lse (nullable) float [total_draft + batch][q_heads].
+ *   scale > 0 and finite (usually 1 / sqrt(head_dim)).
+ *   dtype SV_DTYPE_BF16 or SV_DTYPE_F16; head_dim 64, 128 or 256.
+ *   Sums, softmax statistics and scores are fp32; the softmax weights are
+ *   rounded to dtype for the product with v.
+ * Errors as for spec_verify_sample; SV_ERR_INVALID_ARGUMENT also for q_heads
+ * no multiple of kv_heads; SV_ERR_UNSUPPORTED also for fp32, another head_dim,
+ * more than 2^30 positions, or positions more than 64 MB apart.  Data
+ * preconditions: keys and values within the lengths finite; cu_draft and
+ * cu_groups prefix sums, no group larger than max_group.  Where they are
+ * violated, out holds unspecified values and nothing out of bounds is read or
+ * written.  out may not overlap the inputs.
+ */
+typedef struct {
+    const void* data;
+    int64_t batch_stride;    /* elements between groups (prefix) or sequences (suffix) */
+    int64_t position_stride; /* elements */
+    int64_t head_stride;     /* elements */
+} sv_cache_t;
+
+typedef struct {
+    int32_t groups;          /* G >= 1                                              */
+    int32_t batch;           /* B >= 1 sequences                                    */
+    int32_t max_group;       /* the largest group's sequences (read with cu_groups) */
+    int32_t max_draft;       /* K, or the largest K_b when cu_draft != NULL         */
+    int32_t total_draft;     /* sum_b K_b; must be B*K when cu_draft == NULL        */
+    int32_t q_heads;
+    int32_t kv_heads;
+    int32_t head_dim;
+    int32_t max_prefix;      /* positions a prefix cache holds                      */
+    int32_t max_suffix;      /* positions a suffix cache holds                      */
+    sv_dtype_t dtype;
+    int64_t q_row_stride, q_head_stride;
+    int64_t out_row_stride, out_head_stride;
+    const int32_t* cu_draft;       /* device [B+1], or NULL */
+    const int32_t* cu_groups;      /* device [G+1], or NULL */
+    const int32_t* prefix_lengths; /* device [G], or NULL   */
+    const int32_t* suffix_lengths; /* device [B], or NULL   */
+} sv_attention_shape_t;
+
+SV_API sv_status_t spec_prefix_attention(const sv_attention_shape_t* shape,
+                                   const void* q,
+                                   const sv_cache_t* prefix_k,
+                                   const sv_cache_t* prefix_v,
+                                   const sv_cache_t* suffix_k,
+                                   const sv_cache_t* suffix_v,
+                                   float scale,
+                                   void* out,
+                                   float* out_lse,
+                                   void* workspace,
+                                   size_t* workspace_bytes,
+                                   hipStream_t stream);
+
 /* A static, human-readable name for a status code. */
 SV_API const char* spec_verify_status_string(sv_status_t status);
 

@@ -4,7 +4,7 @@
  * Each *_profiled call below is the call of the same name in specverify.h
  * with one more leading argument, `events`.  When `events` is non-NULL, the call records
  * events->start on its stream right before the launch of its streaming pass
- * (the kernel that reads every logit row once) and events->stop right after
+ * (the kernel that reads every logit row, state or cache once) and events->stop right after
  * it, so that hipEventElapsedTime(start, stop) is that kernel's duration.
  * With events == NULL a call is exactly its plain counterpart.
  *
@@ -71,6 +71,12 @@ SV_API sv_status_t spec_beam_select_profiled(const sv_profile_events_t* events, 
 SV_API sv_status_t spec_state_reorder_profiled(const sv_profile_events_t* events, const sv_state_shape_t* shape,
                                                void* states, const int32_t* parents, const int32_t* lengths,
                                                hipStream_t stream);
+
+SV_API sv_status_t spec_prefix_attention_profiled(const sv_profile_events_t* events, const sv_attention_shape_t* shape,
+                                                  const void* q, const sv_cache_t* prefix_k,
+                                                  const sv_cache_t* prefix_v, const sv_cache_t* suffix_k,
+                                                  const sv_cache_t* suffix_v, float scale, void* out, float* out_lse,
+                                                  void* workspace, size_t* workspace_bytes, hipStream_t stream);
 
 /*
  * A plain streaming read, the practical roof the streaming passes are

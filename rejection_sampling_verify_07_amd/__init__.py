@@ -24,7 +24,9 @@ from .binding import (  # noqa: F401
 )
 from .beam import (  # noqa: F401
     BeamSelectPlan,
+    PrefixAttentionPlan,
     StateReorderPlan,
     beam_select,
+    prefix_attention,
     reorder_states,
 )

@@ -31,16 +31,28 @@ class StateShapeT(C.Structure):
                 ("beam_stride", C.c_int64), ("head_stride", C.c_int64), ("position_stride", C.c_int64)]
 
 
+class CacheT(C.Structure):
+    """sv_cache_t."""
+    _fields_ = [("data", C.c_void_p), ("batch_stride", C.c_int64), ("position_stride", C.c_int64),
+                ("head_stride", C.c_int64)]
+
+
+class AttentionShapeT(C.Structure):
+    """sv_attention_shape_t."""
+    _fields_ = ([(n, C.c_int32) for n in ("groups", "batch", "max_group", "max_draft", "total_draft", "q_heads",
+                                          "kv_heads", "head_dim", "max_prefix", "max_suffix", "dtype")]
+                + [(n, C.c_int64) for n in ("q_row_stride", "q_head_stride", "out_row_stride", "out_head_stride")]
+                + [(n, C.c_void_p) for n in ("cu_draft", "cu_groups", "prefix_lengths", "suffix_lengths")])
+
+
 def _on(dev, stream):
-    """A context in which `dev` is the current device and `stream` (default:
-    the device's current one) its current stream, and that stream."""
+    """A context whose allocations on `dev` belong to `stream` (default: the
+    device's current one)."""
     if stream is None:
-        if dev.index == torch.cuda.current_device():
-            return contextlib.nullcontext(), torch.cuda.current_stream()
-        stream = torch.cuda.current_stream(dev)
+        return contextlib.nullcontext()
     if stream.device != dev:
         raise ValueError(f"stream is on {stream.device} but the tensors are on {dev}")
-    return torch.cuda.stream(stream), stream
+    return torch.cuda.stream(stream)
 
 
 def _vector(t, name, numel, dtype, dev):
@@ -68,25 +80,35 @@ def _workspace(workspace, need, dev):
 
 
 class _DevicePlan(_Plan):
-    """A plan that makes its tensors' device current around the launch."""
+    """A plan that launches on `stream` or, without one, on the stream that is
+    current for its tensors' device at each call (so a graph capture on another
+    stream than the plan was made on records it), whichever device is current."""
+
+    def _launch(self, fn, name, *lead):
+        # (the raw handle: making a torch.cuda.Stream object takes 2 us of a call's 5)
+        s = self.stream.cuda_stream if self.stream is not None else torch._C._cuda_getCurrentRawStream(self.dev.index)
+        st = fn(*lead, *self.args, s)
+        if st != _b.SV_OK:
+            raise SpecVerifyError(st, name)
+        return self.out
 
     def __call__(self):
-        if self.dev.index == torch.cuda.current_device():
-            return super().__call__()
+        if self.dev.index == torch._C._cuda_getDevice():
+            return self._launch(self.fn, self.name)
         with torch.cuda.device(self.dev):
-            return super().__call__()
+            return self._launch(self.fn, self.name)
 
     def profiled(self, events):
         with torch.cuda.device(self.dev):
-            return super().profiled(events)
+            return self._launch(self.fn_profiled, self.name + "_profiled", events)
 
 
 class BeamSelectPlan(_DevicePlan):
     """spec_beam_select with every argument marshalled once.
 
     Holds references to the tensors it was built from; __call__ enqueues one
-    selection on `stream` (default: the current stream at construction) and
-    returns the outputs, the same tensors every time.  See beam_select.
+    selection on `stream` (default: the stream current at the call) and returns
+    the outputs, the same tensors every time.  See beam_select.
     """
 
     name = "spec_beam_select"
@@ -117,19 +139,17 @@ class BeamSelectPlan(_DevicePlan):
         need = C.c_size_t(0)
         _check(lib.spec_beam_select(*args, None, None, None, None, C.byref(need), None),
                "spec_beam_select(workspace query)")
-        ctx, s = _on(dev, stream)
-        with ctx:
+        with _on(dev, stream):
             self.workspace = _workspace(workspace, need.value, dev)
             if out is None:
                 out = {k: torch.empty((groups, num_select), dtype=d, device=dev)
                        for k, d in (("scores", torch.float32), ("tokens", torch.int32), ("parents", torch.int32))}
         outs = [_vector(out[k], f"out[{k!r}]", groups * num_select, d, dev)
                 for k, d in (("scores", torch.float32), ("tokens", torch.int32), ("parents", torch.int32))]
-        self.out, self.dev, self.shape = out, dev, shape
+        self.out, self.dev, self.shape, self.stream = out, dev, shape, stream
         self.have = C.c_size_t(self.workspace.numel())
-        self._keep = (logits, scores, finished, s)
-        self.args = (*args, *outs, C.c_void_p(self.workspace.data_ptr()), C.byref(self.have),
-                     C.c_void_p(s.cuda_stream))
+        self._keep = (logits, scores, finished)
+        self.args = (*args, *outs, C.c_void_p(self.workspace.data_ptr()), C.byref(self.have))
         self.fn, self.fn_profiled = lib.spec_beam_select, lib.spec_beam_select_profiled
 
 
@@ -182,13 +202,12 @@ class StateReorderPlan(_DevicePlan):
         es = states.element_size()
         shape = StateShapeT(slabs, batch // beams, beams, heads, positions, row * es,
                             *(v.stride(i) * es for i in range(4)))
-        ctx, s = _on(dev, stream)
-        self.out, self.dev, self.shape = states, dev, shape
-        self._keep = (parents, lengths, s)
+        _on(dev, stream)
+        self.out, self.dev, self.shape, self.stream = states, dev, shape, stream
+        self._keep = (parents, lengths)
         self.args = (C.byref(shape), C.c_void_p(states.data_ptr()),
                      _vector(parents, "parents", batch, torch.int32, dev),
-                     None if lengths is None else _vector(lengths, "lengths", batch, torch.int32, dev),
-                     C.c_void_p(s.cuda_stream))
+                     None if lengths is None else _vector(lengths, "lengths", batch, torch.int32, dev))
         self.fn, self.fn_profiled = lib.spec_state_reorder, lib.spec_state_reorder_profiled
 
 
@@ -205,3 +224,128 @@ def reorder_states(states: torch.Tensor, parents: torch.Tensor, beams: int, leng
     Returns `states`.
     """
     return StateReorderPlan(states, parents, beams, lengths, stream)()
+
+
+def _rows3(t, name):
+    """Row and head stride of [rows, heads, dim] (a dimension of one place may report any stride)."""
+    if t.shape[2] > 1 and t.stride(2) != 1:
+        raise ValueError(f"{name} must have unit stride in its last dimension")
+    dim = t.shape[2]
+    return (t.stride(0) if t.shape[0] > 1 else 0), (t.stride(1) if t.shape[1] > 1 else dim)
+
+
+def _cache(t, name, count, kv_heads, dim, dtype, dev):
+    if t.dim() != 4:
+        raise ValueError(f"{name} must be [{'groups' if name.startswith('prefix') else 'batch'}, positions, kv_heads, "
+                         "head_dim]")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} is {t.dtype} but q is {dtype}")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device} but q is on {dev}")
+    if t.shape[0] != count or t.shape[2] != kv_heads or t.shape[3] != dim:
+        raise ValueError(f"{name} is {tuple(t.shape)}; [{count}, positions, {kv_heads}, {dim}] is needed")
+    if t.numel() > 0 and t.stride(3) != 1:
+        raise ValueError(f"{name} must have unit stride in its last dimension")
+    st = [t.stride(i) if t.shape[i] > 1 else 0 for i in range(3)]
+    return CacheT(t.data_ptr() or None, *st)
+
+
+class PrefixAttentionPlan(_DevicePlan):
+    """spec_prefix_attention with every argument marshalled once: __call__
+    enqueues one call and returns {"out"} and, with return_lse, {"lse"}, the
+    same tensors every time.  See prefix_attention."""
+
+    name = "spec_prefix_attention"
+
+    def __init__(self, q, prefix_k, prefix_v, suffix_k, suffix_v, prefix_lengths=None, suffix_lengths=None,
+                 cu_draft=None, max_draft=None, cu_groups=None, max_group=None, scale=None, return_lse=False, out=None,
+                 workspace=None, stream=None):
+        lib = load_library()
+        if q.dim() != 3:
+            raise ValueError("q must be [rows, q_heads, head_dim]")
+        for name, t in (("prefix_k", prefix_k), ("prefix_v", prefix_v), ("suffix_k", suffix_k),
+                        ("suffix_v", suffix_v)):
+            if t.dim() != 4:
+                raise ValueError(f"{name} must be a 4-D tensor [groups or batch, positions, kv_heads, head_dim]")
+        rows, q_heads, dim = q.shape
+        groups, max_prefix, kv_heads, _ = prefix_k.shape
+        batch, max_suffix = suffix_k.shape[:2]
+        if batch < 1 or groups < 1 or kv_heads < 1 or q_heads % kv_heads != 0:
+            raise ValueError(f"{batch} sequences, {groups} groups, {q_heads} query heads and {kv_heads} key/value heads "
+                             "do not fit together")
+        if prefix_v.shape[1] != max_prefix or suffix_v.shape[1] != max_suffix:
+            raise ValueError("keys and values must hold the same number of positions")
+        total = rows - batch
+        if total < 0:
+            raise ValueError(f"q has {rows} rows; {batch} sequences need one each at least")
+        code = _dtype_code(q)
+        dev, dtype = q.device, q.dtype
+        if dev.type != "cuda":
+            raise ValueError("q must be on a GPU")
+        caches = [_cache(t, n, c, kv_heads, dim, dtype, dev) for n, t, c in (
+            ("prefix_k", prefix_k, groups), ("prefix_v", prefix_v, groups), ("suffix_k", suffix_k, batch),
+            ("suffix_v", suffix_v, batch))]
+        if cu_draft is None:
+            if total % batch != 0:
+                raise ValueError("q must have batch * (K + 1) rows; pass cu_draft for ragged K")
+            if max_draft is not None and max_draft != total // batch:
+                raise ValueError("max_draft does not match the uniform draft length")
+            max_draft = total // batch
+        if cu_groups is None and batch % groups != 0:
+            raise ValueError(f"{batch} sequences do not divide into {groups} groups; pass cu_groups")
+        vectors = [None if t is None else _vector(t, n, c, torch.int32, dev) for n, t, c in (
+            ("cu_draft", cu_draft, batch + 1), ("cu_groups", cu_groups, groups + 1),
+            ("prefix_lengths", prefix_lengths, groups), ("suffix_lengths", suffix_lengths, batch))]
+        if max_draft is None:
+            max_draft = int((cu_draft[1:] - cu_draft[:-1]).max().item())
+        if cu_groups is not None and max_group is None:
+            max_group = int((cu_groups[1:] - cu_groups[:-1]).max().item())
+        lse = None
+        with _on(dev, stream):
+            if out is None:
+                out = {"out": torch.empty((rows, q_heads, dim), dtype=dtype, device=dev)}
+                if return_lse:
+                    out["lse"] = torch.empty((rows, q_heads), dtype=torch.float32, device=dev)
+        o = out["out"]
+        if tuple(o.shape) != (rows, q_heads, dim) or o.dtype != dtype or o.device != dev:
+            raise ValueError(f"out['out'] must be {dtype} [{rows}, {q_heads}, {dim}] on {dev}")
+        if out.get("lse") is not None:
+            lse = _vector(out["lse"], "out['lse']", rows * q_heads, torch.float32, dev)
+        shape = AttentionShapeT(groups, batch, int(max_group or 0), int(max_draft), total, q_heads, kv_heads, dim,
+                                max_prefix, max_suffix, code, *_rows3(q, "q"), *_rows3(o, "out['out']"), *vectors)
+        scale = dim ** -0.5 if scale is None else float(scale)
+        args = (C.byref(shape), C.c_void_p(q.data_ptr()), *[C.byref(c) for c in caches], C.c_float(scale),
+                C.c_void_p(o.data_ptr()), lse)
+        need = C.c_size_t(0)
+        _check(lib.spec_prefix_attention(*args, None, C.byref(need), None), "spec_prefix_attention(workspace query)")
+        with _on(dev, stream):
+            self.workspace = _workspace(workspace, need.value, dev)
+        self.out, self.dev, self.shape, self.stream = out, dev, shape, stream
+        self.have = C.c_size_t(self.workspace.numel())
+        self._keep = (q, prefix_k, prefix_v, suffix_k, suffix_v, prefix_lengths, suffix_lengths, cu_draft, cu_groups,
+                      caches)
+        self.args = (*args, C.c_void_p(self.workspace.data_ptr()), C.byref(self.have))
+        self.fn, self.fn_profiled = lib.spec_prefix_attention, lib.spec_prefix_attention_profiled
+
+
+def prefix_attention(q: torch.Tensor, prefix_k: torch.Tensor, prefix_v: torch.Tensor, suffix_k: torch.Tensor,
+                     suffix_v: torch.Tensor, prefix_lengths: Optional[torch.Tensor] = None,
+                     suffix_lengths: Optional[torch.Tensor] = None, cu_draft: Optional[torch.Tensor] = None,
+                     max_draft: Optional[int] = None, cu_groups: Optional[torch.Tensor] = None,
+                     max_group: Optional[int] = None, scale: Optional[float] = None, return_lse: bool = False,
+                     out: Optional[dict] = None, workspace: Optional[torch.Tensor] = None, stream=None) -> dict:
+    """Attention over group-shared prefixes and own suffixes on the GPU
+    (spec_prefix_attention).
+
+    q [sum(K_b + 1), q_heads, D], bfloat16 or float16, rows packed as the target
+    rows of a verify (one row per sequence at a plain decode step); prefix_k and
+    prefix_v [groups, positions, kv_heads, D]; suffix_k and suffix_v [batch,
+    positions, kv_heads, D], the newest rows' keys and values written; lengths
+    int32, the positions in use (None: all).  cu_draft int32 [batch + 1] or None
+    (uniform K); cu_groups int32 [groups + 1], the groups' first sequences, or
+    None (equal groups).  max_draft and max_group are read back from the device
+    where they are needed and not given.  scale defaults to D ** -0.5.
+    Returns out [rows, q_heads, D] and, with return_lse, lse [rows, q_heads].
+    """
+    return PrefixAttentionPlan(q, prefix_k, prefix_v, suffix_k, suffix_v, prefix_lengths, suffix_lengths, cu_draft,
+                               max_draft, cu_groups, max_group, scale, return_lse, out, workspace, stream)()

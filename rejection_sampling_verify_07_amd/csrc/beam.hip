@@ -11,6 +11,7 @@
 #include "sv_host.hpp"
 #include "sv_beam.hpp"
 #include "sv_reorder.hpp"
+#include "sv_attention.hpp"
 
 static_assert(SV_MAX_BEAMS == sv::kBeamMaxBeams, "beam limit mismatch");
 static_assert(SV_MAX_SELECT == sv::kBeamMaxSelect, "selection limit mismatch");
@@ -209,6 +210,203 @@ sv_status_t state_reorder_common(const sv_state_shape_t* sh, void* states, const
     return launch_status();
 }
 
+// ---- shared-prefix attention
+
+constexpr int32_t kMaxPosStride = 1 << 26;   // bytes: 32 positions stay within a 32-bit offset
+constexpr int32_t kMaxPositions = 1 << 30;
+constexpr int64_t kAttnGroups = 1024;        // workgroups that the splits aim at
+constexpr int32_t kAttnMinKeys = 256;        // keys per workgroup that a split keeps
+
+struct AttnPlan {
+    int32_t rows, rep, mtp, ptiles, stiles, psplits, ssplits;
+    int64_t punits, pblocks, grid;
+    size_t off_acc, off_ml, bytes;
+};
+
+int32_t attn_splits(int64_t workgroups, int32_t positions)
+{
+    if (positions == 0) return 0;
+    int64_t n = kAttnGroups / workgroups;
+    const int64_t most = (positions + kAttnMinKeys - 1) / kAttnMinKeys;
+    if (n > most) n = most;
+    return n < 1 ? 1 : (int32_t)n;
+}
+
+AttnPlan attn_plan(const sv_attention_shape_t* sh)
+{
+    AttnPlan p{};
+    p.rows = sh->total_draft + sh->batch;
+    p.rep = sh->q_heads / sh->kv_heads;
+    const int64_t per_group = sh->cu_groups != nullptr ? sh->max_group : sh->batch / sh->groups;
+    const int64_t prows = per_group * (sh->max_draft + 1) * p.rep;
+    p.mtp = prows <= 16 ? 1 : prows <= 32 || sh->head_dim == 256 ? 2 : 4;
+    p.ptiles = (int32_t)((prows + p.mtp * 16 - 1) / (p.mtp * 16));
+    p.stiles = (int32_t)(((int64_t)(sh->max_draft + 1) * p.rep + 15) / 16);
+    p.psplits = attn_splits((int64_t)sh->groups * sh->kv_heads * p.ptiles, sh->max_prefix);
+    p.ssplits = attn_splits((int64_t)sh->batch * sh->kv_heads * p.stiles, sh->max_suffix);
+    p.punits = (int64_t)sh->groups * sh->kv_heads * p.psplits;
+    p.pblocks = (p.punits + 7) / 8 * 8 * p.ptiles;
+    p.grid = p.pblocks + (int64_t)sh->batch * sh->kv_heads * p.stiles * p.ssplits;
+    const size_t n = (size_t)p.rows * (size_t)sh->q_heads * (size_t)(p.psplits + p.ssplits);
+    p.off_acc = 0;
+    p.off_ml = align_up(n * (size_t)sh->head_dim * sizeof(float));
+    p.bytes = align_up(p.off_ml + n * sizeof(float2));
+    if (p.bytes == 0) p.bytes = kAlign;
+    return p;
+}
+
+sv_status_t check_attention(const sv_attention_shape_t* sh, float scale)
+{
+    if (sh == nullptr) return SV_ERR_INVALID_ARGUMENT;
+    const int32_t dt = dtype_of(sh);
+    if (dt != SV_DTYPE_F32 && dt != SV_DTYPE_BF16 && dt != SV_DTYPE_F16) return SV_ERR_INVALID_ARGUMENT;
+    if (sh->groups < 1 || sh->batch < 1 || sh->max_draft < 0 || sh->total_draft < 0 || sh->q_heads < 1 ||
+        sh->kv_heads < 1 || sh->head_dim < 1 || sh->max_prefix < 0 || sh->max_suffix < 0)
+        return SV_ERR_INVALID_ARGUMENT;
+    if (sh->q_heads % sh->kv_heads != 0) return SV_ERR_INVALID_ARGUMENT;
+    if (sh->cu_groups == nullptr && sh->batch % sh->groups != 0) return SV_ERR_INVALID_ARGUMENT;
+    if (sh->cu_groups != nullptr && (sh->max_group < 1 || sh->max_group > sh->batch)) return SV_ERR_INVALID_ARGUMENT;
+    const int64_t all = (int64_t)sh->batch * sh->max_draft;
+    if (sh->total_draft > all || (sh->cu_draft == nullptr && sh->total_draft != all)) return SV_ERR_INVALID_ARGUMENT;
+    if (!aligned(sh->cu_draft, 4) || !aligned(sh->cu_groups, 4) || !aligned(sh->prefix_lengths, 4) ||
+        !aligned(sh->suffix_lengths, 4))
+        return SV_ERR_INVALID_ARGUMENT;
+    if (!(scale > 0.0f) || !isfinite(scale) || !isfinite((float)((double)scale * 1.4426950408889634)))
+        return SV_ERR_INVALID_ARGUMENT;
+    if (dt == SV_DTYPE_F32) return SV_ERR_UNSUPPORTED;
+    if (sh->head_dim != 64 && sh->head_dim != 128 && sh->head_dim != 256) return SV_ERR_UNSUPPORTED;
+    if (sh->max_draft > SV_MAX_DRAFT || sh->max_prefix > kMaxPositions || sh->max_suffix > kMaxPositions)
+        return SV_ERR_UNSUPPORTED;
+    if (((int64_t)sh->total_draft + sh->batch) * sh->q_heads > INT32_MAX / 2) return SV_ERR_UNSUPPORTED;
+    const AttnPlan p = attn_plan(sh);
+    if (p.grid > INT32_MAX || p.punits > INT32_MAX / 16) return SV_ERR_UNSUPPORTED;
+    return SV_OK;
+}
+
+// A cache's pointer and strides (elements of 2 bytes): 16-byte places.
+bool cache_ok(const sv_cache_t* c)
+{
+    if (c == nullptr || c->data == nullptr || !aligned(c->data, 16)) return false;
+    return c->batch_stride >= 0 && c->head_stride >= 0 && c->position_stride >= 0 && c->batch_stride % 8 == 0 &&
+           c->head_stride % 8 == 0 && c->position_stride % 8 == 0;
+}
+
+template <int DT, int D>
+sv_status_t run_attention(const AttnPlan& p, const sv::AttnArgs& a, hipStream_t stream,
+                          const sv_profile_events_t* prof)
+{
+    const uint32_t grid = (uint32_t)p.grid;
+    if (grid > 0) {
+        if (p.mtp == 1) launch_stream_nt(prof, sv::attn_part_kernel<DT, D, 1, 1>, grid, sv::kAttnThreads, stream, a);
+        else if (D == 256 || p.mtp == 2)
+            launch_stream_nt(prof, sv::attn_part_kernel<DT, D, 2, 1>, grid, sv::kAttnThreads, stream, a);
+        else
+            launch_stream_nt(prof, sv::attn_part_kernel<DT, D, D == 256 ? 2 : 4, 1>, grid, sv::kAttnThreads, stream, a);
+        if (launch_status() != SV_OK) return SV_ERR_HIP;
+    }
+    const int64_t per = sv::kThreads / (D / 4);
+    const int64_t n = (int64_t)a.rows * a.q_heads;
+    hipLaunchKernelGGL((sv::attn_join_kernel<DT, D>), dim3((uint32_t)((n + per - 1) / per)), dim3(sv::kThreads), 0,
+                       stream, a);
+    return launch_status();
+}
+
+sv_status_t prefix_attention_common(const sv_attention_shape_t* sh, const void* q, const sv_cache_t* prefix_k,
+                                    const sv_cache_t* prefix_v, const sv_cache_t* suffix_k, const sv_cache_t* suffix_v,
+                                    float scale, void* out, float* out_lse, void* workspace, size_t* workspace_bytes,
+                                    hipStream_t stream, const sv_profile_events_t* prof)
+{
+    if (workspace_bytes == nullptr) return SV_ERR_INVALID_ARGUMENT;
+    const sv_status_t st = check_attention(sh, scale);
+    if (st != SV_OK) return st;
+    const AttnPlan p = attn_plan(sh);
+    if (workspace == nullptr) {
+        *workspace_bytes = p.bytes;
+        return SV_OK;
+    }
+    if (q == nullptr || out == nullptr || !aligned(q, 16) || !aligned(out, 8) || !aligned(out_lse, 4) ||
+        !aligned(workspace, kAlign))
+        return SV_ERR_INVALID_ARGUMENT;
+    if (sh->q_row_stride < 0 || sh->q_head_stride < 0 || sh->q_row_stride % 8 != 0 || sh->q_head_stride % 8 != 0 ||
+        sh->out_row_stride < 0 || sh->out_head_stride < 0 || sh->out_row_stride % 4 != 0 ||
+        sh->out_head_stride % 4 != 0)
+        return SV_ERR_INVALID_ARGUMENT;
+    const sv_cache_t none{};
+    const sv_cache_t *pk = &none, *pv = &none, *sk = &none, *svc = &none;
+    if (sh->max_prefix > 0) {
+        if (!cache_ok(prefix_k) || !cache_ok(prefix_v)) return SV_ERR_INVALID_ARGUMENT;
+        pk = prefix_k;
+        pv = prefix_v;
+    }
+    if (sh->max_suffix > 0) {
+        if (!cache_ok(suffix_k) || !cache_ok(suffix_v)) return SV_ERR_INVALID_ARGUMENT;
+        sk = suffix_k;
+        svc = suffix_v;
+    }
+    for (const sv_cache_t* c : {pk, pv, sk, svc})
+        if (c->position_stride * 2 > kMaxPosStride) return SV_ERR_UNSUPPORTED;
+    if (*workspace_bytes < p.bytes) return SV_ERR_WORKSPACE_TOO_SMALL;
+    sv::AttnArgs a{};
+    a.q = static_cast<const char*>(q);
+    a.pk = static_cast<const char*>(pk->data);
+    a.pv = static_cast<const char*>(pv->data);
+    a.sk = static_cast<const char*>(sk->data);
+    a.sv = static_cast<const char*>(svc->data);
+    a.out = static_cast<char*>(out);
+    a.lse = out_lse;
+    a.q_row = sh->q_row_stride * 2;
+    a.q_head = sh->q_head_stride * 2;
+    a.out_row = sh->out_row_stride * 2;
+    a.out_head = sh->out_head_stride * 2;
+    a.pk_group = pk->batch_stride * 2;
+    a.pk_head = pk->head_stride * 2;
+    a.pk_pos = (int32_t)(pk->position_stride * 2);
+    a.pv_group = pv->batch_stride * 2;
+    a.pv_head = pv->head_stride * 2;
+    a.pv_pos = (int32_t)(pv->position_stride * 2);
+    a.sk_seq = sk->batch_stride * 2;
+    a.sk_head = sk->head_stride * 2;
+    a.sk_pos = (int32_t)(sk->position_stride * 2);
+    a.sv_seq = svc->batch_stride * 2;
+    a.sv_head = svc->head_stride * 2;
+    a.sv_pos = (int32_t)(svc->position_stride * 2);
+    a.cu_draft = sh->cu_draft;
+    a.cu_groups = sh->cu_groups;
+    a.prefix_len = sh->prefix_lengths;
+    a.suffix_len = sh->suffix_lengths;
+    a.groups = sh->groups;
+    a.batch = sh->batch;
+    a.rows = p.rows;
+    a.max_draft = sh->max_draft;
+    a.per_group = sh->batch / sh->groups;
+    a.max_prefix = sh->max_prefix;
+    a.max_suffix = sh->max_suffix;
+    a.q_heads = sh->q_heads;
+    a.kv_heads = sh->kv_heads;
+    a.rep = p.rep;
+    a.c = (float)((double)scale * 1.4426950408889634);
+    a.psplits = p.psplits;
+    a.ssplits = p.ssplits;
+    a.ptiles = p.ptiles;
+    a.stiles = p.stiles;
+    a.punits = (uint32_t)p.punits;
+    a.pblocks = (uint32_t)p.pblocks;
+    a.acc = ws_at<float>(workspace, p.off_acc);
+    a.ml = ws_at<float2>(workspace, p.off_ml);
+    return by_dtype(sh->dtype, [&](auto dtc) -> sv_status_t {
+        constexpr int DT = decltype(dtc)::value;
+        if constexpr (DT == sv::DT_F32) {
+            return SV_ERR_UNSUPPORTED;
+        } else {
+            switch (sh->head_dim) {
+                case 64: return run_attention<DT, 64>(p, a, stream, prof);
+                case 128: return run_attention<DT, 128>(p, a, stream, prof);
+                default: return run_attention<DT, 256>(p, a, stream, prof);
+            }
+        }
+    });
+}
+
 }  // namespace
 
 extern "C" {
@@ -242,6 +440,25 @@ sv_status_t spec_state_reorder_profiled(const sv_profile_events_t* events, const
                                         const int32_t* parents, const int32_t* lengths, hipStream_t stream)
 {
     return state_reorder_common(shape, states, parents, lengths, stream, events);
+}
+
+sv_status_t spec_prefix_attention(const sv_attention_shape_t* shape, const void* q, const sv_cache_t* prefix_k,
+                                  const sv_cache_t* prefix_v, const sv_cache_t* suffix_k, const sv_cache_t* suffix_v,
+                                  float scale, void* out, float* out_lse, void* workspace, size_t* workspace_bytes,
+                                  hipStream_t stream)
+{
+    return prefix_attention_common(shape, q, prefix_k, prefix_v, suffix_k, suffix_v, scale, out, out_lse, workspace,
+                                   workspace_bytes, stream, nullptr);
+}
+
+sv_status_t spec_prefix_attention_profiled(const sv_profile_events_t* events, const sv_attention_shape_t* shape,
+                                           const void* q, const sv_cache_t* prefix_k, const sv_cache_t* prefix_v,
+                                           const sv_cache_t* suffix_k, const sv_cache_t* suffix_v, float scale,
+                                           void* out, float* out_lse, void* workspace, size_t* workspace_bytes,
+                                           hipStream_t stream)
+{
+    return prefix_attention_common(shape, q, prefix_k, prefix_v, suffix_k, suffix_v, scale, out, out_lse, workspace,
+                                   workspace_bytes, stream, events);
 }
 
 }  // extern "C"

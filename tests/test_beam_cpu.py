@@ -134,3 +134,81 @@ def test_reorder_binding_refusals(B):
         B.reorder_states(torch.zeros(8), par, 4)
     with pytest.raises(ValueError, match="GPU"):
         B.reorder_states(torch.zeros(8, 3), par, 4)
+
+
+# ---- spec_prefix_attention
+def _attn_shape(B, **kw):
+    d = dict(groups=2, batch=6, max_group=3, max_draft=2, total_draft=12, q_heads=8, kv_heads=2, head_dim=128,
+             max_prefix=1000, max_suffix=50, dtype=1, q_row_stride=1024, q_head_stride=128, out_row_stride=1024,
+             out_head_stride=128)
+    d.update(kw)
+    return B.AttentionShapeT(**d)
+
+
+def _attend(B, lib, sh, scale=0.1, q=FAKE, caches=None, out=FAKE, lse=None, ws=None, have=0):
+    ok = B.CacheT(FAKE, 1024, 256, 128)
+    cs = [C.byref(ok)] * 4
+    for i, c in (caches or {}).items():
+        cs[i] = None if c is None else C.byref(c)
+    n = C.c_size_t(have)
+    st = lib.spec_prefix_attention(C.byref(sh) if sh is not None else None, q, *cs, scale, out, lse, ws, C.byref(n),
+                                   None)
+    return st, n.value
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(), 0), (dict(groups=0), 1), (dict(batch=0), 1), (dict(batch=7, total_draft=14), 1), (dict(q_heads=0), 1),
+    (dict(kv_heads=3), 1), (dict(kv_heads=0), 1), (dict(head_dim=0), 1), (dict(head_dim=80), 2), (dict(dtype=0), 2),
+    (dict(dtype=3), 1), (dict(max_draft=-1), 1), (dict(total_draft=11), 1), (dict(total_draft=13, cu_draft=FAKE), 1),
+    (dict(total_draft=11, cu_draft=FAKE), 0), (dict(cu_draft=FAKE + 2), 1), (dict(cu_groups=FAKE), 0),
+    (dict(cu_groups=FAKE, max_group=0), 1), (dict(cu_groups=FAKE, max_group=7), 1), (dict(cu_groups=FAKE + 1), 1),
+    (dict(prefix_lengths=FAKE + 2), 1), (dict(suffix_lengths=FAKE + 2), 1), (dict(max_prefix=-1), 1),
+    (dict(max_suffix=-1), 1), (dict(max_prefix=0), 0), (dict(max_suffix=0), 0), (dict(max_prefix=0, max_suffix=0), 0),
+    (dict(max_draft=129, total_draft=774), 2), (dict(max_prefix=(1 << 30) + 1), 2),
+    (dict(groups=1 << 20, batch=1 << 26, max_draft=0, total_draft=0, q_heads=64, kv_heads=64), 2)])
+def test_attention_shapes(B, lib, kw, code):
+    st, n = _attend(B, lib, _attn_shape(B, **kw))
+    assert st == code
+    if code == 0:
+        assert n > 0 and n % 256 == 0
+
+
+@pytest.mark.parametrize("scale,code", [(0.0, 1), (-0.1, 1), (float("nan"), 1), (float("inf"), 1), (3e38, 1),
+                                        (1e-30, 0)])
+def test_attention_scale(B, lib, scale, code):
+    assert _attend(B, lib, _attn_shape(B), scale)[0] == code
+
+
+def test_attention_pointers(B, lib):
+    sh = _attn_shape(B)
+    need = _attend(B, lib, sh)[1]
+    ok = dict(ws=FAKE, have=need)
+    cache = lambda **kw: B.CacheT(**{**dict(data=FAKE, batch_stride=1024, position_stride=256, head_stride=128), **kw})  # noqa: E731
+    for bad in (dict(q=None), dict(q=FAKE + 8), dict(out=None), dict(out=FAKE + 4), dict(lse=FAKE + 2),
+                dict(ws=FAKE + 128), *(dict(caches={i: None}) for i in range(4)),
+                *(dict(caches={i: cache(**kw)}) for i in range(4) for kw in (
+                    dict(data=None), dict(data=FAKE + 8), dict(batch_stride=1020), dict(position_stride=-256),
+                    dict(head_stride=4)))):
+        assert _attend(B, lib, sh, **{**ok, **bad})[0] == 1, bad
+    for kw in (dict(q_row_stride=1020), dict(q_head_stride=-8), dict(out_row_stride=1022), dict(out_head_stride=-128)):
+        assert _attend(B, lib, _attn_shape(B, **kw), **ok)[0] == 1, kw
+    assert _attend(B, lib, sh, **ok, caches={0: cache(position_stride=(1 << 25) + 8)})[0] == 2
+    assert _attend(B, lib, sh, ws=FAKE, have=need - 1)[0] == 3
+    assert _attend(B, lib, None)[0] == 1
+
+
+def test_attention_binding_refusals(B):
+    q, c = torch.zeros(4, 8, 64, dtype=torch.bfloat16), torch.zeros(2, 10, 2, 64, dtype=torch.bfloat16)
+    s = torch.zeros(4, 3, 2, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="GPU"):
+        B.prefix_attention(q, c, c, s, s)
+    with pytest.raises(ValueError, match=r"\[rows, q_heads, head_dim\]"):
+        B.prefix_attention(q[0], c, c, s, s)
+    with pytest.raises(ValueError, match="do not fit"):
+        B.prefix_attention(q[:, :7], c, c, s, s)
+    with pytest.raises(ValueError, match="one each"):
+        B.prefix_attention(q[:3], c, c, s, s)
+    with pytest.raises(ValueError, match="same number of positions"):
+        B.prefix_attention(q, c, c[:, :9], s, s)
+    with pytest.raises(ValueError, match="4-D"):
+        B.prefix_attention(q, c[0], c, s, s)

@@ -1,0 +1,209 @@
+"""spec_prefix_attention on the GPU against the plain 64-bit form, within the
+bounds that beam_util.attention_ref derives for each value."""
+import numpy as np
+import pytest
+import torch
+
+from beam_util import DTYPES, attention_ref, widen
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+
+
+@pytest.fixture(scope="module")
+def sv():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import rejection_sampling_verify_07_amd as sv
+
+    sv.load_library()
+    return sv
+
+
+class Case:
+    """Inputs of one call; positions behind the lengths hold NaN."""
+
+    def __init__(self, sizes, drafts, Hq, Hk, D, P, S, dtype, seed=0, plen=None, slen=None, q_scale=2.0, ragged=None,
+                 layout="phd"):
+        gen = torch.Generator().manual_seed(seed)
+        dt = DTYPES[dtype]
+        self.sizes, self.drafts, self.dtype = sizes, list(drafts), dt
+        G, B = len(sizes), sum(sizes)
+        assert len(self.drafts) == B
+        self.plen = np.asarray([P] * G if plen is None else plen, np.int32)
+        self.slen = np.asarray([S] * B if slen is None else slen, np.int32)
+        self.groups = np.repeat(np.arange(G), sizes)
+
+        def cache(n, pos, lens):
+            shape = (n, pos, Hk, D) if layout == "phd" else (n, Hk, pos, D)
+            x = torch.randn(shape, generator=gen).to(dt)
+            x = x if layout == "phd" else x.transpose(1, 2)
+            for i in range(n):
+                x[i, max(0, int(lens[i])):] = float("nan")
+            # (permuted layouts keep their strides on the device)
+            return x.to(DEV) if layout == "phd" else x.transpose(1, 2).contiguous().to(DEV).transpose(1, 2)
+
+        rows = sum(self.drafts) + B
+        self.q = (torch.randn(rows, Hq, D, generator=gen) * q_scale).to(dt).to(DEV)
+        self.pk, self.pv = cache(G, P, self.plen), cache(G, P, self.plen)
+        self.sk, self.sv = cache(B, S, self.slen), cache(B, S, self.slen)
+        uniform = len(set(self.drafts)) == 1
+        self.cu = None
+        if ragged or (ragged is None and not uniform):
+            self.cu = torch.tensor(np.concatenate([[0], np.cumsum(self.drafts)]), dtype=torch.int32, device=DEV)
+        self.cug = None
+        if len(set(sizes)) != 1:
+            self.cug = torch.tensor(np.concatenate([[0], np.cumsum(sizes)]), dtype=torch.int32, device=DEV)
+        self.scale = D ** -0.5
+
+    def run(self, sv, **kw):
+        kw.setdefault("return_lse", True)
+        return sv.prefix_attention(self.q, self.pk, self.pv, self.sk, self.sv, torch.from_numpy(self.plen).to(DEV),
+                                   torch.from_numpy(self.slen).to(DEV), cu_draft=self.cu, cu_groups=self.cug,
+                                   scale=self.scale, **kw)
+
+    def check(self, out):
+        eps = torch.finfo(self.dtype).eps
+        tiny = 2.0 ** -25 if self.dtype == torch.float16 else 0.0
+        ref = attention_ref(*(widen(x) for x in (self.q, self.pk, self.pv, self.sk, self.sv)), self.plen, self.slen,
+                            self.drafts, self.groups, float(np.float32(self.scale)), eps, tiny)
+        o, z = widen(out["out"]), widen(out["lse"])
+        assert np.isfinite(o).all()
+        bad = np.abs(o - ref[0]) > ref[2]
+        assert not bad.any(), (np.argwhere(bad)[:5], np.abs(o - ref[0])[bad][:5], ref[2][bad][:5])
+        none = np.isneginf(ref[1])
+        assert np.array_equal(none, np.isneginf(z))
+        assert np.all(o[none] == 0)
+        assert np.all(np.abs(z[~none] - ref[1][~none]) <= ref[3][~none])
+
+
+def run_case(sv, *args, **kw):
+    c = Case(*args, **kw)
+    print(f"attention sizes={c.sizes} drafts={c.drafts[:8]} q={tuple(c.q.shape)} prefix={tuple(c.pk.shape)} "
+          f"suffix={tuple(c.sk.shape)} {c.dtype}", flush=True)
+    out = c.run(sv)
+    torch.cuda.synchronize()
+    c.check(out)
+    return c, out
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("sizes,K,Hq,Hk,P,S", [
+    ([1], 0, 1, 1, 1, 1), ([2], 0, 4, 4, 33, 5), ([4], 0, 8, 2, 500, 20), ([3, 3], 2, 6, 2, 127, 33),
+    ([5], 3, 9, 3, 257, 130), ([2, 2, 2], 8, 4, 1, 64, 9), ([33], 1, 2, 1, 700, 3)])
+def test_attention_sizes(sv, dtype, D, sizes, K, Hq, Hk, P, S):
+    run_case(sv, sizes, [K] * sum(sizes), Hq, Hk, D, P, S, dtype, seed=P + D)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_attention_ragged_everything(sv, dtype):
+    sizes = [3, 1, 0, 6, 2]
+    drafts = [0, 4, 1, 2, 0, 0, 7, 3, 1, 5, 2, 6]
+    plen = [200, 1, 90, 0, 513]
+    slen = [1, 5, 40, 3, 77, 1, 8, 4, 65, 6, 3, 7]
+    run_case(sv, sizes, drafts, 6, 3, 64, 513, 80, dtype, plen=plen, slen=slen)
+
+
+def test_attention_lengths_out_of_range_and_rows_that_see_nothing(sv):
+    """Lengths below 0 and above the caches; suffixes shorter than their rows."""
+    c = Case([2, 2], [2, 2, 2, 2], 4, 2, 64, 40, 10, "bf16")
+    c.plen = np.array([-5, 99], np.int32)
+    c.slen = np.array([0, 2, -1, 50], np.int32)  # rows of the first group see 0, then at most 2 positions
+    c.check(c.run(sv))
+
+
+@pytest.mark.parametrize("P,S", [(0, 7), (300, 0), (0, 0)])
+def test_attention_without_prefix_or_suffix(sv, P, S):
+    run_case(sv, [3], [0, 0, 0], 4, 2, 128, P, S, "bf16")
+
+
+def test_attention_splits_and_long_suffix(sv):
+    run_case(sv, [1], [0], 2, 1, 64, 9001, 3001, "f16")
+    run_case(sv, [2], [1, 1], 2, 2, 128, 2050, 2049, "bf16", slen=[2049, 1025])
+
+
+def test_attention_head_major_caches_and_strided_rows(sv):
+    c, ref = run_case(sv, [2, 2], [1, 0, 2, 1], 4, 2, 128, 150, 30, "bf16", layout="hpd", plen=[150, 77],
+                      slen=[3, 30, 9, 2])
+    # q and out as slices of wider rows
+    rows = c.q.shape[0]
+    wide = torch.zeros(rows, 3, 4, 128, dtype=c.dtype, device=DEV)
+    wide[:, 1] = c.q
+    o = torch.full((rows, 6, 132), 7.0, dtype=c.dtype, device=DEV)
+    c.q = wide[:, 1]
+    got = c.run(sv, out={"out": o[:, 1:5, 4:], "lse": torch.empty(rows, 4, device=DEV)})
+    assert torch.equal(got["out"], ref["out"]) and torch.equal(got["lse"], ref["lse"])
+    o[:, 1:5, 4:] = 7.0
+    assert bool((o == 7.0).all())
+
+
+def test_attention_sharp_and_large_scores(sv):
+    """Scores of hundreds, rising along the keys, so that the reference moves often."""
+    c = Case([2], [0, 0], 2, 1, 64, 600, 10, "bf16", q_scale=1.0)
+    ramp = torch.linspace(0.1, 40.0, 600, device=DEV).view(1, 600, 1, 1)
+    c.pk = (torch.sign(c.q[0, 0]).float() * ramp).to(c.dtype).expand(1, 600, 1, 64).contiguous()
+    c.check(c.run(sv))
+    c.pk = c.pk.flip(1).contiguous()
+    c.check(c.run(sv))
+    c.pk = -c.pk
+    c.check(c.run(sv))
+
+
+def test_attention_matches_itself_across_group_shapes(sv):
+    """Sequences with copies of one prefix, each in a group of its own, against one group."""
+    c, ref = run_case(sv, [6], [1] * 6, 8, 2, 128, 400, 20, "bf16")
+    c.pk, c.pv = c.pk.expand(6, -1, -1, -1).contiguous(), c.pv.expand(6, -1, -1, -1).contiguous()
+    c.sizes, c.groups, c.plen = [1] * 6, np.arange(6), np.repeat(c.plen, 6)
+    c.check(c.run(sv))
+
+
+def test_attention_offsets_past_32_bits(sv):
+    """A prefix cache of 9 GB of which the last group's positions lie past 2^32 bytes."""
+    G, P, Hk, D = 2, 1200, 2, 64
+    big_k = torch.empty((G, P, 16384 * Hk, D), dtype=torch.bfloat16, device=DEV)[:, :, -Hk:]
+    c = Case([1, 1], [0, 0], 4, Hk, D, P, 4, "bf16")
+    big_k.copy_(c.pk)
+    c.pk = big_k
+    c.check(c.run(sv))
+
+
+def test_attention_repeats_bit_for_bit_with_any_workspace(sv):
+    c, ref = run_case(sv, [4, 4], [3] * 8, 8, 2, 128, 1000, 50, "bf16", plen=[1000, 300], slen=list(range(4, 52, 6)))
+    plan = sv.PrefixAttentionPlan(c.q, c.pk, c.pv, c.sk, c.sv)
+    ws = torch.empty(plan.workspace.numel(), dtype=torch.uint8, device=DEV)
+    store = torch.full((c.q.shape[0] + 2, 8, 128), 3.0, dtype=c.dtype, device=DEV)
+    lse = torch.full((c.q.shape[0] + 2, 8), 3.0, device=DEV)
+    for fill in (0, 255, 127):
+        ws.fill_(fill)
+        got = c.run(sv, workspace=ws, out={"out": store[1:-1], "lse": lse[1:-1]})
+        torch.cuda.synchronize()
+        assert torch.equal(got["out"], ref["out"]) and torch.equal(got["lse"], ref["lse"])
+        assert bool((store[[0, -1]] == 3.0).all()) and bool((lse[[0, -1]] == 3.0).all())
+
+
+def test_attention_on_another_stream_and_in_a_graph(sv):
+    c, ref = run_case(sv, [3], [2] * 3, 4, 2, 64, 200, 12, "f16")
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    got = c.run(sv, stream=s)
+    torch.cuda.current_stream().wait_stream(s)
+    torch.cuda.synchronize()
+    assert torch.equal(got["out"], ref["out"]) and torch.equal(got["lse"], ref["lse"])
+    plen = torch.tensor([200], dtype=torch.int32, device=DEV)
+    slen = torch.tensor([12, 12, 12], dtype=torch.int32, device=DEV)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = sv.prefix_attention(c.q, c.pk, c.pv, c.sk, c.sv, plen, slen, return_lse=True)
+    for p, n in ((200, 12), (31, 5), (1, 3), (200, 12)):
+        plen.fill_(p)
+        slen.fill_(n)
+        out["out"].fill_(0)
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        c.plen[:], c.slen[:] = p, n
+        want = c.run(sv)
+        torch.cuda.synchronize()
+        assert torch.equal(out["out"], want["out"]) and torch.equal(out["lse"], want["lse"])
+    c.check(want)

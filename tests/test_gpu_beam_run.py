@@ -1,0 +1,157 @@
+"""The beam-decoding calls together, as a decode loop uses them: attention over
+the shared prompt and the beams' own caches, selection over the vocabulary,
+reorder of caches, histories and lengths; a verify's scoring rows at the end."""
+import numpy as np
+import pytest
+import torch
+
+from beam_util import attention_ref, select_ref, widen
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+
+
+@pytest.fixture(scope="module")
+def sv():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import rejection_sampling_verify_07_amd as sv
+
+    sv.load_library()
+    return sv
+
+
+class Model:
+    """Two layers whose queries, keys and values are tables over (token,
+    position): a beam's caches must then equal the tables' rows of its history."""
+
+    def __init__(self, V=331, Hq=4, Hk=2, D=64, layers=2, positions=16, seed=3):
+        g = torch.Generator().manual_seed(seed)
+        self.V, self.Hq, self.Hk, self.D, self.layers = V, Hq, Hk, D, layers
+        mk = lambda *s: torch.randn(*s, generator=g).to(torch.bfloat16).to(DEV)  # noqa: E731
+        self.q, self.k, self.v = mk(layers, V, Hq, D), mk(layers, V, Hk, D), mk(layers, V, Hk, D)
+        self.pos = mk(positions, Hk, D)
+        self.head = torch.randn(Hq * D, V, generator=g).to(DEV) * 0.2
+
+    def kv(self, layer, tokens, at):
+        """Key and value rows of tokens at positions `at`."""
+        return self.k[layer][tokens] + self.pos[at], self.v[layer][tokens] - self.pos[at]
+
+
+@pytest.mark.parametrize("graph", [False, True])
+def test_beam_search_run(sv, graph):
+    m = Model()
+    G, W, P, S, steps, end = 3, 4, 70, 16, 7, 5
+    B = G * W
+    gen = torch.Generator().manual_seed(1)
+    prompts = torch.randint(0, m.V, (G, P), generator=gen).to(DEV)
+    plen = torch.tensor([70, 31, 1], dtype=torch.int32, device=DEV)
+    pk = torch.stack([m.k[i][prompts] for i in range(m.layers)])
+    pv = torch.stack([m.v[i][prompts] for i in range(m.layers)])
+    own = torch.zeros(2 * m.layers, B, S, m.Hk, m.D, dtype=torch.bfloat16, device=DEV)  # slab 2 i: keys, 2 i + 1: values
+    history = torch.full((B, S), -1, dtype=torch.int32, device=DEV)
+    lengths = torch.zeros(B, dtype=torch.int32, device=DEV)
+    tokens = prompts[torch.arange(G), plen.long() - 1].repeat_interleave(W)
+    scores = torch.full((G, W), -float("inf"), device=DEV)
+    scores[:, 0] = 0.0
+    scores, finished = scores.reshape(-1), torch.zeros(B, dtype=torch.uint8, device=DEV)
+    logits = torch.empty(B, m.V, device=DEV)
+    q = torch.empty(m.layers, B, m.Hq, m.D, dtype=torch.bfloat16, device=DEV)
+    picked = {"scores": torch.empty(G, W, device=DEV), "tokens": torch.empty(G, W, dtype=torch.int32, device=DEV),
+              "parents": torch.empty(G, W, dtype=torch.int32, device=DEV)}
+    attn = [sv.PrefixAttentionPlan(q[i], pk[i], pv[i], own[2 * i], own[2 * i + 1], plen, lengths)
+            for i in range(m.layers)]
+    select = sv.BeamSelectPlan(logits, scores, W, finished=finished, pad_token=end, out=picked)
+    flat = own.view(2 * m.layers, B, S, m.Hk * m.D)
+    moves = [sv.StateReorderPlan(flat, picked["parents"], W, lengths),
+             sv.StateReorderPlan(history, picked["parents"], W), sv.StateReorderPlan(finished[:, None], picked["parents"], W)]
+    rows = torch.arange(B, device=DEV)
+
+    def before():  # the newest token's keys and values, then the layers and the logits
+        at = lengths.long()
+        history[rows, at] = tokens.int()
+        for i in range(m.layers):
+            own[2 * i][rows, at], own[2 * i + 1][rows, at] = m.kv(i, tokens.long(), at)
+        lengths.add_(1)
+        hidden = 0
+        for i in range(m.layers):
+            q[i].copy_(m.q[i][tokens.long()])
+            hidden = hidden + attn[i]()["out"].float()
+        logits.copy_(hidden.view(B, -1) @ m.head)
+
+    def after():
+        select()
+        for p in moves:
+            p()
+        tokens.copy_(picked["tokens"].reshape(-1))
+        scores.copy_(picked["scores"].reshape(-1))
+        finished.copy_(finished | (tokens == end).to(torch.uint8))
+
+    captured = None
+    for step in range(steps):
+        before()
+        torch.cuda.synchronize()
+        for i in range(m.layers):
+            out = attn[i].out
+            ref = attention_ref(*(widen(x) for x in (q[i], pk[i], pv[i], own[2 * i], own[2 * i + 1])), plen.cpu().numpy(),
+                                lengths.cpu().numpy(), [0] * B, np.repeat(np.arange(G), W), float(np.float32(m.D ** -0.5)),
+                                2.0 ** -7, 0.0)
+            assert np.all(np.abs(widen(out["out"]) - ref[0]) <= ref[2])
+        want = select_ref(widen(logits), widen(scores), W, W, 1.0, finished.cpu().numpy(), end)
+        old = history.cpu()
+        if graph and captured is None and step == 2:
+            # (the capture runs nothing; the replay below does this step)
+            captured = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(captured):
+                after()
+        if captured is not None:
+            captured.replay()
+        else:
+            after()
+        torch.cuda.synchronize()
+        par = picked["parents"].cpu()
+        assert np.array_equal(par.numpy(), want[2]) and np.array_equal(picked["tokens"].cpu().numpy(), want[1])
+        src = (par + torch.arange(G)[:, None] * W).reshape(-1).long()
+        assert torch.equal(history.cpu(), old[src])
+        # every beam's caches are the tables' rows of its history
+        at = torch.arange(step + 1, device=DEV)
+        for i in range(m.layers):
+            k, v = m.kv(i, history[:, :step + 1].long(), at)
+            assert torch.equal(own[2 * i][:, :step + 1], k) and torch.equal(own[2 * i + 1][:, :step + 1], v)
+        assert not own[:, :, step + 1:].any()
+
+
+def test_scoring_rows_of_a_verify(sv):
+    """The target rows of a ragged verify from one attention call over a shared
+    prompt, against the rows of decode steps one at a time."""
+    m = Model(V=211, seed=8)
+    drafts = [3, 0, 5, 1]
+    B, P, S = len(drafts), 40, 16
+    gen = torch.Generator().manual_seed(2)
+    prompt = torch.randint(0, m.V, (1, P), generator=gen).to(DEV)
+    pk, pv = m.k[0][prompt], m.v[0][prompt]
+    guesses = [torch.randint(0, m.V, (k + 1,), generator=gen) for k in drafts]
+    sk = torch.zeros(B, S, m.Hk, m.D, dtype=torch.bfloat16, device=DEV)
+    vs = torch.zeros_like(sk)
+    for b, t in enumerate(guesses):
+        sk[b, :len(t)], vs[b, :len(t)] = m.kv(0, t.to(DEV), torch.arange(len(t), device=DEV))
+    slen = torch.tensor([k + 1 for k in drafts], dtype=torch.int32, device=DEV)
+    cu = torch.tensor(np.concatenate([[0], np.cumsum(drafts)]), dtype=torch.int32, device=DEV)
+    q = m.q[0][torch.cat(guesses).to(DEV)]
+    out = sv.prefix_attention(q, pk, pv, sk, vs, None, slen, cu_draft=cu)["out"]
+    target = out.float().view(q.shape[0], -1) @ m.head
+    drf = torch.randn(sum(drafts), m.V, generator=gen).to(DEV)
+    ids = torch.cat([t[1:] for t in guesses]).int().to(DEV)
+    got = sv.verify_sample(target, drf, ids, cu_draft=cu, max_draft=max(drafts), seed=4)
+    ref = attention_ref(*(widen(x) for x in (q, pk, pv, sk, vs)), [P], slen.cpu().numpy(), drafts, [0] * B,
+                        float(np.float32(m.D ** -0.5)), 2.0 ** -7, 0.0)
+    assert np.all(np.abs(widen(out) - ref[0]) <= ref[2])
+    row = 0
+    for b, t in enumerate(guesses):
+        for k in range(len(t)):
+            one = sv.prefix_attention(q[row:row + 1], pk, pv, sk[b:b + 1], vs[b:b + 1], None,
+                                      torch.tensor([k + 1], dtype=torch.int32, device=DEV))["out"]
+            assert np.all(np.abs(widen(one) - ref[0][row:row + 1]) <= ref[2][row:row + 1])
+            row += 1
+    n = got["num_accepted"].cpu()
+    assert bool(((n >= 0) & (n <= torch.tensor(drafts))).all())
