@@ -214,11 +214,21 @@ sv_status_t state_reorder_common(const sv_state_shape_t* sh, void* states, const
 
 constexpr int32_t kMaxPosStride = 1 << 26;   // bytes: 32 positions stay within a 32-bit offset
 constexpr int32_t kMaxPositions = 1 << 30;
-constexpr int64_t kAttnGroups = 1024;        // workgroups that the splits aim at
-constexpr int32_t kAttnMinKeys = 256;        // keys per workgroup that a split keeps
+#ifndef SV_AT_G
+#define SV_AT_G 512
+#endif
+#ifndef SV_AT_TROWS
+#define SV_AT_TROWS 32
+#endif
+#ifndef SV_AT_K
+#define SV_AT_K 512
+#endif
+constexpr int64_t kAttnGroups = SV_AT_G;        // workgroups that the splits aim at
+constexpr int32_t kAttnMinKeys = SV_AT_K;        // keys per workgroup that a split keeps
 
 struct AttnPlan {
-    int32_t rows, rep, mtp, ptiles, stiles, psplits, ssplits;
+    bool tiles;
+    int32_t rows, rep, mtp, mts, ptiles, stiles, psplits, ssplits;
     int64_t punits, pblocks, grid;
     size_t off_acc, off_ml, bytes;
 };
@@ -239,9 +249,14 @@ AttnPlan attn_plan(const sv_attention_shape_t* sh)
     p.rep = sh->q_heads / sh->kv_heads;
     const int64_t per_group = sh->cu_groups != nullptr ? sh->max_group : sh->batch / sh->groups;
     const int64_t prows = per_group * (sh->max_draft + 1) * p.rep;
-    p.mtp = prows <= 16 ? 1 : prows <= 32 || sh->head_dim == 256 ? 2 : 4;
-    p.ptiles = (int32_t)((prows + p.mtp * 16 - 1) / (p.mtp * 16));
-    p.stiles = (int32_t)(((int64_t)(sh->max_draft + 1) * p.rep + 15) / 16);
+    const int32_t most = sh->head_dim == 256 ? 1 : 2;  // 16-row tiles per wave that the registers hold
+    p.tiles = prows > most * 16;
+    p.mtp = prows <= 16 ? 1 : most;
+    const int32_t wg_rows = p.mtp * 16 * (p.tiles ? sv::kAttnWaves : 1);
+    p.ptiles = (int32_t)((prows + wg_rows - 1) / wg_rows);
+    const int64_t srows = (int64_t)(sh->max_draft + 1) * p.rep;
+    p.mts = srows <= 16 ? 1 : most;
+    p.stiles = (int32_t)((srows + p.mts * 16 - 1) / (p.mts * 16));
     p.psplits = attn_splits((int64_t)sh->groups * sh->kv_heads * p.ptiles, sh->max_prefix);
     p.ssplits = attn_splits((int64_t)sh->batch * sh->kv_heads * p.stiles, sh->max_suffix);
     p.punits = (int64_t)sh->groups * sh->kv_heads * p.psplits;
@@ -297,14 +312,18 @@ sv_status_t run_attention(const AttnPlan& p, const sv::AttnArgs& a, hipStream_t 
 {
     const uint32_t grid = (uint32_t)p.grid;
     if (grid > 0) {
-        if (p.mtp == 1) launch_stream_nt(prof, sv::attn_part_kernel<DT, D, 1, 1>, grid, sv::kAttnThreads, stream, a);
-        else if (D == 256 || p.mtp == 2)
-            launch_stream_nt(prof, sv::attn_part_kernel<DT, D, 2, 1>, grid, sv::kAttnThreads, stream, a);
-        else
-            launch_stream_nt(prof, sv::attn_part_kernel<DT, D, D == 256 ? 2 : 4, 1>, grid, sv::kAttnThreads, stream, a);
+        const auto launch = [&](auto kernel) {
+            launch_stream_nt(prof, kernel, grid, sv::kAttnThreads, stream, a);
+        };
+        constexpr int MT = D == 256 ? 1 : 2;
+        if (p.tiles && p.mts == 1) launch(sv::attn_part_kernel<DT, D, true, MT, 1>);
+        else if (p.tiles) launch(sv::attn_part_kernel<DT, D, true, MT, MT>);
+        else if (p.mtp == 1) launch(sv::attn_part_kernel<DT, D, false, 1, 1>);
+        else if (p.mts == 1) launch(sv::attn_part_kernel<DT, D, false, MT, 1>);
+        else launch(sv::attn_part_kernel<DT, D, false, MT, MT>);
         if (launch_status() != SV_OK) return SV_ERR_HIP;
     }
-    const int64_t per = sv::kThreads / (D / 4);
+    const int64_t per = sv::kWaves;  // one wave per (row, head)
     const int64_t n = (int64_t)a.rows * a.q_heads;
     hipLaunchKernelGGL((sv::attn_join_kernel<DT, D>), dim3((uint32_t)((n + per - 1) / per)), dim3(sv::kThreads), 0,
                        stream, a);

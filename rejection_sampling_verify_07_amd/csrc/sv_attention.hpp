@@ -26,6 +26,8 @@
 // the end; scores, statistics and accumulators are fp32.
 #pragma once
 
+#include <type_traits>
+
 #include "sv_common.hpp"
 
 namespace sv {
@@ -58,7 +60,7 @@ struct AttnArgs {
     int32_t psplits, ssplits, ptiles, stiles;
     uint32_t punits, pblocks;  // prefix units (group, head, split), and workgroups that serve them
     float* acc;                // [slot][row][head][D]
-    float2* ml;                // [slot][row][head]
+    float2* ml;                // [row][head][slot]
 };
 
 template <int DT>
@@ -144,24 +146,34 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const KeyRange& kr, in
         for (int d = 0; d < DPL; ++d) o[mt][d] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     }
 
-    // a lane's keys inside a block: K rows l16 and 16 + l16; V rows 4 lg + j and 16 + 4 lg + j
-    auto load_k = [&](int32_t kb, u32x4 (&kf)[2][DC]) {
+    // a lane's keys inside a block: K rows l16 and 16 + l16; V rows 4 lg + j and 16 + 4 lg + j.
+    // Offsets of a whole block are kept; a block that the range ends in takes the last key for those past it
+    // (finite, and masked below).
+    uint32_t koff[2], voff[8];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) koff[t] = (uint32_t)((t * 16 + l16) * kr.k_pos + lg * 16);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) voff[j] = (uint32_t)(((j < 4 ? 0 : 12) + lg * 4 + j) * kr.v_pos + l16 * (DPL * 2));
+    auto load_k = [&](int32_t kb, u32x4 (&kf)[2][DC], auto masked) {
         const char* base = kr.k + (int64_t)kb * kr.k_pos;
-        const int32_t last = kr.end - 1 - kb;  // (a key past the end: the last one, masked below)
+        const int32_t last = kr.end - 1 - kb;
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-            const uint32_t off = (uint32_t)(min(t * 16 + l16, last) * kr.k_pos + lg * 16);
+            uint32_t off = koff[t];
+            if constexpr (decltype(masked)::value) off = (uint32_t)(min(t * 16 + l16, last) * kr.k_pos + lg * 16);
 #pragma unroll
             for (int c = 0; c < DC; ++c) kf[t][c] = *(const SV_GLOBAL u32x4*)(base + off + c * 64);
         }
     };
-    auto load_v = [&](int32_t kb, uint32_t (&vr)[8][VW]) {
+    auto load_v = [&](int32_t kb, uint32_t (&vr)[8][VW], auto masked) {
         const char* base = kr.v + (int64_t)kb * kr.v_pos;
         const int32_t last = kr.end - 1 - kb;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const int32_t key = (j < 4 ? 0 : 12) + lg * 4 + j;
-            const char* p = base + (uint32_t)(min(key, last) * kr.v_pos + l16 * (DPL * 2));
+            uint32_t off = voff[j];
+            if constexpr (decltype(masked)::value)
+                off = (uint32_t)(min((j < 4 ? 0 : 12) + lg * 4 + j, last) * kr.v_pos + l16 * (DPL * 2));
+            const char* p = base + off;
             if constexpr (VW == 2) {
                 const u32x2 w = *(const SV_GLOBAL u32x2*)p;
                 vr[j][0] = w.x;
@@ -177,12 +189,16 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const KeyRange& kr, in
         }
     };
 
-    u32x4 kf[2][DC];
-    int32_t kb = kr.begin + wave * kKeyBlock;
-    if (kb < kr.end) load_k(kb, kf);
-    for (; kb < kr.end; kb += kKeyRound) {
+    u32x4 kf[2][DC];  // the block at hand; the next one's is loaded once the scores have taken it
+    auto next_k = [&](int32_t kb) {
+        if (kb >= kr.end) return;
+        if (kb + kKeyBlock <= kr.end) load_k(kb, kf, std::false_type{});
+        else load_k(kb, kf, std::true_type{});
+    };
+    auto step = [&](int32_t kb, auto masked) {
+        constexpr bool MASKED = decltype(masked)::value;
         uint32_t vr[8][VW];
-        load_v(kb, vr);
+        load_v(kb, vr, masked);
         f32x4 s[2][MT];
 #pragma unroll
         for (int t = 0; t < 2; ++t)
@@ -192,8 +208,8 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const KeyRange& kr, in
 #pragma unroll
                 for (int c = 0; c < DC; ++c) s[t][mt] = mfma_16x16x32<DT>(kf[t][c], qf[mt][c], s[t][mt]);
             }
-        if (kb + kKeyRound < kr.end) load_k(kb + kKeyRound, kf);
-        if (kb + kKeyBlock > whole) {
+        next_k(kb + kKeyRound);
+        if constexpr (MASKED) {
 #pragma unroll
             for (int t = 0; t < 2; ++t)
 #pragma unroll
@@ -248,7 +264,11 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const KeyRange& kr, in
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) o[mt][d] = mfma_16x16x32<DT>(vf, pf[mt], o[mt][d]);
         }
-    }
+    };
+    int32_t kb = kr.begin + wave * kKeyBlock;
+    next_k(kb);
+    for (; kb + kKeyBlock <= whole; kb += kKeyRound) step(kb, std::false_type{});
+    for (; kb < kr.end; kb += kKeyRound) step(kb, std::true_type{});
 
     // ---- join the four waves: a common reference, then o summed in a fixed order
 #pragma unroll
@@ -302,14 +322,230 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const KeyRange& kr, in
         const int32_t r = r0 + mt * 16 + l16;
         if (r >= m_total) continue;
         const int32_t t = r / a.rep, h = hk * a.rep + (r - t * a.rep);
-        const int64_t at = ((int64_t)slot * a.rows + row0 + t) * a.q_heads + h;
-        if (lg == 0) a.ml[at] = float2{m[mt], l[mt]};
+        const int64_t rh = (int64_t)(row0 + t) * a.q_heads + h;
+        const int64_t at = (int64_t)slot * a.rows * a.q_heads + rh;
+        if (lg == 0) a.ml[rh * (a.psplits + a.ssplits) + slot] = float2{m[mt], l[mt]};
         SV_GLOBAL f32x4* dst = (SV_GLOBAL f32x4*)(a.acc + at * D + lg * 4 * DPL);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int d = 0; d < DPL; d += 4)
                 dst[(i * DPL + d) / 4] = f32x4{o[mt][d][i], o[mt][d + 1][i], o[mt][d + 2][i], o[mt][d + 3][i]};
+    }
+}
+
+// ---- many rows per key/value head: keys and values through LDS
+//
+// Four waves of MT * 16 rows each share tiles of KT keys.  At these row counts
+// the products bound the kernel, and what feeds them: with each wave reading
+// its own keys (attend above) 64 rows per wave hold all registers and leave one
+// wave per SIMD; 32 rows and two workgroups per CU let one wave's exponentials
+// run beside another's products, and LDS serves a key row to four waves.
+//
+// A tile's 16-byte chunks are stored at chunk ^ (row mod 16) (mod 8 for D = 64): the score
+// product reads 16 rows at one column, which would otherwise all lie in the same banks.
+// V is read transposed (each 16 lanes exchange a 4 x 16 block), so that lane
+// l16 of tile d holds four keys of column d * 16 + l16.
+// The next tile travels in registers while the present one is used.
+template <int DT, int D, int MT>
+struct TileAttention {
+    static constexpr int DC = D / 32, DT16 = D / 16;
+    static constexpr int KT = D == 256 ? 32 : 64;         // keys per tile
+    static constexpr int ROW = D * 2;                     // bytes per key row
+    static constexpr int CH = ROW / 16;                   // 16-byte chunks per row
+    static constexpr int MASK = CH < 16 ? CH - 1 : 15;    // swizzle
+    static constexpr int TILE = KT * ROW;                 // bytes of K (or V) per tile
+    static constexpr int LOADS = TILE / 16 / kAttnThreads;
+    static constexpr int LDS = 4 * TILE;                  // K and V, two tiles each
+    static constexpr int ROWS = kAttnWaves * MT * 16;     // query rows per workgroup
+};
+
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+#define SV_LDS __attribute__((address_space(3)))
+
+__device__ __forceinline__ u32x2 lds_read_transposed(const char* p)
+{
+    return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((SV_LDS s16x4*)p));
+}
+
+template <int DT, int D, int MT>
+__device__ __forceinline__ void attend_tiles(const AttnArgs& a, const KeyRange& kr, int32_t row0, int32_t nrows,
+                                             int32_t hk, int32_t tile, int32_t slot, char* s_kv)
+{
+    typedef TileAttention<DT, D, MT> TA;
+    constexpr int DC = TA::DC, DT16 = TA::DT16, KT = TA::KT, SUBS = KT / kKeyBlock;
+    const int lane = lane_id(), wave = wave_id(), l16 = lane & 15, lg = lane >> 4;
+    const int32_t m_total = nrows * a.rep;
+    const int32_t r0 = tile * TA::ROWS + wave * (MT * 16);
+    const bool idle = r0 >= m_total;  // no rows: the wave only moves tiles
+
+    u32x4 qf[MT][DC];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+        const int32_t r = r0 + mt * 16 + l16;
+        const int32_t t = r / a.rep, h = hk * a.rep + (r - t * a.rep);
+        const char* qp = a.q + (int64_t)(row0 + t) * a.q_row + (int64_t)h * a.q_head + lg * 16;
+#pragma unroll
+        for (int c = 0; c < DC; ++c)
+            qf[mt][c] = r < m_total ? *(const SV_GLOBAL u32x4*)(qp + c * 64) : u32x4{0u, 0u, 0u, 0u};
+    }
+    f32x4 o[MT][DT16];
+    float m[MT], l[MT];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+        m[mt] = kNoReference;
+        l[mt] = 0.0f;
+#pragma unroll
+        for (int d = 0; d < DT16; ++d) o[mt][d] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+
+    // this thread's chunks of a tile: row and column, and the place in LDS
+    u32x4 kreg[TA::LOADS], vreg[TA::LOADS];
+    uint32_t koff[TA::LOADS], voff[TA::LOADS];
+#pragma unroll
+    for (int i = 0; i < TA::LOADS; ++i) {
+        const int32_t x = i * kAttnThreads + (int32_t)threadIdx.x;
+        koff[i] = (uint32_t)(x / TA::CH * kr.k_pos + x % TA::CH * 16);
+        voff[i] = (uint32_t)(x / TA::CH * kr.v_pos + x % TA::CH * 16);
+    }
+    auto fetch = [&](int32_t kb) {
+        const char* kbase = kr.k + (int64_t)kb * kr.k_pos;
+        const char* vbase = kr.v + (int64_t)kb * kr.v_pos;
+        const int32_t last = kr.end - 1 - kb;
+        if (last >= KT - 1) {
+#pragma unroll
+            for (int i = 0; i < TA::LOADS; ++i) {
+                kreg[i] = *(const SV_GLOBAL u32x4*)(kbase + koff[i]);
+                vreg[i] = *(const SV_GLOBAL u32x4*)(vbase + voff[i]);
+            }
+        } else {  // the range ends in this tile: the last key (finite) in place of those past it, masked below
+#pragma unroll
+            for (int i = 0; i < TA::LOADS; ++i) {
+                const int32_t x = i * kAttnThreads + (int32_t)threadIdx.x;
+                const int32_t row = min(x / TA::CH, last), ch = x % TA::CH;
+                kreg[i] = *(const SV_GLOBAL u32x4*)(kbase + (uint32_t)(row * kr.k_pos + ch * 16));
+                vreg[i] = *(const SV_GLOBAL u32x4*)(vbase + (uint32_t)(row * kr.v_pos + ch * 16));
+            }
+        }
+    };
+    auto keep = [&](int buf) {
+        char* dst = s_kv + buf * (2 * TA::TILE);
+#pragma unroll
+        for (int i = 0; i < TA::LOADS; ++i) {
+            const int32_t x = i * kAttnThreads + (int32_t)threadIdx.x;
+            const int32_t row = x / TA::CH, ch = x % TA::CH;
+            const int32_t at = row * TA::ROW + ((ch ^ (row & TA::MASK)) * 16);
+            *(u32x4*)(dst + at) = kreg[i];
+            *(u32x4*)(dst + TA::TILE + at) = vreg[i];
+        }
+    };
+
+    if (kr.begin < kr.end) {
+        fetch(kr.begin);
+        keep(0);
+    }
+    __syncthreads();
+    int buf = 0;
+    // one tile; MASKED: the range ends inside it
+    auto use = [&](int32_t kb, auto masked) {
+        constexpr bool MASKED = decltype(masked)::value;
+        const char* s_k = s_kv + buf * (2 * TA::TILE);
+        const char* s_v = s_k + TA::TILE;
+        f32x4 s[SUBS][2][MT];
+#pragma unroll
+        for (int u = 0; u < SUBS; ++u)
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) s[u][t][mt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+                const int32_t row = u * kKeyBlock + t * 16 + l16;
+#pragma unroll
+                for (int c = 0; c < DC; ++c) {
+                    const u32x4 kf = *(const u32x4*)(s_k + row * TA::ROW + (((c * 4 + lg) ^ (l16 & TA::MASK)) * 16));
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt) s[u][t][mt] = mfma_16x16x32<DT>(kf, qf[mt][c], s[u][t][mt]);
+                }
+                if constexpr (MASKED) {
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (kb + u * kKeyBlock + t * 16 + lg * 4 + i >= kr.end) s[u][t][mt][i] = neg_inf();
+                }
+            }
+        float top[MT];
+        bool over = false;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+            float x = s[0][0][mt][0];
+#pragma unroll
+            for (int i = 1; i < 8 * SUBS; ++i) x = fmaxf(x, s[i / 8][(i / 4) & 1][mt][i & 3]);
+            top[mt] = x * a.c;
+            over |= top[mt] > m[mt] + kReferenceSlack;
+        }
+        if (__any(over)) {
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+                float x = top[mt];
+                x = fmaxf(x, __shfl_xor(x, 16, kWave));
+                x = fmaxf(x, __shfl_xor(x, 32, kWave));
+                x = fmaxf(x, m[mt]);
+                const float f = __builtin_amdgcn_exp2f(m[mt] - x);
+                m[mt] = x;
+                l[mt] *= f;
+#pragma unroll
+                for (int d = 0; d < DT16; ++d) o[mt][d] *= f;
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < SUBS; ++u) {
+            u32x4 pf[MT];
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+                float p[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[u][i / 4][mt][i & 3], a.c, -m[mt]));
+                    l[mt] += p[i];
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) pf[mt][i] = pack2<DT>(p[2 * i], p[2 * i + 1]);
+            }
+            // four keys (lg * 4 + l16 / 4) and 8 bytes of columns per lane before the exchange
+            const int32_t vrow = u * kKeyBlock + lg * 4 + (l16 >> 2);
+#pragma unroll
+            for (int d = 0; d < DT16; ++d) {
+                const int32_t at =
+                    vrow * TA::ROW + (((d * 2 + ((l16 & 3) >> 1)) ^ (vrow & TA::MASK)) * 16) + (l16 & 1) * 8;
+                const u32x2 v0 = lds_read_transposed(s_v + at), v1 = lds_read_transposed(s_v + at + 16 * TA::ROW);
+                const u32x4 vf = {v0.x, v0.y, v1.x, v1.y};
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) o[mt][d] = mfma_16x16x32<DT>(vf, pf[mt], o[mt][d]);
+            }
+        }
+    };
+    int32_t kb = kr.begin;
+    for (; kb + KT < kr.end; kb += KT, buf ^= 1) {
+        fetch(kb + KT);
+        if (!idle) use(kb, std::false_type{});
+        keep(buf ^ 1);
+        __syncthreads();
+    }
+    if (kb < kr.end && !idle) use(kb, std::true_type{});
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+        l[mt] += __shfl_xor(l[mt], 16, kWave);
+        l[mt] += __shfl_xor(l[mt], 32, kWave);
+        const int32_t r = r0 + mt * 16 + l16;
+        if (r >= m_total) continue;
+        const int32_t t = r / a.rep, h = hk * a.rep + (r - t * a.rep);
+        const int64_t rh = (int64_t)(row0 + t) * a.q_heads + h;
+        const int64_t at = (int64_t)slot * a.rows * a.q_heads + rh;
+        if (lg == 0) a.ml[rh * (a.psplits + a.ssplits) + slot] = float2{m[mt], l[mt]};
+        // accumulator i of tile d holds column d * 16 + lg * 4 + i
+        SV_GLOBAL f32x4* dst = (SV_GLOBAL f32x4*)(a.acc + at * D + lg * 4);
+#pragma unroll
+        for (int d = 0; d < DT16; ++d) dst[d * 4] = o[mt][d];
     }
 }
 
@@ -328,10 +564,16 @@ __device__ __forceinline__ void share(int32_t total, int32_t i, int32_t n, int32
     *end = (int32_t)min((int64_t)total, (int64_t)*begin + chunk);
 }
 
-template <int DT, int D, int MTP, int MTS>
-__global__ __launch_bounds__(kAttnThreads) void attn_part_kernel(AttnArgs a)
+// MTP, MTS: 16-row tiles per wave for prefix and suffix work.  TILES: prefix
+// work goes through attend_tiles.
+// Two waves per SIMD where 256 registers hold a wave's rows.
+template <int DT, int D, bool TILES, int MTP, int MTS>
+__global__ __launch_bounds__(kAttnThreads, D == 256 ? 1 : 2) void attn_part_kernel(AttnArgs a)
 {
-    __shared__ __align__(16) float s_mem[attn_lds_floats(D, MTP > MTS ? MTP : MTS)];
+    constexpr size_t kLdsPrefix = TILES ? TileAttention<DT, D, MTP>::LDS : attn_lds_floats(D, MTP) * 4;
+    constexpr size_t kLdsSuffix = attn_lds_floats(D, MTS) * 4;
+    constexpr int kRowsPrefix = TILES ? TileAttention<DT, D, MTP>::ROWS : MTP * 16;
+    __shared__ __align__(16) char s_mem[kLdsPrefix > kLdsSuffix ? kLdsPrefix : kLdsSuffix];
     KeyRange kr;
     if (blockIdx.x < a.pblocks) {
         // the tiles of one unit (the same keys) run on one XCD (workgroups go to the 8 XCDs in turn)
@@ -348,7 +590,7 @@ __global__ __launch_bounds__(kAttnThreads) void attn_part_kernel(AttnArgs a)
             b1 = min(max(a.cu_groups[g + 1], 0), a.batch);
         }
         const int32_t row0 = first_row(a, b0), nrows = b1 > b0 ? first_row(a, b1) - row0 : 0;
-        if (tile * (MTP * 16) >= nrows * a.rep) return;
+        if (tile * kRowsPrefix >= nrows * a.rep) return;
         const int32_t total = a.prefix_len != nullptr ? min(max(a.prefix_len[g], 0), a.max_prefix) : a.max_prefix;
         share(total, split, a.psplits, &kr.begin, &kr.end);
         kr.total = total;
@@ -356,7 +598,8 @@ __global__ __launch_bounds__(kAttnThreads) void attn_part_kernel(AttnArgs a)
         kr.v = a.pv + (int64_t)g * a.pv_group + (int64_t)hk * a.pv_head;
         kr.k_pos = a.pk_pos;
         kr.v_pos = a.pv_pos;
-        attend<DT, D, MTP>(a, kr, row0, nrows, hk, tile, 0, split, s_mem);
+        if constexpr (TILES) attend_tiles<DT, D, MTP>(a, kr, row0, nrows, hk, tile, split, s_mem);
+        else attend<DT, D, MTP>(a, kr, row0, nrows, hk, tile, 0, split, (float*)s_mem);
     } else {
         uint32_t y = blockIdx.x - a.pblocks;
         const int32_t tile = (int32_t)(y % (uint32_t)a.stiles);
@@ -373,38 +616,62 @@ __global__ __launch_bounds__(kAttnThreads) void attn_part_kernel(AttnArgs a)
         kr.v = a.sv + (int64_t)b * a.sv_seq + (int64_t)hk * a.sv_head;
         kr.k_pos = a.sk_pos;
         kr.v_pos = a.sv_pos;
-        attend<DT, D, MTS>(a, kr, row0, nrows, hk, tile, nrows - 1, a.psplits + split, s_mem);
+        attend<DT, D, MTS>(a, kr, row0, nrows, hk, tile, nrows - 1, a.psplits + split, (float*)s_mem);
     }
 }
 
-// Join of the parts: one thread per 4 columns of a (row, head).
+// Join of the parts: one wave per (row, head).  Lanes first hold one part's
+// (m, l) each, then D / 4 lanes take the columns of a part and the lane groups
+// take parts in turn.  All loads of a round are independent: the join is bound
+// by their latency.
 template <int DT, int D>
 __global__ __launch_bounds__(kThreads) void attn_join_kernel(AttnArgs a)
 {
-    constexpr int TPR = D / 4;
+    constexpr int LPP = D / 4;         // lanes per part
+    constexpr int PPR = kWave / LPP;   // parts per round
     const int64_t n = (int64_t)a.rows * a.q_heads;
-    const int64_t i = (int64_t)blockIdx.x * (kThreads / TPR) + threadIdx.x / TPR;
+    const int64_t i = (int64_t)blockIdx.x * kWaves + wave_id();
     if (i >= n) return;
-    const int d = (threadIdx.x % TPR) * 4;
+    const int lane = lane_id(), col = (lane % LPP) * 4, sub = lane / LPP;
     const int slots = a.psplits + a.ssplits;
+    const float2* ml = a.ml + i * slots;
     float m = kNoReference;
-    for (int s = 0; s < slots; ++s) m = fmaxf(m, a.ml[s * n + i].x);
+    float2 own = {kNoReference, 0.0f};  // this lane's part of the current 64
+    for (int s0 = 0; s0 < slots; s0 += kWave) {
+        own = s0 + lane < slots ? ml[s0 + lane] : float2{kNoReference, 0.0f};
+        m = fmaxf(m, own.x);
+    }
+    m = wave_max_dpp(m);
     float l = 0.0f;
     f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int s = 0; s < slots; ++s) {
-        const float2 p = a.ml[s * n + i];
-        if (p.y == 0.0f) continue;  // a part without a visible key
-        const float f = __builtin_amdgcn_exp2f(p.x - m);
-        l += p.y * f;
-        o += *(const SV_GLOBAL f32x4*)(a.acc + (s * n + i) * D + d) * f;
+    for (int s0 = 0; s0 < slots; s0 += kWave) {
+        if (slots > kWave) own = s0 + lane < slots ? ml[s0 + lane] : float2{kNoReference, 0.0f};
+        // (a part without a visible key has l = 0 and no o)
+        const float w = own.y > 0.0f ? __builtin_amdgcn_exp2f(own.x - m) : 0.0f;
+        l += own.y * w;
+        const int count = min(slots - s0, kWave);
+#pragma unroll 4
+        for (int s = 0; s < count; s += PPR) {
+            const float f = __shfl(w, s + sub, kWave);
+            if (s + sub < count && f > 0.0f)
+                o += *(const SV_GLOBAL f32x4*)(a.acc + ((int64_t)(s0 + s + sub) * n + i) * D + col) * f;
+        }
     }
+#pragma unroll
+    for (int x = kWave / 2; x > 0; x >>= 1) l += __shfl_xor(l, x, kWave);
+#pragma unroll
+    for (int x = LPP; x < kWave; x <<= 1) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[e] += __shfl_xor(o[e], x, kWave);
+    }
+    if (sub != 0) return;
     const int32_t t = (int32_t)(i / a.q_heads), h = (int32_t)(i - (int64_t)t * a.q_heads);
     const float inv = l > 0.0f ? 1.0f / l : 0.0f;
     u32x2 w;
     w.x = pack2<DT>(o.x * inv, o.y * inv);
     w.y = pack2<DT>(o.z * inv, o.w * inv);
-    *(SV_GLOBAL u32x2*)(a.out + (int64_t)t * a.out_row + (int64_t)h * a.out_head + d * 2) = w;
-    if (a.lse != nullptr && d == 0)
+    *(SV_GLOBAL u32x2*)(a.out + (int64_t)t * a.out_row + (int64_t)h * a.out_head + col * 2) = w;
+    if (a.lse != nullptr && lane == 0)
         a.lse[i] = l > 0.0f ? (m + __builtin_amdgcn_logf(l)) * 0.69314718055994531f : neg_inf();
 }
 
