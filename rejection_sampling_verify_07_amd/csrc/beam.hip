@@ -30,7 +30,9 @@ int32_t dtype_of(const Shape* sh)
 
 // ---- beam selection
 
-constexpr int kBeamLoads = 4;  // 16-byte loads per thread of the streaming pass
+// 16-byte loads per thread of the streaming pass: 29.8 us on 512 rows of 151936 bf16 logits, against 33.7 us with 2,
+// 31.4 with 6 and 31.0 with 8; 1 to 8 within 1 us of one another on 4 to 128 rows of 50304.
+constexpr int kBeamLoads = 4;
 
 struct BeamPlan {
     int32_t rows, nchunk, nblk, nblkp;

@@ -4,8 +4,8 @@
 // ties to the lowest w * V + v.
 //
 // Two kernels.  beam_stream_kernel reads every logit once (HBM bound) and
-// leaves, per 256-byte block of a row, the block's largest logit (1/64 of the
-// bytes read for 16-bit logits, 1/64 for fp32), and per wave's tile its
+// leaves, per 512-byte block of a row, the block's largest logit (1/128 of the
+// bytes read), and per wave's tile its
 // maximum and sum of exponentials.  beam_pick_kernel, one workgroup per group,
 // merges the sums into lse_w and needs only those n blocks that come first by
 // (largest score, position): blocks are contiguous runs of w * V + v, so a
@@ -37,11 +37,12 @@ namespace sv {
 
 constexpr int kBeamMaxBeams = 64;
 constexpr int kBeamMaxSelect = 128;
-constexpr int kBeamBlockBytes = 256;  // 16 lanes' 16-byte loads
+constexpr int kBeamBlockBytes = 512;  // 32 lanes' 16-byte loads
 constexpr int kPickThreads = 1024;
 constexpr int kPickWaves = kPickThreads / kWave;
-constexpr int kPickCap = 1024;   // candidate blocks, and candidate elements, held in LDS
+constexpr int kPickCap = kPickThreads;  // candidate blocks, and candidate elements, held in LDS: one per thread
 constexpr int kPickBins = 256;   // maxima the pick's lower bound is taken from (at least kBeamMaxSelect)
+constexpr int kPickHeld = 8;     // block maxima a thread holds at a time (8192 blocks per group)
 constexpr double kBeamWindow = 6.4e-6;
 static_assert(kPickBins >= kBeamMaxSelect, "the bound needs one bin per selected candidate");
 
@@ -58,8 +59,8 @@ __device__ __forceinline__ bool beam_streams(const float* cum, const uint8_t* fi
     return s - s == 0.0f && !(finished != nullptr && finished[row] != 0);
 }
 
-// One workgroup per (row, chunk) tile.  blkmax[row][chunk * LOADS * 16 + i]:
-// the largest logit of the tile's i-th 256-byte block (-inf outside the row);
+// One workgroup per (row, chunk) tile.  blkmax[row][chunk * LOADS * 8 + i]:
+// the largest logit of the tile's i-th 512-byte block (-inf outside the row);
 // parts[row][chunk * 4 + wave].  Rows that do not take part are not read.
 template <int DT, int LOADS>
 __global__ __launch_bounds__(kThreads) void beam_stream_kernel(RowSet rs, const float* __restrict__ cum,
@@ -75,7 +76,7 @@ __global__ __launch_bounds__(kThreads) void beam_stream_kernel(RowSet rs, const 
     issue_tile<DT, LOADS, true>(t, base, raw);
     sanitize_edge<DT, LOADS>(t, vocab, raw);
     float tm = neg_inf();
-    float* bm = blkmax + (int64_t)t.row * nblkp + t.cb0 / 16 + (threadIdx.x >> 4);
+    float* bm = blkmax + (int64_t)t.row * nblkp + t.cb0 / 32 + (threadIdx.x >> 5);
 #pragma unroll
     for (int i = 0; i < LOADS; ++i) {
         float f[VEC];
@@ -88,7 +89,9 @@ __global__ __launch_bounds__(kThreads) void beam_stream_kernel(RowSet rs, const 
         b = fmaxf(b, __int_as_float(dpp_mov<kDppQuad2301>(ninf, __float_as_int(b))));
         b = fmaxf(b, __int_as_float(dpp_mov<kDppHalfMirror>(ninf, __float_as_int(b))));
         b = fmaxf(b, __int_as_float(dpp_mov<kDppMirror>(ninf, __float_as_int(b))));
-        if ((threadIdx.x & 15) == 0) bm[i * (kThreads / 16)] = b;
+        // row_bcast:15 brings row 0's maximum to row 1 and row 2's to row 3
+        b = fmaxf(b, __int_as_float(dpp_mov<kDppBcast15, 0xa>(ninf, __float_as_int(b))));
+        if ((threadIdx.x & 31) == 31) bm[i * (kThreads / 32)] = b;
         tm = fmaxf(tm, b);
     }
     const float wm = wave_max_dpp(tm);
@@ -135,27 +138,72 @@ __device__ __forceinline__ bool ahead(double sa, int32_t ia, double sb, int32_t 
     return sa > sb || (sa == sb && ia < ib);
 }
 
+// exp(x) in fp64 for x <= 0 (and NaN): 2^(n / 32) from a table and exp of the
+// rest, at most ln 2 / 64 = 0.0109, by its series to the 6th power (the next
+// term is below 4e-18 relative).  About a dozen fp64 instructions; the library's
+// exp took four times as long over a row.
+constexpr int kExpTable = 32;
+static __device__ const double kExp2Of32nds[kExpTable] = {  // 2^(j / 32)
+    0x1.0000000000000p+0, 0x1.059b0d3158574p+0, 0x1.0b5586cf9890fp+0, 0x1.11301d0125b51p+0,
+    0x1.172b83c7d517bp+0, 0x1.1d4873168b9aap+0, 0x1.2387a6e756238p+0, 0x1.29e9df51fdee1p+0,
+    0x1.306fe0a31b715p+0, 0x1.371a7373aa9cbp+0, 0x1.3dea64c123422p+0, 0x1.44e086061892dp+0,
+    0x1.4bfdad5362a27p+0, 0x1.5342b569d4f82p+0, 0x1.5ab07dd485429p+0, 0x1.6247eb03a5585p+0,
+    0x1.6a09e667f3bcdp+0, 0x1.71f75e8ec5f74p+0, 0x1.7a11473eb0187p+0, 0x1.82589994cce13p+0,
+    0x1.8ace5422aa0dbp+0, 0x1.93737b0cdc5e5p+0, 0x1.9c49182a3f090p+0, 0x1.a5503b23e255dp+0,
+    0x1.ae89f995ad3adp+0, 0x1.b7f76f2fb5e47p+0, 0x1.c199bdd85529cp+0, 0x1.cb720dcef9069p+0,
+    0x1.d5818dcfba487p+0, 0x1.dfc97337b9b5fp+0, 0x1.ea4afa2a490dap+0, 0x1.f50765b6e4540p+0,
+};
+__device__ __forceinline__ double exp_f64(double x, const double* table)
+{
+    const double n = __builtin_rint(x * (kExpTable * 1.4426950408889634));
+    // ln 2 / 32 in two parts, the first of 25 bits: its product with n (16 bits where the result is not 0) is exact
+    const double r = __builtin_fma(n, -0x1.f473de6af278fp-35, __builtin_fma(n, -0x1.62e42fep-6, x));
+    double p = __builtin_fma(r, 1.0 / 720, 1.0 / 120);
+    p = __builtin_fma(r, p, 1.0 / 24);
+    p = __builtin_fma(r, p, 1.0 / 6);
+    p = __builtin_fma(r, p, 0.5);
+    p = __builtin_fma(r, p, 1.0);
+    p = __builtin_fma(r, p, 1.0);
+    const int k = (int)n;
+    const double e = __builtin_ldexp(p * table[k & (kExpTable - 1)], k >> 5);
+    return x < -800.0 ? 0.0 : e;
+}
+
+// What the fp32 pass over the block maxima needs of a beam: a block's score is
+// off + (m - top) / T for blocks first .. last, -inf elsewhere.  (An ended
+// beam: off at its pad token's block, with scale 0 for whatever m holds there.)
+struct BeamView {
+    float off, top;
+    int32_t first, last;
+};
+
 template <int DT>
 __global__ __launch_bounds__(kPickThreads) void beam_pick_kernel(PickArgs a)
 {
     constexpr int ES = Dt<DT>::kSize;
     constexpr int BE = kBeamBlockBytes / ES;  // elements per block
     __shared__ double s_off[kBeamMaxBeams];   // score = s_off + (l - s_top) / T; -inf: the beam gives no candidate
+    __shared__ __align__(16) BeamView s_view[kBeamMaxBeams];
     __shared__ float s_top[kBeamMaxBeams];    // the row's largest logit
     __shared__ int32_t s_end[kBeamMaxBeams];  // ended beam: 1
-    __shared__ uint32_t s_key[kPickThreads];
+    __shared__ float s_bin[kPickThreads];
     __shared__ double s_bs[kPickCap];
     __shared__ int32_t s_bi[kPickCap];
+    __shared__ float s_bm[kPickCap];
+    __shared__ int32_t s_br[kPickCap];
     __shared__ double s_es[kPickCap];
     __shared__ int32_t s_ei[kPickCap];
+    __shared__ int32_t s_er[kPickCap];
     __shared__ double s_ss[kBeamMaxSelect];   // the selected blocks, later the selected candidates
     __shared__ int32_t s_si[kBeamMaxSelect];
-    __shared__ int32_t s_cnt, s_ecnt, s_bound;
+    __shared__ int32_t s_cnt, s_ecnt;
+    __shared__ float s_bound;
     __shared__ uint32_t s_mark[2];
     __shared__ double s_red[kPickWaves];
     __shared__ int32_t s_redi[kPickWaves];
+    __shared__ double s_exp[kExpTable];
 
-    const int tid = threadIdx.x, lane = lane_id(), wave = wave_id();
+    const int tid = threadIdx.x, lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(wave_id());
     const int32_t g = (int32_t)blockIdx.x, W = a.beams, V = a.vocab, n = a.nsel;
     const int32_t row0 = g * W;
     const double T = (double)a.temperature;
@@ -165,25 +213,60 @@ __global__ __launch_bounds__(kPickThreads) void beam_pick_kernel(PickArgs a)
     // an ended beam's only block with a candidate
     auto pad_block = [&](int32_t w) { return (a.pad_token + mis_of(w)) / BE; };
 
-    // ---- the beams' offsets: cum - lse, one wave per beam in turn
+    // ---- the block maxima, before anything that their scores wait for (blocks of beams that were not streamed hold
+    // old bytes, which block_score ignores)
+    const int32_t per_row = a.nblkp / kWave;  // runs of 64 blocks per row: a wave's run lies in one row
+    const int32_t runs = W * per_row;
+    // A wave's runs wave, wave + 16, ... as (beam, run of its row).  The quotient by a multiplication: runs < 2^14 and
+    // per_row <= 2^8, so the rounded-up reciprocal's excess, below 2^-24 per run, never reaches the next integer.
+    struct Run {
+        int32_t q, w, r;
+    };
+    const uint32_t recip = per_row > 1 ? (uint32_t)(0xffffffffu / (uint32_t)per_row) + 1u : 0u;
+    // (the empty asm keeps the compiler from computing every run once, up front, and holding all of them: that spilled
+    // 588 bytes a lane)
+    auto run_at = [&](int32_t q) {
+        asm volatile("" : "+s"(q));
+        const int32_t w = per_row > 1 ? (int32_t)__umulhi((uint32_t)q, recip) : q;
+        return Run{q, w, q - w * per_row};
+    };
+    auto next_run = [&](Run& c) { c = run_at(c.q + kPickWaves); };
+    const float* blkmax = a.blkmax + (int64_t)row0 * a.nblkp;
+    constexpr int kGroupRuns = kPickHeld * kPickWaves;  // runs that the workgroup's registers hold at a time
+    float held[kPickHeld];
+    auto bring = [&](int32_t q0) {
+#pragma unroll
+        for (int j = 0; j < kPickHeld; ++j) {
+            const int32_t q = q0 + wave + j * kPickWaves;
+            held[j] = q < runs ? blkmax[q * kWave + lane] : 0.0f;
+        }
+    };
+    bring(0);
+
+    if (tid < kExpTable) s_exp[tid] = kExp2Of32nds[tid];
+    __syncthreads();
+
+    // ---- the beams' offsets: cum - log S, one wave per beam in turn
     for (int32_t w = wave; w < W; w += kPickWaves) {
         const int32_t row = row0 + w;
+        // (parts of a beam that was not streamed hold old bytes and are not used)
+        const BeamPart* p = a.parts + (int64_t)row * a.nparts;
+        BeamPart first{0.0, neg_inf(), 0};  // this lane's first part stays in registers
+        if (lane < a.nparts) first = p[lane];
         const float cum = a.cum[row];
         double off = ninf;
         float top = neg_inf();
         int32_t ended = 0;
         if (beam_streams(a.cum, a.finished, row)) {
-            const BeamPart* p = a.parts + (int64_t)row * a.nparts;
-            float m = neg_inf();
-            for (int32_t i = lane; i < a.nparts; i += kWave) m = fmaxf(m, p[i].m);
+            float m = first.m;
+            for (int32_t i = lane + kWave; i < a.nparts; i += kWave) m = fmaxf(m, p[i].m);
             top = wave_max_dpp(m);
-            double s = 0.0;
-            for (int32_t i = lane; i < a.nparts; i += kWave) {
-                const float pm = p[i].m;
-                const double ps = p[i].s;
-                // a part with no finite logit holds 0 (or NaN, from a NaN logit)
-                s += pm == neg_inf() ? ps : ps * exp(((double)pm - (double)top) / T);
-            }
+            // a part with no finite logit holds 0 (or NaN, from a NaN logit)
+            auto share = [&](float pm, double ps) {
+                return pm == neg_inf() ? ps : ps * exp_f64(((double)pm - (double)top) / T, s_exp);
+            };
+            double s = share(first.m, first.s);
+            for (int32_t i = lane + kWave; i < a.nparts; i += kWave) s += share(p[i].m, p[i].s);
             s = wave_sum_dpp(s);
             off = (double)cum - log(s);
             if (!(off - off == 0.0)) off = ninf;  // no finite logit, or NaN or +inf among them
@@ -194,19 +277,42 @@ __global__ __launch_bounds__(kPickThreads) void beam_pick_kernel(PickArgs a)
         if (lane == 0) {
             s_off[w] = off;
             s_top[w] = top;
+            s_view[w] = off == ninf ? BeamView{0.0f, 0.0f, 1, 0}
+                        : ended     ? BeamView{(float)off, __builtin_nanf(""), pad_block(w), pad_block(w)}
+                                    : BeamView{(float)off, top, 0, a.nblk - 1};
             s_end[w] = ended;
         }
     }
     if (tid < 2) s_mark[tid] = 0u;
     __syncthreads();
 
-    const int32_t per_row = a.nblkp / kWave;  // runs of 64 blocks per row: a wave's run lies in one row
-    // the largest score of block `blk` of beam w
-    auto block_score = [&](int32_t w, int32_t blk) -> double {
+    // the largest score of block `blk` of beam w, and its fp32 form
+    auto block_score = [&](int32_t w, int32_t blk, float m) -> double {
         const double off = s_off[w];
         if (off == ninf || blk >= a.nblk) return ninf;
         if (s_end[w] != 0) return blk == pad_block(w) ? off : ninf;
-        return off + ((double)a.blkmax[(int64_t)(row0 + w) * a.nblkp + blk] - (double)s_top[w]) / T;
+        return off + ((double)m - (double)s_top[w]) / T;
+    };
+    const float inv_t = 1.0f / a.temperature;
+    auto block_score_f = [&](int32_t w, int32_t blk, float m) -> float {
+        const BeamView v = s_view[w];
+        const float x = v.top == v.top ? (m - v.top) * inv_t : 0.0f;
+        return blk >= v.first && blk <= v.last ? v.off + x : neg_inf();
+    };
+    // The places of the first `count` entries (s, i) of two lists: place(entry, its place), called by one thread per
+    // entry.  16 threads share an entry's comparisons.
+    auto rank = [&](const double* ls, const int32_t* li, int32_t count, auto place) {
+        for (int32_t c0 = 0; c0 < count; c0 += kPickThreads / 16) {
+            const int32_t c = c0 + tid / 16, at = min(c, count - 1);
+            const double s = ls[at];
+            const int32_t i = li[at];
+            int32_t r = 0;
+#pragma unroll 4
+            for (int32_t j = tid & 15; j < count; j += 16) r += ahead(ls[j], li[j], s, i) ? 1 : 0;
+#pragma unroll
+            for (int o = 1; o < 16; o <<= 1) r += __shfl_xor(r, o, kWave);
+            if (c < count && (tid & 15) == 0) place(c, r);
+        }
     };
     // the score of element j of block `blk` of beam w, and its position in the group
     auto element_score = [&](int32_t w, int32_t blk, int32_t j, int32_t* pos) -> double {
@@ -246,69 +352,101 @@ __global__ __launch_bounds__(kPickThreads) void beam_pick_kernel(PickArgs a)
     int32_t nout = 0;
     for (int pass = 0;; ++pass) {
         const double win = pass == 0 ? kBeamWindow : 0.0;
-        // ---- a lower bound of the n-th best block: the n-th largest of kPickBins bins' maxima (fp32 keys: the
-        // rounding keeps the order, so every block at or above the n-th best has a key at or above the bound)
+        // ---- a lower bound of the n-th best block: the n-th largest of kPickBins bins' maxima, in fp32, by its
+        // distance below the largest to 5 mantissa bits
         if (tid == 0) s_cnt = s_ecnt = 0;
-        float km = neg_inf();
-        for (int32_t q = wave; q < W * per_row; q += kPickWaves) {
-            const int32_t w = q / per_row;
-            km = fmaxf(km, (float)block_score(w, (q - w * per_row) * kWave + lane));
+        float km = neg_inf(), near[kPickHeld];
+        auto score_group = [&](int32_t q0) {
+            Run c = run_at(q0 + wave);
+#pragma unroll
+            for (int j = 0; j < kPickHeld; ++j) {
+                near[j] = c.q < runs ? block_score_f(c.w, c.r * kWave + lane, held[j]) : neg_inf();
+                km = fmaxf(km, near[j]);
+                next_run(c);
+            }
+        };
+        for (int32_t q0 = 0; q0 < runs; q0 += kGroupRuns) {
+            if (q0 > 0) bring(q0);
+            score_group(q0);
         }
-        s_key[tid] = order_key(km);
+        s_bin[tid] = km;
+        float most = lane < W && s_view[lane].first <= s_view[lane].last ? fabsf(s_view[lane].off) : 0.0f;
+        most = wave_max_dpp(most);
         __syncthreads();
         if (wave == 0) {
-            uint32_t k[kPickBins / kWave];
+            constexpr int KEYS = kPickBins / kWave;
+            float v[KEYS], best = neg_inf();
 #pragma unroll
-            for (int j = 0; j < kPickBins / kWave; ++j) {
-                k[j] = 0u;
+            for (int j = 0; j < KEYS; ++j) {
+                v[j] = neg_inf();
 #pragma unroll
-                for (int i = 0; i < kPickThreads / kPickBins; ++i)
-                    k[j] = max(k[j], s_key[(i * (kPickBins / kWave) + j) * kWave + lane]);
+                for (int i = 0; i < kPickThreads / kPickBins; ++i) v[j] = fmaxf(v[j], s_bin[(i * KEYS + j) * kWave + lane]);
+                best = fmaxf(best, v[j]);
             }
-            uint32_t cur = 0u;
-            for (int b = 31; b >= 0; --b) {
-                const uint32_t t = cur | (1u << b);
+            best = wave_max_dpp(best);
+            uint32_t k[KEYS];
+#pragma unroll
+            for (int j = 0; j < KEYS; ++j) k[j] = __float_as_uint(best - v[j]) >> 18;
+            uint32_t cur = 0u;  // the least prefix that n bins do not exceed
+#pragma unroll
+            for (int b = 12; b >= 0; --b) {
+                const uint32_t t = cur + (1u << b);
                 int cnt = 0;
 #pragma unroll
-                for (int j = 0; j < kPickBins / kWave; ++j) cnt += __popcll(__ballot(k[j] >= t));
-                if (cnt >= n) cur = t;
+                for (int j = 0; j < KEYS; ++j) cnt += __popcll(__ballot(k[j] < t));
+                if (cnt < n) cur = t;
             }
-            if (lane == 0) s_bound = (int32_t)cur;
+            // An fp32 score is off by less than e = 2^-21 (|score| + the largest |offset|): difference, 1 / T, product,
+            // offset and sum each rounded once, (m - top) / T at most |score| + |offset|.  The n bins are at least
+            // best - d in fp32 (two roundings here), so at least that less e in fp64, and a block that reaches this
+            // less the window has an fp32 score another e lower.
+            const float d = __uint_as_float((cur << 18) | 0x3ffffu);
+            float low = neg_inf();
+            if (best != neg_inf() && d < __builtin_inff()) {
+                const float bound = best - d;
+                low = bound - 0x1p-21f * (3.0f * fabsf(bound) + 3.0f * most + fabsf(best)) - 1e-30f - (float)(win * 1.01);
+            }
+            if (lane == 0) s_bound = low;
         }
         __syncthreads();
-        const uint32_t bound = (uint32_t)s_bound;
-        // one fp32 step below the bound, less the window: an fp64 score under it cannot matter
-        const double low = bound <= order_key(neg_inf())
-                               ? ninf
-                               : (double)key_to_float(bound) - fabs((double)key_to_float(bound)) * 0x1p-23 - 1e-30 - win;
+        const float low = s_bound;
         // ---- the blocks at or above it
-        for (int32_t q = wave; q < W * per_row; q += kPickWaves) {
-            const int32_t w = q / per_row;
-            const int32_t blk = (q - w * per_row) * kWave + lane;
-            const double s = block_score(w, blk);
-            if (s >= low && s > ninf) {
-                const int32_t at = atomicAdd(&s_cnt, 1);
-                if (at < kPickCap) {
-                    s_bs[at] = s;
-                    s_bi[at] = w * a.nblkp + blk;
-                }
+        auto take = [&](const Run& c, float m) {
+            const int32_t at = atomicAdd(&s_cnt, 1);
+            if (at < kPickCap) {
+                s_bm[at] = m;
+                s_bi[at] = c.w * a.nblkp + c.r * kWave + lane;
+            }
+        };
+        for (int32_t q0 = 0; q0 < runs; q0 += kGroupRuns) {
+            if (runs > kGroupRuns) {
+                bring(q0);
+                score_group(q0);
+            }
+            Run c = run_at(q0 + wave);
+#pragma unroll
+            for (int j = 0; j < kPickHeld; ++j) {
+                if (near[j] >= low && near[j] > neg_inf()) take(c, held[j]);
+                next_run(c);
             }
         }
         __syncthreads();
         const int32_t cnt = s_cnt;
         int32_t nblocks = min(cnt, n);
         bool overflow = cnt > kPickCap;
-        int32_t rb = 0;  // this thread's block's place
         if (!overflow) {
             if (tid < cnt) {
-                const double s = s_bs[tid];
-                const int32_t i = s_bi[tid];
-                for (int32_t j = 0; j < cnt; ++j) rb += ahead(s_bs[j], s_bi[j], s, i) ? 1 : 0;
-                if (rb < n) {
-                    s_ss[rb] = s;
-                    s_si[rb] = i;
-                }
+                const int32_t w = s_bi[tid] / a.nblkp;
+                s_bs[tid] = block_score(w, s_bi[tid] - w * a.nblkp, s_bm[tid]);
             }
+            __syncthreads();
+            rank(s_bs, s_bi, cnt, [&](int32_t c, int32_t r) {
+                s_br[c] = r;
+                if (r < n) {
+                    s_ss[r] = s_bs[c];
+                    s_si[r] = s_bi[c];
+                }
+            });
             __syncthreads();
         } else if (pass > 0) {
             // more ties than the list holds: take the first n blocks one after another
@@ -317,11 +455,9 @@ __global__ __launch_bounds__(kPickThreads) void beam_pick_kernel(PickArgs a)
             for (nblocks = 0; nblocks < n; ++nblocks) {
                 double bs = ninf;
                 int32_t bi = INT32_MAX;
-                for (int32_t q = wave; q < W * per_row; q += kPickWaves) {
-                    const int32_t w = q / per_row;
-                    const int32_t blk = (q - w * per_row) * kWave + lane;
-                    const double s = block_score(w, blk);
-                    const int32_t i = w * a.nblkp + blk;
+                for (Run c = run_at(wave); c.q < runs; next_run(c)) {
+                    const int32_t blk = c.r * kWave + lane, i = c.w * a.nblkp + blk;
+                    const double s = block_score(c.w, blk, blkmax[c.q * kWave + lane]);
                     if (ahead(ps, pi, s, i) && ahead(s, i, bs, bi)) {
                         bs = s;
                         bi = i;
@@ -358,17 +494,13 @@ __global__ __launch_bounds__(kPickThreads) void beam_pick_kernel(PickArgs a)
             const int32_t ecnt = s_ecnt;
             nout = min(ecnt, n);
             if (ecnt <= kPickCap) {
-                int32_t r = n;
-                if (tid < ecnt) {
-                    const double s = s_es[tid];
-                    const int32_t i = s_ei[tid];
-                    r = 0;
-                    for (int32_t j = 0; j < ecnt; ++j) r += ahead(s_es[j], s_ei[j], s, i) ? 1 : 0;
+                rank(s_es, s_ei, ecnt, [&](int32_t c, int32_t r) {
+                    s_er[c] = r;
                     if (r < n) {
-                        s_ss[r] = s;  // (the blocks' places are no longer needed: see the barrier above)
-                        s_si[r] = i;
+                        s_ss[r] = s_es[c];  // (the blocks' places are no longer needed: see the barrier above)
+                        s_si[r] = s_ei[c];
                     }
-                }
+                });
                 __syncthreads();
                 if (pass == 0) {
                     // candidates of different beams closer than the window, in the list or just outside it
@@ -382,12 +514,12 @@ __global__ __launch_bounds__(kPickThreads) void beam_pick_kernel(PickArgs a)
                     if (nout == n) {
                         const double last = s_ss[n - 1];
                         const int32_t wl = s_si[n - 1] / V;
-                        if (tid < ecnt && r >= n && s_es[tid] >= last - win && s_ei[tid] / V != wl) {
+                        if (tid < ecnt && s_er[tid] >= n && s_es[tid] >= last - win && s_ei[tid] / V != wl) {
                             mark(wl);
                             mark(s_ei[tid] / V);
                         }
                         // (a block that was not read: its largest element is outside)
-                        if (tid < cnt && rb >= n && s_bs[tid] >= last - win && s_bi[tid] / a.nblkp != wl) {
+                        if (tid < cnt && s_br[tid] >= n && s_bs[tid] >= last - win && s_bi[tid] / a.nblkp != wl) {
                             mark(wl);
                             mark(s_bi[tid] / a.nblkp);
                         }
@@ -436,10 +568,31 @@ __global__ __launch_bounds__(kPickThreads) void beam_pick_kernel(PickArgs a)
         for (int32_t w = 0; w < W; ++w) {
             if (!(marked >> w & 1) || s_end[w] != 0 || s_off[w] == ninf) continue;
             const char* row = row_ptr(a.rs, row0 + w);
-            const double m = (double)s_top[w];
+            const double m = (double)s_top[w], inv = 1.0 / T;
             double s = 0.0;
-#pragma unroll 4
-            for (int32_t v = tid; v < V; v += kPickThreads) s += exp(((double)load_one<DT>(row, v) - m) / T);
+            // Chunks of 16 bytes counted from the row's start wherever it lies (the loads need no alignment): the
+            // same terms go to the same thread in the same order in every row, so rows that are copies of one
+            // another get the same bits and tie.
+            constexpr int VEC = Dt<DT>::kVec;
+            typedef u32x4 loose __attribute__((aligned(2)));
+            auto chunk = [&](int32_t k) { return *(const SV_GLOBAL loose*)(row + (int64_t)k * 16); };
+            const int32_t nk = V / VEC;
+            u32x4 ahead1{}, ahead2{};
+            if (tid < nk) ahead1 = chunk(tid);
+            if (tid + kPickThreads < nk) ahead2 = chunk(tid + kPickThreads);
+            for (int32_t k = tid; k < nk; k += kPickThreads) {
+                float x[VEC];
+                unpack<DT>(ahead1, x);
+                ahead1 = ahead2;
+                if (k + 2 * kPickThreads < nk) ahead2 = chunk(k + 2 * kPickThreads);
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) {
+                    s += exp_f64(((double)x[j] - m) * inv, s_exp);
+                    if (j & 1) __builtin_amdgcn_sched_barrier(0);  // more side by side spills registers
+                }
+            }
+            for (int32_t v = nk * VEC + tid; v < V; v += kPickThreads)
+                s += exp_f64(((double)load_one<DT>(row, v) - m) * inv, s_exp);
             s = wave_sum_dpp(s);
             __syncthreads();
             if (lane == 0) s_red[wave] = s;
@@ -448,8 +601,10 @@ __global__ __launch_bounds__(kPickThreads) void beam_pick_kernel(PickArgs a)
                 double t = 0.0;
                 for (int k = 0; k < kPickWaves; ++k) t += s_red[k];
                 s_off[w] = (double)a.cum[row0 + w] - log(t);
+                s_view[w].off = (float)s_off[w];
             }
         }
+        bring(0);  // (not held across the sums)
         __syncthreads();
     }
     if (tid < n) {
