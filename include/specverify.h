@@ -340,8 +340,9 @@ SV_API sv_status_t spec_token_likelihood(const sv_shape_t* shape,
  *   extends (0 .. beams - 1, within its group).  Places that no candidate
  *   fills hold -inf, -1, -1.
  *   1 <= beams <= SV_MAX_BEAMS, 1 <= num_select <= SV_MAX_SELECT.
- * Outputs may not overlap inputs.  Memory, execution, workspace and errors as
- * for spec_verify_sample.
+ * out_scores may be `scores` itself when num_select == beams; other overlaps of
+ * outputs with inputs are not allowed.  Memory, execution, workspace and errors
+ * as for spec_verify_sample.
  */
 #define SV_MAX_BEAMS 64
 #define SV_MAX_SELECT 128
@@ -386,9 +387,11 @@ SV_API sv_status_t spec_beam_select(const sv_beam_shape_t* shape,
  *   `positions` as `positions`.
  * Arguments
  *   states: device memory, read and written; parents int32 [groups * beams];
- *   lengths int32 [groups * beams] or NULL.  Strides are in bytes.
+ *   lengths int32 [groups * beams] or NULL, neither of them among the states'
+ *   bytes.  Strides are in bytes.
  * Errors: SV_ERR_INVALID_ARGUMENT (null or misaligned pointer, a count < 1,
- * positions, row_bytes or a stride < 0, places that overlap),
+ * positions, row_bytes or a stride < 0, places that overlap, parents or lengths
+ * between the states' first and last byte),
  * SV_ERR_UNSUPPORTED (beams > SV_MAX_BEAMS, or one slab and head of a beam of
  * more than 2^31 - 1 pieces, a piece being 16, 4, 2 or 1 bytes as the
  * alignment of states, row_bytes and the strides allows), SV_ERR_HIP.  Execution as for
@@ -444,12 +447,12 @@ SV_API sv_status_t spec_state_reorder(const sv_state_shape_t* shape,
  *   Sums, softmax statistics and scores are fp32; the softmax weights are
  *   rounded to dtype for the product with v.
  * Errors as for spec_verify_sample; SV_ERR_INVALID_ARGUMENT also for q_heads
- * no multiple of kv_heads; SV_ERR_UNSUPPORTED also for fp32, another head_dim,
- * more than 2^30 positions, or positions more than 64 MB apart.  Data
+ * no multiple of kv_heads and for rows of out that overlap; SV_ERR_UNSUPPORTED also for fp32, another head_dim,
+ * more than 2^30 positions, or positions more than 32 MB apart.  Data
  * preconditions: keys and values within the lengths finite; cu_draft and
  * cu_groups prefix sums, no group larger than max_group.  Where they are
  * violated, out holds unspecified values and nothing out of bounds is read or
- * written.  out may not overlap the inputs.
+ * written.  out may be q itself; it may not overlap the inputs otherwise.
  */
 typedef struct {
     const void* data;

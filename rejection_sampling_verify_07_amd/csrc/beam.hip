@@ -112,12 +112,13 @@ sv_status_t beam_select_common(const sv_beam_shape_t* sh, const void* logits, co
 
 // Whether the places of [slabs][beams][heads][positions][row_bytes] with these
 // strides are all distinct: every stride clears the extent of the dimensions
-// inside it.
-bool distinct_places(const sv_state_shape_t* sh, int64_t beams)
+// inside it.  *bytes: the extent of all of them.
+bool distinct_places(const sv_state_shape_t* sh, int64_t beams, int64_t* bytes)
 {
     int64_t size[4] = {sh->slabs, beams, sh->heads, sh->positions};
     int64_t stride[4] = {sh->slab_stride, sh->beam_stride, sh->head_stride, sh->position_stride};
-    int64_t extent = sh->row_bytes;
+    int64_t& extent = *bytes;
+    extent = sh->row_bytes;
     bool done[4] = {};
     for (int k = 0; k < 4; ++k) {
         int at = -1;  // the smallest stride left, of the dimensions that have more than one place
@@ -179,14 +180,22 @@ sv_status_t state_reorder_common(const sv_state_shape_t* sh, void* states, const
     if (sh->slab_stride < 0 || sh->beam_stride < 0 || sh->head_stride < 0 || sh->position_stride < 0)
         return SV_ERR_INVALID_ARGUMENT;
     const bool empty = sh->positions == 0 || sh->row_bytes == 0;
-    if (!empty && !distinct_places(sh, (int64_t)sh->groups * sh->beams)) return SV_ERR_INVALID_ARGUMENT;
+    const int64_t batch = (int64_t)sh->groups * sh->beams;
+    int64_t extent = 0;
+    if (!empty && !distinct_places(sh, batch, &extent)) return SV_ERR_INVALID_ARGUMENT;
     if ((states == nullptr && !empty) || parents == nullptr || !aligned(parents, 4) || !aligned(lengths, 4))
         return SV_ERR_INVALID_ARGUMENT;
     if (empty) return SV_OK;
+    // the order is read while states move: it may not lie among them
+    const auto inside = [&](const int32_t* p) {
+        const uintptr_t a = (uintptr_t)p, b = (uintptr_t)states;
+        return p != nullptr && a < b + (uintptr_t)extent && b < a + (uintptr_t)batch * 4;
+    };
+    if (inside(parents) || inside(lengths)) return SV_ERR_INVALID_ARGUMENT;
     // the widest piece that every row divides into; 16-byte pieces need rows on 4-byte places only
     uint64_t places = (uint64_t)(uintptr_t)states;
     if (sh->slabs > 1) places |= (uint64_t)sh->slab_stride;
-    if ((int64_t)sh->groups * sh->beams > 1) places |= (uint64_t)sh->beam_stride;
+    if (batch > 1) places |= (uint64_t)sh->beam_stride;
     if (sh->heads > 1) places |= (uint64_t)sh->head_stride;
     if (sh->positions > 1) places |= (uint64_t)sh->position_stride;
     places |= (uint64_t)sh->row_bytes % 16;
@@ -214,19 +223,20 @@ sv_status_t state_reorder_common(const sv_state_shape_t* sh, void* states, const
 
 // ---- shared-prefix attention
 
-constexpr int32_t kMaxPosStride = 1 << 26;   // bytes: 32 positions stay within a 32-bit offset
+constexpr int32_t kMaxPosStride = 1 << 25;  // bytes: 64 positions stay within a 31-bit offset
 constexpr int32_t kMaxPositions = 1 << 30;
-#ifndef SV_AT_G
-#define SV_AT_G 512
-#endif
-#ifndef SV_AT_TROWS
-#define SV_AT_TROWS 32
-#endif
-#ifndef SV_AT_K
-#define SV_AT_K 512
-#endif
-constexpr int64_t kAttnGroups = SV_AT_G;        // workgroups that the splits aim at
-constexpr int32_t kAttnMinKeys = SV_AT_K;        // keys per workgroup that a split keeps
+constexpr int64_t kMaxRows = INT32_MAX / 2;  // query rows of one key/value head in one group
+
+// Workgroups that the splits of the keys aim at.  Work whose rows fit one workgroup is bound by reading the caches, and
+// one workgroup per CU reads them as fast as two while its parts cost half as much to write and join: 194 against
+// 214 us on 4 groups of 8 beams with 65536 shared positions, 27 against 31 us for 128 rows per key head on 32768.
+// Work of more row tiles is bound by the products, which two workgroups per CU overlap better: 122 against 150 us for
+// 1280 rows per key head on 16384 positions.
+constexpr int64_t kSplitReading = 256;
+constexpr int64_t kSplitProducts = 512;
+// Keys that a split keeps at least, one step of the four waves: 7.5 us for 4 single rows on 500 positions, 9.9 us with
+// 512; 17 us for 80 rows of 256 columns on 2049 positions, 28 us with 512.
+constexpr int32_t kSplitKeys = sv::kKeyRound;
 
 struct AttnPlan {
     bool tiles;
@@ -235,11 +245,11 @@ struct AttnPlan {
     size_t off_acc, off_ml, bytes;
 };
 
-int32_t attn_splits(int64_t workgroups, int32_t positions)
+int32_t attn_splits(int64_t workgroups, int32_t positions, int64_t target)
 {
     if (positions == 0) return 0;
-    int64_t n = kAttnGroups / workgroups;
-    const int64_t most = (positions + kAttnMinKeys - 1) / kAttnMinKeys;
+    int64_t n = target / workgroups;
+    const int64_t most = (positions + kSplitKeys - 1) / kSplitKeys;
     if (n > most) n = most;
     return n < 1 ? 1 : (int32_t)n;
 }
@@ -252,15 +262,19 @@ AttnPlan attn_plan(const sv_attention_shape_t* sh)
     const int64_t per_group = sh->cu_groups != nullptr ? sh->max_group : sh->batch / sh->groups;
     const int64_t prows = per_group * (sh->max_draft + 1) * p.rep;
     const int32_t most = sh->head_dim == 256 ? 1 : 2;  // 16-row tiles per wave that the registers hold
+    // More rows than one wave holds: the waves share the rows and the keys pass through LDS.  (64 rows per key head on
+    // 8192 positions: 50 us, against 77 us with 64 rows in every wave; 32 rows on 4096: 32 us, against 26 us without.)
     p.tiles = prows > most * 16;
     p.mtp = prows <= 16 ? 1 : most;
     const int32_t wg_rows = p.mtp * 16 * (p.tiles ? sv::kAttnWaves : 1);
     p.ptiles = (int32_t)((prows + wg_rows - 1) / wg_rows);
+    // (20 rows per sequence and key head on 300 own positions: 30 us with two tiles per wave, 36 us with one)
     const int64_t srows = (int64_t)(sh->max_draft + 1) * p.rep;
     p.mts = srows <= 16 ? 1 : most;
     p.stiles = (int32_t)((srows + p.mts * 16 - 1) / (p.mts * 16));
-    p.psplits = attn_splits((int64_t)sh->groups * sh->kv_heads * p.ptiles, sh->max_prefix);
-    p.ssplits = attn_splits((int64_t)sh->batch * sh->kv_heads * p.stiles, sh->max_suffix);
+    p.psplits = attn_splits((int64_t)sh->groups * sh->kv_heads * p.ptiles, sh->max_prefix,
+                            p.ptiles == 1 ? kSplitReading : kSplitProducts);
+    p.ssplits = attn_splits((int64_t)sh->batch * sh->kv_heads * p.stiles, sh->max_suffix, kSplitReading);
     p.punits = (int64_t)sh->groups * sh->kv_heads * p.psplits;
     p.pblocks = (p.punits + 7) / 8 * 8 * p.ptiles;
     p.grid = p.pblocks + (int64_t)sh->batch * sh->kv_heads * p.stiles * p.ssplits;
@@ -295,6 +309,8 @@ sv_status_t check_attention(const sv_attention_shape_t* sh, float scale)
     if (sh->max_draft > SV_MAX_DRAFT || sh->max_prefix > kMaxPositions || sh->max_suffix > kMaxPositions)
         return SV_ERR_UNSUPPORTED;
     if (((int64_t)sh->total_draft + sh->batch) * sh->q_heads > INT32_MAX / 2) return SV_ERR_UNSUPPORTED;
+    const int64_t per_group = sh->cu_groups != nullptr ? sh->max_group : sh->batch / sh->groups;
+    if (per_group * (sh->max_draft + 1) > kMaxRows / (sh->q_heads / sh->kv_heads)) return SV_ERR_UNSUPPORTED;
     const AttnPlan p = attn_plan(sh);
     if (p.grid > INT32_MAX || p.punits > INT32_MAX / 16) return SV_ERR_UNSUPPORTED;
     return SV_OK;
@@ -306,6 +322,17 @@ bool cache_ok(const sv_cache_t* c)
     if (c == nullptr || c->data == nullptr || !aligned(c->data, 16)) return false;
     return c->batch_stride >= 0 && c->head_stride >= 0 && c->position_stride >= 0 && c->batch_stride % 8 == 0 &&
            c->head_stride % 8 == 0 && c->position_stride % 8 == 0;
+}
+
+// Whether rows of `width` elements at two strides lie apart.
+bool distinct_rows(int64_t s0, int64_t n0, int64_t s1, int64_t n1, int64_t width)
+{
+    if (n0 < 2) s0 = 0;
+    if (n1 < 2) s1 = 0;
+    const bool first = n1 < 2 || (n0 > 1 && s0 < s1);  // the inner of the two
+    const int64_t si = first ? s0 : s1, ni = first ? n0 : n1, so = first ? s1 : s0, no = first ? n1 : n0;
+    if (ni > 1 && si < width) return false;
+    return no < 2 || (ni < 2 ? so >= width : so >= width && (so - width) / si >= ni - 1);
 }
 
 template <int DT, int D>
@@ -351,6 +378,8 @@ sv_status_t prefix_attention_common(const sv_attention_shape_t* sh, const void* 
     if (sh->q_row_stride < 0 || sh->q_head_stride < 0 || sh->q_row_stride % 8 != 0 || sh->q_head_stride % 8 != 0 ||
         sh->out_row_stride < 0 || sh->out_head_stride < 0 || sh->out_row_stride % 4 != 0 ||
         sh->out_head_stride % 4 != 0)
+        return SV_ERR_INVALID_ARGUMENT;
+    if (!distinct_rows(sh->out_row_stride, p.rows, sh->out_head_stride, sh->q_heads, sh->head_dim))
         return SV_ERR_INVALID_ARGUMENT;
     const sv_cache_t none{};
     const sv_cache_t *pk = &none, *pv = &none, *sk = &none, *svc = &none;

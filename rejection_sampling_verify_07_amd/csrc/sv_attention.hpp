@@ -451,28 +451,48 @@ __device__ __forceinline__ void attend_tiles(const AttnArgs& a, const KeyRange& 
         constexpr bool MASKED = decltype(masked)::value;
         const char* s_k = s_kv + buf * (2 * TA::TILE);
         const char* s_v = s_k + TA::TILE;
-        f32x4 s[SUBS][2][MT];
+        // The fragments that a group of products needs are read while the group before it runs (the barriers keep the
+        // scheduler from moving a read down to its use, which exposed the LDS latency once per product).
+        auto k_rows = [&](int i, u32x4 (&kf)[DC]) {  // 16 keys
+            const int32_t row = i * 16 + l16;
 #pragma unroll
-        for (int u = 0; u < SUBS; ++u)
+            for (int c = 0; c < DC; ++c)
+                kf[c] = *(const u32x4*)(s_k + row * TA::ROW + (((c * 4 + lg) ^ (l16 & TA::MASK)) * 16));
+        };
+        auto v_columns = [&](int u, u32x4 (&vf)[DT16]) {  // 32 keys: four (lg * 4 + l16 / 4) and 8 bytes of columns per
+                                                          // lane before the exchange
+            const int32_t vrow = u * kKeyBlock + lg * 4 + (l16 >> 2);
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt) s[u][t][mt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-                const int32_t row = u * kKeyBlock + t * 16 + l16;
-#pragma unroll
-                for (int c = 0; c < DC; ++c) {
-                    const u32x4 kf = *(const u32x4*)(s_k + row * TA::ROW + (((c * 4 + lg) ^ (l16 & TA::MASK)) * 16));
-#pragma unroll
-                    for (int mt = 0; mt < MT; ++mt) s[u][t][mt] = mfma_16x16x32<DT>(kf, qf[mt][c], s[u][t][mt]);
-                }
-                if constexpr (MASKED) {
-#pragma unroll
-                    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            if (kb + u * kKeyBlock + t * 16 + lg * 4 + i >= kr.end) s[u][t][mt][i] = neg_inf();
-                }
+            for (int d = 0; d < DT16; ++d) {
+                const int32_t at =
+                    vrow * TA::ROW + (((d * 2 + ((l16 & 3) >> 1)) ^ (vrow & TA::MASK)) * 16) + (l16 & 1) * 8;
+                const u32x2 v0 = lds_read_transposed(s_v + at), v1 = lds_read_transposed(s_v + at + 16 * TA::ROW);
+                vf[d] = u32x4{v0.x, v0.y, v1.x, v1.y};
             }
+        };
+        f32x4 s[SUBS][2][MT];
+        u32x4 kf[2][DC], vf[DT16];
+        k_rows(0, kf[0]);
+#pragma unroll
+        for (int i = 0; i < 2 * SUBS; ++i) {
+            const int u = i / 2, t = i & 1;
+            if (i + 1 < 2 * SUBS) k_rows(i + 1, kf[(i + 1) & 1]);
+            else v_columns(0, vf);
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) s[u][t][mt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int c = 0; c < DC; ++c)
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) s[u][t][mt] = mfma_16x16x32<DT>(kf[i & 1][c], qf[mt][c], s[u][t][mt]);
+            if constexpr (MASKED) {
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                    for (int i2 = 0; i2 < 4; ++i2)
+                        if (kb + u * kKeyBlock + t * 16 + lg * 4 + i2 >= kr.end) s[u][t][mt][i2] = neg_inf();
+            }
+        }
         float top[MT];
         bool over = false;
 #pragma unroll
@@ -511,17 +531,11 @@ __device__ __forceinline__ void attend_tiles(const AttnArgs& a, const KeyRange& 
 #pragma unroll
                 for (int i = 0; i < 4; ++i) pf[mt][i] = pack2<DT>(p[2 * i], p[2 * i + 1]);
             }
-            // four keys (lg * 4 + l16 / 4) and 8 bytes of columns per lane before the exchange
-            const int32_t vrow = u * kKeyBlock + lg * 4 + (l16 >> 2);
 #pragma unroll
-            for (int d = 0; d < DT16; ++d) {
-                const int32_t at =
-                    vrow * TA::ROW + (((d * 2 + ((l16 & 3) >> 1)) ^ (vrow & TA::MASK)) * 16) + (l16 & 1) * 8;
-                const u32x2 v0 = lds_read_transposed(s_v + at), v1 = lds_read_transposed(s_v + at + 16 * TA::ROW);
-                const u32x4 vf = {v0.x, v0.y, v1.x, v1.y};
+            for (int d = 0; d < DT16; ++d)
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt) o[mt][d] = mfma_16x16x32<DT>(vf, pf[mt], o[mt][d]);
-            }
+                for (int mt = 0; mt < MT; ++mt) o[mt][d] = mfma_16x16x32<DT>(vf[d], pf[mt], o[mt][d]);
+            if (u + 1 < SUBS) v_columns(u + 1, vf);
         }
     };
     int32_t kb = kr.begin;
@@ -620,10 +634,12 @@ __global__ __launch_bounds__(kAttnThreads, D == 256 ? 1 : 2) void attn_part_kern
     }
 }
 
-// Join of the parts: one wave per (row, head).  Lanes first hold one part's
-// (m, l) each, then D / 4 lanes take the columns of a part and the lane groups
-// take parts in turn.  All loads of a round are independent: the join is bound
-// by their latency.
+// Join of the parts: one wave per (row, head).  D / 4 lanes take the columns
+// of a part, so kWave / (D / 4) parts are read side by side, kJoinRounds times
+// without waiting: those loads go out before the parts' (m, l), one per lane,
+// have arrived, and before it is known which parts hold anything (a part
+// without a visible key has l = 0 and old bytes for o, which are dropped).
+constexpr int kJoinRounds = 4;
 template <int DT, int D>
 __global__ __launch_bounds__(kThreads) void attn_join_kernel(AttnArgs a)
 {
@@ -635,26 +651,35 @@ __global__ __launch_bounds__(kThreads) void attn_join_kernel(AttnArgs a)
     const int lane = lane_id(), col = (lane % LPP) * 4, sub = lane / LPP;
     const int slots = a.psplits + a.ssplits;
     const float2* ml = a.ml + i * slots;
-    float m = kNoReference;
-    float2 own = {kNoReference, 0.0f};  // this lane's part of the current 64
-    for (int s0 = 0; s0 < slots; s0 += kWave) {
-        own = s0 + lane < slots ? ml[s0 + lane] : float2{kNoReference, 0.0f};
-        m = fmaxf(m, own.x);
-    }
+    const int64_t part = n * (D * 4);  // bytes from a part to the next
+    const SV_GLOBAL char* acc = (const SV_GLOBAL char*)(a.acc + i * D + col) + sub * part;
+    f32x4 v[kJoinRounds];
+    auto bring = [&](int s0) {
+        const SV_GLOBAL char* p = acc + s0 * part;
+#pragma unroll
+        for (int r = 0; r < kJoinRounds; ++r, p += PPR * part)
+            v[r] = s0 + r * PPR + sub < slots ? *(const SV_GLOBAL f32x4*)p : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    };
+    bring(0);
+    float2 own = lane < slots ? ml[lane] : float2{kNoReference, 0.0f};  // this lane's part of the current 64
+    float m = own.x;
+    for (int s = kWave + lane; s < slots; s += kWave) m = fmaxf(m, ml[s].x);
     m = wave_max_dpp(m);
     float l = 0.0f;
     f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
     for (int s0 = 0; s0 < slots; s0 += kWave) {
-        if (slots > kWave) own = s0 + lane < slots ? ml[s0 + lane] : float2{kNoReference, 0.0f};
-        // (a part without a visible key has l = 0 and no o)
+        if (s0 > 0) own = s0 + lane < slots ? ml[s0 + lane] : float2{kNoReference, 0.0f};
         const float w = own.y > 0.0f ? __builtin_amdgcn_exp2f(own.x - m) : 0.0f;
         l += own.y * w;
-        const int count = min(slots - s0, kWave);
-#pragma unroll 4
-        for (int s = 0; s < count; s += PPR) {
-            const float f = __shfl(w, s + sub, kWave);
-            if (s + sub < count && f > 0.0f)
-                o += *(const SV_GLOBAL f32x4*)(a.acc + ((int64_t)(s0 + s + sub) * n + i) * D + col) * f;
+#pragma unroll 1
+        for (int q = 0; q < kWave && s0 + q < slots; q += kJoinRounds * PPR) {
+            if (s0 + q > 0) bring(s0 + q);
+#pragma unroll
+            for (int r = 0; r < kJoinRounds; ++r) {
+                const float f = __shfl(w, q + r * PPR + sub, kWave);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[e] += f > 0.0f ? v[r][e] * f : 0.0f;
+            }
         }
     }
 #pragma unroll

@@ -100,7 +100,7 @@ def _state_shape(B, **kw):
     return B.StateShapeT(**d)
 
 
-def _reorder(lib, sh, states=FAKE, parents=FAKE, lengths=None):
+def _reorder(lib, sh, states=FAKE, parents=1 << 30, lengths=None):
     return lib.spec_state_reorder(C.byref(sh) if sh is not None else None, states, parents, lengths, None)
 
 
@@ -121,8 +121,8 @@ def test_reorder_pointers(B, lib):
     assert _reorder(lib, None) == 1
     assert _reorder(lib, sh, states=None) == 1
     assert _reorder(lib, sh, parents=None) == 1
-    assert _reorder(lib, sh, parents=FAKE + 2) == 1
-    assert _reorder(lib, sh, lengths=FAKE + 2) == 1
+    assert _reorder(lib, sh, parents=(1 << 30) + 2) == 1
+    assert _reorder(lib, sh, lengths=(1 << 30) + 2) == 1
     # no position, no bytes: nothing to move, nothing launched
     assert _reorder(lib, _state_shape(B, positions=0), states=None) == 0
     assert _reorder(lib, _state_shape(B, row_bytes=0), states=None) == 0
@@ -212,3 +212,46 @@ def test_attention_binding_refusals(B):
         B.prefix_attention(q, c, c[:, :9], s, s)
     with pytest.raises(ValueError, match="4-D"):
         B.prefix_attention(q, c[0], c, s, s)
+
+
+# ---- overlaps and limits
+def test_reorder_refuses_an_order_among_the_states(B, lib):
+    sh = _state_shape(B)  # 16 beams in 2 slabs: 15360 bytes from the first place to the last
+    last = FAKE + 2 * 8 * 960
+    for p in (FAKE, FAKE + 4096, last - 4, FAKE - 28):
+        assert _reorder(lib, sh, parents=p) == 1, p
+        assert _reorder(lib, sh, parents=last, lengths=p) == 1, p
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(out_row_stride=1020), 1), (dict(out_head_stride=124), 1), (dict(out_row_stride=0), 1),
+    (dict(out_head_stride=0), 1), (dict(out_row_stride=128, out_head_stride=128), 1),
+    # head-major: rows inside heads
+    (dict(out_row_stride=128, out_head_stride=18 * 128 - 4), 1)])
+def test_attention_refuses_overlapping_rows_of_out(B, lib, kw, code):
+    need = _attend(B, lib, _attn_shape(B))[1]
+    assert _attend(B, lib, _attn_shape(B, **kw), ws=FAKE, have=need)[0] == code
+
+
+@pytest.mark.parametrize("kw", [dict(), dict(out_row_stride=128, out_head_stride=18 * 128),
+                                dict(out_row_stride=4096, out_head_stride=256)])
+def test_attention_takes_rows_of_out_that_lie_apart(B, lib, kw):
+    # (the too small workspace is what ends the call: its check comes last)
+    need = _attend(B, lib, _attn_shape(B))[1]
+    assert _attend(B, lib, _attn_shape(B, **kw), ws=FAKE, have=need - 1)[0] == 3
+
+
+def test_attention_position_stride_limit(B, lib):
+    need = _attend(B, lib, _attn_shape(B))[1]
+    for stride, code in ((1 << 24, 3), ((1 << 24) + 8, 2)):
+        for i in range(4):
+            c = B.CacheT(FAKE, 1024, stride, 128)
+            assert _attend(B, lib, _attn_shape(B), ws=FAKE, have=need - 1, caches={i: c})[0] == code
+
+
+def test_attention_row_limit(B, lib):
+    """max_group * (max_draft + 1) rows of a key head may be far more than the batch holds."""
+    kw = dict(groups=1, batch=1 << 20, max_group=1 << 20, max_draft=128, total_draft=0, q_heads=64, kv_heads=1,
+              cu_draft=FAKE, cu_groups=FAKE)
+    assert _attend(B, lib, _attn_shape(B, **kw))[0] == 2
+    assert _attend(B, lib, _attn_shape(B, **{**kw, "max_group": 1 << 10}))[0] == 0

@@ -207,3 +207,12 @@ def test_attention_on_another_stream_and_in_a_graph(sv):
         torch.cuda.synchronize()
         assert torch.equal(out["out"], want["out"]) and torch.equal(out["lse"], want["lse"])
     c.check(want)
+
+
+def test_attention_out_over_q(sv):
+    c, ref = run_case(sv, [40], [1] * 40, 4, 2, 64, 300, 20, "bf16")
+    q = c.q.clone()
+    got = sv.prefix_attention(q, c.pk, c.pv, c.sk, c.sv, return_lse=True,
+                              out={"out": q, "lse": torch.empty(80, 4, device=DEV)})
+    torch.cuda.synchronize()
+    assert torch.equal(got["out"], ref["out"]) and torch.equal(got["lse"], ref["lse"])

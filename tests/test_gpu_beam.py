@@ -201,3 +201,18 @@ def test_select_on_another_stream_and_in_a_graph(sv):
         want = sv.beam_select(logits, scores, W, n)
         torch.cuda.synchronize()
         assert all(torch.equal(out[k], want[k]) for k in want)
+
+
+def test_select_scores_in_place(sv):
+    """out_scores may be the scores themselves when num_select == beams."""
+    W, V = 4, 6000
+    logits = make_logits(5 * W, V, "bf16", 51)
+    scores = (-torch.rand(5 * W, generator=torch.Generator().manual_seed(6))).to(DEV)
+    scores[W:2 * W] = scores[W]  # ties: the fp64 sums read the scores again
+    logits[W + 1] = logits[W]
+    ref = check(sv, logits, scores, W, W)
+    out = {"scores": scores.view(5, W), "tokens": torch.empty(5, W, dtype=torch.int32, device=DEV),
+           "parents": torch.empty(5, W, dtype=torch.int32, device=DEV)}
+    sv.beam_select(logits, scores, W, W, out=out)
+    torch.cuda.synchronize()
+    assert all(torch.equal(out[k], ref[k]) for k in ref)
