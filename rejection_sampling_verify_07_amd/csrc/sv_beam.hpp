@@ -38,11 +38,13 @@ namespace sv {
 constexpr int kBeamMaxBeams = 64;
 constexpr int kBeamMaxSelect = 128;
 constexpr int kBeamBlockBytes = 512;  // 32 lanes' 16-byte loads
+// The pick's workgroup.  The pick is a chain of short steps, 0.5 to 1 us each, between barriers; 256 threads take longer
+// for it even where a group has few blocks (12.8 against 10.2 us for 4 beams of 50304 logits), and 512 as long.
 constexpr int kPickThreads = 1024;
 constexpr int kPickWaves = kPickThreads / kWave;
-constexpr int kPickCap = kPickThreads;  // candidate blocks, and candidate elements, held in LDS: one per thread
+constexpr int kPickCap = 1024;  // candidate blocks, and candidate elements, held in LDS
 constexpr int kPickBins = 256;   // maxima the pick's lower bound is taken from (at least kBeamMaxSelect)
-constexpr int kPickHeld = 8;     // block maxima a thread holds at a time (8192 blocks per group)
+constexpr int kPickHeld = 8;     // block maxima a thread holds at a time
 constexpr double kBeamWindow = 6.4e-6;
 static_assert(kPickBins >= kBeamMaxSelect, "the bound needs one bin per selected candidate");
 
@@ -415,7 +417,7 @@ __global__ __launch_bounds__(kPickThreads) void beam_pick_kernel(PickArgs a)
             const int32_t at = atomicAdd(&s_cnt, 1);
             if (at < kPickCap) {
                 s_bm[at] = m;
-                s_bi[at] = c.w * a.nblkp + c.r * kWave + lane;
+                s_bi[at] = (c.w << 16) | (c.r * kWave + lane);  // in the order of positions
             }
         };
         for (int32_t q0 = 0; q0 < runs; q0 += kGroupRuns) {
@@ -435,10 +437,8 @@ __global__ __launch_bounds__(kPickThreads) void beam_pick_kernel(PickArgs a)
         int32_t nblocks = min(cnt, n);
         bool overflow = cnt > kPickCap;
         if (!overflow) {
-            if (tid < cnt) {
-                const int32_t w = s_bi[tid] / a.nblkp;
-                s_bs[tid] = block_score(w, s_bi[tid] - w * a.nblkp, s_bm[tid]);
-            }
+            for (int32_t c = tid; c < cnt; c += kPickThreads)
+                s_bs[c] = block_score(s_bi[c] >> 16, s_bi[c] & 0xffff, s_bm[c]);
             __syncthreads();
             rank(s_bs, s_bi, cnt, [&](int32_t c, int32_t r) {
                 s_br[c] = r;
@@ -456,7 +456,7 @@ __global__ __launch_bounds__(kPickThreads) void beam_pick_kernel(PickArgs a)
                 double bs = ninf;
                 int32_t bi = INT32_MAX;
                 for (Run c = run_at(wave); c.q < runs; next_run(c)) {
-                    const int32_t blk = c.r * kWave + lane, i = c.w * a.nblkp + blk;
+                    const int32_t blk = c.r * kWave + lane, i = (c.w << 16) | blk;
                     const double s = block_score(c.w, blk, blkmax[c.q * kWave + lane]);
                     if (ahead(ps, pi, s, i) && ahead(s, i, bs, bi)) {
                         bs = s;
@@ -477,16 +477,33 @@ __global__ __launch_bounds__(kPickThreads) void beam_pick_kernel(PickArgs a)
         // ---- the elements of those blocks that can be among the first n
         if (!overflow || pass > 0) {
             const double elow = nblocks == n ? s_ss[n - 1] - win : ninf;
-            for (int32_t e = tid; e < nblocks * BE; e += kPickThreads) {
-                const int32_t bi = s_si[e / BE];
-                const int32_t w = bi / a.nblkp;
-                int32_t pos = 0;
-                const double s = element_score(w, bi - w * a.nblkp, e % BE, &pos);
-                if (s >= elow && s > ninf) {
+            // (fp32 scores first, with the margin of the bound above)
+            const float elowf = elow == ninf ? neg_inf() : (float)elow - 0x1p-20f * (fabsf((float)elow) + most) - 1e-30f;
+            for (int32_t e0 = tid; e0 < nblocks * BE; e0 += 4 * kPickThreads) {
+                float x[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int32_t e = e0 + j * kPickThreads;
+                    x[j] = neg_inf();
+                    if (e < nblocks * BE) {
+                        const int32_t bi = s_si[e / BE], w = bi >> 16;
+                        const int32_t v = (bi & 0xffff) * BE + e % BE - mis_of(w);
+                        if (v >= 0 && v < V && (s_end[w] == 0 || v == a.pad_token))
+                            x[j] = s_end[w] != 0 ? 0.0f : load_one<DT>(row_ptr(a.rs, row0 + w), v);
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int32_t e = e0 + j * kPickThreads;
+                    if (x[j] == neg_inf()) continue;
+                    const int32_t bi = s_si[e / BE], w = bi >> 16;
+                    if (block_score_f(w, bi & 0xffff, x[j]) < elowf) continue;
+                    const double s = s_end[w] != 0 ? s_off[w] : s_off[w] + ((double)x[j] - (double)s_top[w]) / T;
+                    if (!(s >= elow && s > ninf)) continue;
                     const int32_t at = atomicAdd(&s_ecnt, 1);
                     if (at < kPickCap) {
                         s_es[at] = s;
-                        s_ei[at] = pos;
+                        s_ei[at] = w * V + (bi & 0xffff) * BE + e % BE - mis_of(w);
                     }
                 }
             }
@@ -514,15 +531,17 @@ __global__ __launch_bounds__(kPickThreads) void beam_pick_kernel(PickArgs a)
                     if (nout == n) {
                         const double last = s_ss[n - 1];
                         const int32_t wl = s_si[n - 1] / V;
-                        if (tid < ecnt && s_er[tid] >= n && s_es[tid] >= last - win && s_ei[tid] / V != wl) {
-                            mark(wl);
-                            mark(s_ei[tid] / V);
-                        }
+                        for (int32_t c = tid; c < ecnt; c += kPickThreads)
+                            if (s_er[c] >= n && s_es[c] >= last - win && s_ei[c] / V != wl) {
+                                mark(wl);
+                                mark(s_ei[c] / V);
+                            }
                         // (a block that was not read: its largest element is outside)
-                        if (tid < cnt && s_br[tid] >= n && s_bs[tid] >= last - win && s_bi[tid] / a.nblkp != wl) {
-                            mark(wl);
-                            mark(s_bi[tid] / a.nblkp);
-                        }
+                        for (int32_t c = tid; c < cnt; c += kPickThreads)
+                            if (s_br[c] >= n && s_bs[c] >= last - win && s_bi[c] >> 16 != wl) {
+                                mark(wl);
+                                mark(s_bi[c] >> 16);
+                            }
                     }
                 }
             } else if (pass > 0) {
@@ -534,9 +553,8 @@ __global__ __launch_bounds__(kPickThreads) void beam_pick_kernel(PickArgs a)
                     int32_t bi = INT32_MAX;
                     for (int32_t e = tid; e < nblocks * BE; e += kPickThreads) {
                         const int32_t blk = s_si[e / BE];
-                        const int32_t w = blk / a.nblkp;
                         int32_t pos = 0;
-                        const double s = element_score(w, blk - w * a.nblkp, e % BE, &pos);
+                        const double s = element_score(blk >> 16, blk & 0xffff, e % BE, &pos);
                         if (s > ninf && ahead(ps, pi, s, pos) && ahead(s, pos, bs, bi)) {
                             bs = s;
                             bi = pos;
