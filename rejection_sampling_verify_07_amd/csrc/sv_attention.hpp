@@ -350,7 +350,7 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const KeyRange& kr, in
 template <int DT, int D, int MT>
 struct TileAttention {
     static constexpr int DC = D / 32, DT16 = D / 16;
-    static constexpr int KT = D == 256 ? 32 : 64;         // keys per tile
+    static constexpr int KT = 64;                         // keys per tile
     static constexpr int ROW = D * 2;                     // bytes per key row
     static constexpr int CH = ROW / 16;                   // 16-byte chunks per row
     static constexpr int MASK = CH < 16 ? CH - 1 : 15;    // swizzle
