@@ -238,8 +238,13 @@ constexpr int64_t kSplitProducts = 512;
 // 512; 17 us for 80 rows of 256 columns on 2049 positions, 28 us with 512.
 constexpr int32_t kSplitKeys = sv::kKeyRound;
 
+// Caches from which keys that one workgroup alone reads are read past the L2: 57 against 63 us on 285 MB, 48 against
+// 52 us on 201 MB; caches that stay in the 256 MB Infinity Cache from step to step lose by it (22.6 against 20.2 us
+// on 74 MB).
+constexpr double kReadPastCaches = 128e6;
+
 struct AttnPlan {
-    bool tiles;
+    bool tiles, past;
     int32_t rows, rep, mtp, mts, ptiles, stiles, psplits, ssplits;
     int64_t punits, pblocks, grid;
     size_t off_acc, off_ml, bytes;
@@ -275,6 +280,8 @@ AttnPlan attn_plan(const sv_attention_shape_t* sh)
     p.psplits = attn_splits((int64_t)sh->groups * sh->kv_heads * p.ptiles, sh->max_prefix,
                             p.ptiles == 1 ? kSplitReading : kSplitProducts);
     p.ssplits = attn_splits((int64_t)sh->batch * sh->kv_heads * p.stiles, sh->max_suffix, kSplitReading);
+    const double positions = (double)sh->groups * sh->max_prefix + (double)sh->batch * sh->max_suffix;
+    p.past = positions * sh->kv_heads * sh->head_dim * 4 > kReadPastCaches;
     p.punits = (int64_t)sh->groups * sh->kv_heads * p.psplits;
     p.pblocks = (p.punits + 7) / 8 * 8 * p.ptiles;
     p.grid = p.pblocks + (int64_t)sh->batch * sh->kv_heads * p.stiles * p.ssplits;
@@ -439,6 +446,7 @@ sv_status_t prefix_attention_common(const sv_attention_shape_t* sh, const void* 
     a.ssplits = p.ssplits;
     a.ptiles = p.ptiles;
     a.stiles = p.stiles;
+    a.past = p.past;
     a.punits = (uint32_t)p.punits;
     a.pblocks = (uint32_t)p.pblocks;
     a.acc = ws_at<float>(workspace, p.off_acc);

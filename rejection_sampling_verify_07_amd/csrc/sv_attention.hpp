@@ -58,6 +58,7 @@ struct AttnArgs {
     int32_t q_heads, kv_heads, rep;
     float c;                                                   // scale * log2(e)
     int32_t psplits, ssplits, ptiles, stiles;
+    int32_t past;              // the caches are larger than what stays in the Infinity Cache
     uint32_t punits, pblocks;  // prefix units (group, head, split), and workgroups that serve them
     float* acc;                // [slot][row][head][D]
     float2* ml;                // [row][head][slot]
@@ -104,7 +105,22 @@ struct KeyRange {
     int32_t k_pos, v_pos;   // bytes between positions
     int32_t begin, end;     // this workgroup's positions
     int32_t total;          // positions of the cache (the last row's view)
+    bool past;              // read past the caches: nothing else will read these keys
 };
+
+// Runs load(true) or load(false) as `past`, uniform over the workgroup, says.  The empty asm statements keep the
+// compiler from merging the two arms' loads, which differ in nothing but the cache policy, into plain ones.
+template <class Load>
+__device__ __forceinline__ void with_policy(bool past, Load load)
+{
+    if (past) {
+        asm volatile("");
+        load(std::true_type{});
+        asm volatile("");
+    } else {
+        load(std::false_type{});
+    }
+}
 
 // MT tiles of 16 query rows.  row0, nrows: the packed query rows of the matrix;
 // tile: which MT * 16 of its nrows * rep rows; seen_short: how many keys
@@ -154,7 +170,7 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const KeyRange& kr, in
     for (int t = 0; t < 2; ++t) koff[t] = (uint32_t)((t * 16 + l16) * kr.k_pos + lg * 16);
 #pragma unroll
     for (int j = 0; j < 8; ++j) voff[j] = (uint32_t)(((j < 4 ? 0 : 12) + lg * 4 + j) * kr.v_pos + l16 * (DPL * 2));
-    auto load_k = [&](int32_t kb, u32x4 (&kf)[2][DC], auto masked) {
+    auto load_k = [&](int32_t kb, u32x4 (&kf)[2][DC], auto masked, auto past) {
         const char* base = kr.k + (int64_t)kb * kr.k_pos;
         const int32_t last = kr.end - 1 - kb;
 #pragma unroll
@@ -162,10 +178,10 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const KeyRange& kr, in
             uint32_t off = koff[t];
             if constexpr (decltype(masked)::value) off = (uint32_t)(min(t * 16 + l16, last) * kr.k_pos + lg * 16);
 #pragma unroll
-            for (int c = 0; c < DC; ++c) kf[t][c] = *(const SV_GLOBAL u32x4*)(base + off + c * 64);
+            for (int c = 0; c < DC; ++c) kf[t][c] = load16<decltype(past)::value>((const u32x4*)(base + off + c * 64));
         }
     };
-    auto load_v = [&](int32_t kb, uint32_t (&vr)[8][VW], auto masked) {
+    auto load_v = [&](int32_t kb, uint32_t (&vr)[8][VW], auto masked, auto past) {
         const char* base = kr.v + (int64_t)kb * kr.v_pos;
         const int32_t last = kr.end - 1 - kb;
 #pragma unroll
@@ -181,7 +197,7 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const KeyRange& kr, in
             } else {
 #pragma unroll
                 for (int x = 0; x < VW / 4; ++x) {
-                    const u32x4 w = *(const SV_GLOBAL u32x4*)(p + x * 16);
+                    const u32x4 w = load16<decltype(past)::value>((const u32x4*)(p + x * 16));
 #pragma unroll
                     for (int y = 0; y < 4; ++y) vr[j][x * 4 + y] = w[y];
                 }
@@ -192,13 +208,15 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const KeyRange& kr, in
     u32x4 kf[2][DC];  // the block at hand; the next one's is loaded once the scores have taken it
     auto next_k = [&](int32_t kb) {
         if (kb >= kr.end) return;
-        if (kb + kKeyBlock <= kr.end) load_k(kb, kf, std::false_type{});
-        else load_k(kb, kf, std::true_type{});
+        with_policy(kr.past, [&](auto past) {
+            if (kb + kKeyBlock <= kr.end) load_k(kb, kf, std::false_type{}, past);
+            else load_k(kb, kf, std::true_type{}, past);
+        });
     };
     auto step = [&](int32_t kb, auto masked) {
         constexpr bool MASKED = decltype(masked)::value;
         uint32_t vr[8][VW];
-        load_v(kb, vr, masked);
+        with_policy(kr.past, [&](auto past) { load_v(kb, vr, masked, past); });
         f32x4 s[2][MT];
 #pragma unroll
         for (int t = 0; t < 2; ++t)
@@ -608,6 +626,7 @@ __global__ __launch_bounds__(kAttnThreads, D == 256 ? 1 : 2) void attn_part_kern
         const int32_t total = a.prefix_len != nullptr ? min(max(a.prefix_len[g], 0), a.max_prefix) : a.max_prefix;
         share(total, split, a.psplits, &kr.begin, &kr.end);
         kr.total = total;
+        kr.past = a.past != 0;  // (one wave's rows: no other workgroup reads these keys; attend_tiles ignores it)
         kr.k = a.pk + (int64_t)g * a.pk_group + (int64_t)hk * a.pk_head;
         kr.v = a.pv + (int64_t)g * a.pv_group + (int64_t)hk * a.pv_head;
         kr.k_pos = a.pk_pos;
@@ -626,6 +645,7 @@ __global__ __launch_bounds__(kAttnThreads, D == 256 ? 1 : 2) void attn_part_kern
         const int32_t total = a.suffix_len != nullptr ? min(max(a.suffix_len[b], 0), a.max_suffix) : a.max_suffix;
         share(total, split, a.ssplits, &kr.begin, &kr.end);
         kr.total = total;
+        kr.past = a.past != 0 && a.stiles == 1;
         kr.k = a.sk + (int64_t)b * a.sk_seq + (int64_t)hk * a.sk_head;
         kr.v = a.sv + (int64_t)b * a.sv_seq + (int64_t)hk * a.sv_head;
         kr.k_pos = a.sk_pos;
