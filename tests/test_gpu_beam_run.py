@@ -155,3 +155,33 @@ def test_scoring_rows_of_a_verify(sv):
             row += 1
     n = got["num_accepted"].cpu()
     assert bool(((n >= 0) & (n <= torch.tensor(drafts))).all())
+
+
+def test_plans_on_other_streams(sv):
+    """A plan runs on the stream that is current at the call; its tensors may go
+    away right after it, and be allocated anew, while that stream still works."""
+    g = torch.Generator().manual_seed(4)
+    logits = torch.randn(32, 20000, generator=g).to(DEV)
+    scores = -torch.rand(32, generator=g).to(DEV)
+    ref = sv.beam_select(logits, scores, 4, 8)
+    q = torch.randn(8, 4, 64, generator=g).bfloat16().to(DEV)
+    c = torch.randn(2, 900, 2, 64, generator=g).bfloat16().to(DEV)
+    s = torch.randn(8, 40, 2, 64, generator=g).bfloat16().to(DEV)
+    want = sv.prefix_attention(q, c, c, s, s)["out"]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    got = []
+    for st in streams * 3:
+        select = sv.BeamSelectPlan(logits, scores, 4, 8)
+        attn = sv.PrefixAttentionPlan(q, c, c, s, s)
+        with torch.cuda.stream(st):
+            got.append(({k: v.clone() for k, v in select().items()}, attn()["out"].clone()))
+        del select, attn
+        torch.full((1 << 20,), 7, dtype=torch.uint8, device=DEV)
+    torch.cuda.synchronize()
+    for a, b in got:
+        assert all(torch.equal(a[k], ref[k]) for k in ref) and torch.equal(b, want)
+    with pytest.raises(ValueError, match="stream is on"):
+        class Other:
+            device = torch.device("cuda:1")
+        sv.beam_select(logits, scores, 4, 8, stream=Other())
