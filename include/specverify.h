@@ -448,11 +448,12 @@ SV_API sv_status_t spec_state_reorder(const sv_state_shape_t* shape,
  *   rounded to dtype for the product with v.
  * Errors as for spec_verify_sample; SV_ERR_INVALID_ARGUMENT also for q_heads
  * no multiple of kv_heads and for rows of out that overlap; SV_ERR_UNSUPPORTED also for fp32, another head_dim,
- * more than 2^30 positions, or positions more than 32 MB apart.  Data
- * preconditions: keys and values within the lengths finite; cu_draft and
- * cu_groups prefix sums, no K_b above max_draft, no group above max_group.  Where they are
- * violated, out holds unspecified values and nothing out of bounds is read or
- * written.  out may be q itself; it may not overlap the inputs otherwise.
+ * more than 2^30 positions, or positions more than 32 MB apart.  A query, key
+ * or value that is not finite reaches only the rows that see it, where a NaN
+ * gives NaN (a value in its column alone).  Data preconditions: cu_draft and cu_groups prefix sums, no K_b above max_draft,
+ * no group above max_group.  Where they are violated, out holds unspecified
+ * values and nothing out of bounds is read or written.  out may be q itself;
+ * it may not overlap the inputs otherwise.
  */
 typedef struct {
     const void* data;

@@ -99,6 +99,16 @@ __device__ __forceinline__ uint32_t pack2(float a, float b)
     }
 }
 
+// A word's two elements, an infinity or a NaN replaced by 0.
+template <int DT>
+__device__ __forceinline__ uint32_t finite_halves(uint32_t w)
+{
+    constexpr uint32_t E = DT == DT_BF16 ? 0x7f80u : 0x7c00u;
+    const uint32_t lo = (w & E) == E ? 0u : w & 0xffffu;
+    const uint32_t hi = (w & (E << 16)) == E << 16 ? 0u : w & 0xffff0000u;
+    return lo | hi;
+}
+
 // First query row of sequence b, and the row count of a sequence; entries of
 // cu_draft outside the batch are clamped, so no row index leaves [0, rows].
 __device__ __forceinline__ int32_t first_row(const AttnArgs& a, int32_t b)
@@ -214,6 +224,7 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const KeyRange& kr, in
         }
     };
 
+    bool wild = false;  // (uniform) a masked block held a value that is not finite
     u32x4 kf[2][DC];  // the block at hand; the next one's is loaded once the scores have taken it
     auto next_k = [&](int32_t kb) {
         if (kb >= kr.end) return;
@@ -282,6 +293,24 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const KeyRange& kr, in
 #pragma unroll
             for (int i = 0; i < 4; ++i) pf[mt][i] = pack2<DT>(p[2 * i], p[2 * i + 1]);
         }
+        if constexpr (MASKED) {
+            // A value that is not finite times the weight 0 of a row that does not see it would be NaN: such values
+            // count as 0 here, and reach the rows that see them after the last block.
+            if (seen_short > 0) {
+                bool any = false;
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+#pragma unroll
+                    for (int x = 0; x < VW; ++x) any |= finite_halves<DT>(vr[j][x]) != vr[j][x];
+                if (__any(any)) {
+                    wild = true;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+#pragma unroll
+                        for (int x = 0; x < VW; ++x) vr[j][x] = finite_halves<DT>(vr[j][x]);
+                }
+            }
+        }
 #pragma unroll
         for (int d = 0; d < DPL; ++d) {
             u32x4 vf;
@@ -295,7 +324,29 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const KeyRange& kr, in
     int32_t kb = kr.begin + wave * kKeyBlock;
     next_k(kb);
     for (; kb + kKeyBlock <= whole; kb += kKeyRound) step(kb, std::false_type{});
+    const int32_t kb_masked = kb;
     for (; kb < kr.end; kb += kKeyRound) step(kb, std::true_type{});
+    if (wild) {
+#pragma unroll 1
+        for (kb = kb_masked; kb < kr.end; kb += kKeyRound)
+#pragma unroll 1
+            for (int32_t x = kb; x < min(kr.end, kb + kKeyBlock); ++x) {
+                // accumulator i of tile d holds column (4 lg + i) * DPL + d
+                const SV_GLOBAL uint32_t* row =
+                    (const SV_GLOBAL uint32_t*)(kr.v + (int64_t)x * kr.v_pos + lg * (4 * DPL * 2));
+#pragma unroll
+                for (int e = 0; e < 4 * DPL; e += 2) {
+                    const uint32_t w = row[e / 2], bad = w ^ finite_halves<DT>(w);
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        const float v = y ? hi16<DT>(bad) : lo16<DT>(bad);  // 0 where the value was finite
+#pragma unroll
+                        for (int mt = 0; mt < MT; ++mt)
+                            if (x < lim[mt]) o[mt][(e + y) % DPL][(e + y) / DPL] += v;
+                    }
+                }
+            }
+    }
 
     // ---- join the four waves: a common reference, then o summed in a fixed order
 #pragma unroll
@@ -675,7 +726,7 @@ __global__ __launch_bounds__(kAttnThreads, D == 256 ? 1 : 2) void attn_part_kern
 // of a part, so kWave / (D / 4) parts are read side by side, kJoinRounds times
 // without waiting: those loads go out before the parts' (m, l), one per lane,
 // have arrived, and before it is known which parts hold anything (a part
-// without a visible key has l = 0 and old bytes for o, which are dropped).
+// without a visible key has l = 0 and old bytes for o, which are dropped; l is NaN where a row sees a NaN).
 // 10240 (row, head) pairs of 128 columns in 7 parts: 9.6 us, 4.1 TB/s; 32 pairs
 // of 4 parts: 3.5 us, latency.
 constexpr int kJoinRounds = 4;
@@ -708,7 +759,7 @@ __global__ __launch_bounds__(kThreads) void attn_join_kernel(AttnArgs a)
     f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
     for (int s0 = 0; s0 < slots; s0 += kWave) {
         if (s0 > 0) own = s0 + lane < slots ? ml[s0 + lane] : float2{kNoReference, 0.0f};
-        const float w = own.y > 0.0f ? __builtin_amdgcn_exp2f(own.x - m) : 0.0f;
+        const float w = own.y != 0.0f ? __builtin_amdgcn_exp2f(own.x - m) : -1.0f;  // -1: nothing in this part
         l += own.y * w;
 #pragma unroll 1
         for (int q = 0; q < kWave && s0 + q < slots; q += kJoinRounds * PPR) {
@@ -717,7 +768,7 @@ __global__ __launch_bounds__(kThreads) void attn_join_kernel(AttnArgs a)
             for (int r = 0; r < kJoinRounds; ++r) {
                 const float f = __shfl(w, q + r * PPR + sub, kWave);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) o[e] += f > 0.0f ? v[r][e] * f : 0.0f;
+                for (int e = 0; e < 4; ++e) o[e] += f < 0.0f ? 0.0f : v[r][e] * f;
             }
         }
     }
@@ -730,13 +781,13 @@ __global__ __launch_bounds__(kThreads) void attn_join_kernel(AttnArgs a)
     }
     if (sub != 0) return;
     const int32_t t = (int32_t)(i / a.q_heads), h = (int32_t)(i - (int64_t)t * a.q_heads);
-    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+    const float inv = l != 0.0f ? 1.0f / l : 0.0f;
     u32x2 w;
     w.x = pack2<DT>(o.x * inv, o.y * inv);
     w.y = pack2<DT>(o.z * inv, o.w * inv);
     *(SV_GLOBAL u32x2*)(a.out + (int64_t)t * a.out_row + (int64_t)h * a.out_head + col * 2) = w;
     if (a.lse != nullptr && lane == 0)
-        a.lse[i] = l > 0.0f ? (m + __builtin_amdgcn_logf(l)) * 0.69314718055994531f : neg_inf();
+        a.lse[i] = l != 0.0f ? (m + __builtin_amdgcn_logf(l)) * 0.69314718055994531f : neg_inf();
 }
 
 }  // namespace sv

@@ -150,6 +150,46 @@ def test_attention_sharp_and_large_scores(sv):
     c.check(c.run(sv))
 
 
+@pytest.mark.parametrize("what", ["k", "v"])
+@pytest.mark.parametrize("wild", [float("nan"), float("inf"), float("-inf")])
+@pytest.mark.parametrize("dtype,D,K,S", [("bf16", 64, 3, 40), ("f16", 128, 8, 33), ("bf16", 256, 5, 300)])
+def test_attention_wild_keys_and_values_reach_only_rows_that_see_them(sv, dtype, D, K, S, wild, what):
+    """A draft token's key or value that is not finite: the rows before it have the results of the formula."""
+    c = Case([2], [K, K], 8, 2, D, 70, S, dtype, slen=[S, S - 2])
+    ref = c.run(sv)
+    torch.cuda.synchronize()
+    c.check(ref)
+    # in sequence 0, the third newest token (rows K - 2.. see it); in sequence 1 the newest (only row K does)
+    cache, col = (c.sk, slice(None)) if what == "k" else (c.sv, 5)
+    cache[0, S - 3, 1, col] = wild
+    cache[1, S - 3, 1, col] = wild
+    got = c.run(sv)
+    torch.cuda.synchronize()
+    touched = torch.zeros_like(ref["out"], dtype=torch.bool)
+    columns = slice(None) if what == "k" else slice(5, 6)
+    touched[K - 2:K + 1, 4:, columns] = True
+    touched[2 * K + 1:, 4:, columns] = True
+    assert torch.equal(got["out"][~touched], ref["out"][~touched])
+    wildest = got["out"][touched]
+    if what == "v":
+        assert not torch.isfinite(wildest).any()
+    if wild != wild:
+        assert torch.isnan(wildest).all()
+
+
+def test_attention_wild_prefix(sv):
+    """A NaN key of a prefix makes its group's rows NaN, in every split and kernel, and no other group's."""
+    for sizes, K in (([2, 2], 1), ([40, 40], 1)):
+        c = Case(sizes, [K] * sum(sizes), 4, 1, 64, 900, 10, "bf16")
+        ref = c.run(sv)
+        c.pk[1, 300] = float("nan")
+        got = c.run(sv)
+        torch.cuda.synchronize()
+        n = sizes[0] * (K + 1)
+        assert torch.equal(got["out"][:n], ref["out"][:n]) and torch.equal(got["lse"][:n], ref["lse"][:n])
+        assert torch.isnan(got["out"][n:]).all() and torch.isnan(got["lse"][n:]).all()
+
+
 def test_attention_matches_itself_across_group_shapes(sv):
     """Sequences with copies of one prefix, each in a group of its own, against one group."""
     c, ref = run_case(sv, [6], [1] * 6, 8, 2, 128, 400, 20, "bf16")
