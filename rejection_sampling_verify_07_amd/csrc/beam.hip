@@ -7,6 +7,8 @@
 #include <stdint.h>
 #include <string.h>
 
+#include <algorithm>
+
 #include "sv_common.hpp"
 #include "sv_host.hpp"
 #include "sv_beam.hpp"
@@ -277,7 +279,11 @@ AttnPlan attn_plan(const sv_attention_shape_t* sh)
     const int64_t srows = (int64_t)(sh->max_draft + 1) * p.rep;
     p.mts = srows <= 16 ? 1 : most;
     p.stiles = (int32_t)((srows + p.mts * 16 - 1) / (p.mts * 16));
-    p.psplits = attn_splits((int64_t)sh->groups * sh->kv_heads * p.ptiles, sh->max_prefix,
+    // Row tiles that hold anything, at most: ragged groups have fewer than groups * ptiles.  (2 groups of 40 with K 0..6,
+    // 2 key heads of 64, 20000 positions: 49 us against 65 us with the splits that the fullest group would need.)
+    const int64_t tiles =
+        std::min<int64_t>((int64_t)sh->groups * p.ptiles, (int64_t)p.rows * p.rep / wg_rows + sh->groups);
+    p.psplits = attn_splits(tiles * sh->kv_heads, sh->max_prefix,
                             p.ptiles == 1 ? kSplitReading : kSplitProducts);
     p.ssplits = attn_splits((int64_t)sh->batch * sh->kv_heads * p.stiles, sh->max_suffix, kSplitReading);
     const double positions = (double)sh->groups * sh->max_prefix + (double)sh->batch * sh->max_suffix;

@@ -656,10 +656,11 @@ constexpr size_t attn_lds_floats(int D, int MT)
 
 __device__ __forceinline__ int32_t div_up(int32_t x, int32_t y) { return (x + y - 1) / y; }
 
-// A share of [0, total) for split i of n, in whole rounds of the workgroup's keys.
+// A share of [0, total) for split i of n, in whole steps of `keys`.
+template <int keys>
 __device__ __forceinline__ void share(int32_t total, int32_t i, int32_t n, int32_t* begin, int32_t* end)
 {
-    const int32_t chunk = div_up(div_up(total, n), kKeyRound) * kKeyRound;
+    const int32_t chunk = div_up(div_up(total, n), keys) * keys;
     *begin = (int32_t)min((int64_t)total, (int64_t)i * chunk);
     *end = (int32_t)min((int64_t)total, (int64_t)*begin + chunk);
 }
@@ -692,7 +693,7 @@ __global__ __launch_bounds__(kAttnThreads, D == 256 ? 1 : 2) void attn_part_kern
         const int32_t row0 = first_row(a, b0), nrows = b1 > b0 ? first_row(a, b1) - row0 : 0;
         if (tile * kRowsPrefix >= nrows * a.rep) return;
         const int32_t total = a.prefix_len != nullptr ? min(max(a.prefix_len[g], 0), a.max_prefix) : a.max_prefix;
-        share(total, split, a.psplits, &kr.begin, &kr.end);
+        share<TILES ? TileAttention<DT, D, MTP>::KT : kKeyRound>(total, split, a.psplits, &kr.begin, &kr.end);
         kr.total = total;
         kr.past = a.past != 0;  // (one wave's rows: no other workgroup reads these keys; attend_tiles ignores it)
         kr.k = a.pk + (int64_t)g * a.pk_group + (int64_t)hk * a.pk_head;
@@ -711,7 +712,7 @@ __global__ __launch_bounds__(kAttnThreads, D == 256 ? 1 : 2) void attn_part_kern
         const int32_t row0 = first_row(a, b), nrows = min(first_row(a, b + 1) - row0, a.max_draft + 1);
         if (tile * (MTS * 16) >= nrows * a.rep) return;
         const int32_t total = a.suffix_len != nullptr ? min(max(a.suffix_len[b], 0), a.max_suffix) : a.max_suffix;
-        share(total, split, a.ssplits, &kr.begin, &kr.end);
+        share<kKeyRound>(total, split, a.ssplits, &kr.begin, &kr.end);
         kr.total = total;
         kr.past = a.past != 0 && a.stiles == 1;
         kr.k = a.sk + (int64_t)b * a.sk_seq + (int64_t)hk * a.sk_head;
