@@ -342,7 +342,7 @@ SV_API sv_status_t spec_token_likelihood(const sv_shape_t* shape,
  *   1 <= beams <= SV_MAX_BEAMS, 1 <= num_select <= SV_MAX_SELECT.
  * out_scores may be `scores` itself when num_select == beams; other overlaps of
  * outputs with inputs are not allowed.  Memory, execution, workspace and errors
- * as for spec_verify_sample.
+ * as for spec_verify_sample; SV_ERR_UNSUPPORTED also for more than 2^32 threads.
  */
 #define SV_MAX_BEAMS 64
 #define SV_MAX_SELECT 128
@@ -392,9 +392,10 @@ SV_API sv_status_t spec_beam_select(const sv_beam_shape_t* shape,
  * Errors: SV_ERR_INVALID_ARGUMENT (null or misaligned pointer, a count < 1,
  * positions, row_bytes or a stride < 0, places that overlap, parents or lengths
  * between the states' first and last byte),
- * SV_ERR_UNSUPPORTED (beams > SV_MAX_BEAMS, or one slab and head of a beam of
+ * SV_ERR_UNSUPPORTED (beams > SV_MAX_BEAMS, one slab and head of a beam of
  * more than 2^31 - 1 pieces, a piece being 16, 4, 2 or 1 bytes as the
- * alignment of states, row_bytes and the strides allows), SV_ERR_HIP.  Execution as for
+ * alignment of states, row_bytes and the strides allows, or more than 2^32
+ * threads of one or two pieces), SV_ERR_HIP.  Execution as for
  * spec_verify_sample; no workspace.
  */
 typedef struct {
@@ -447,13 +448,14 @@ SV_API sv_status_t spec_state_reorder(const sv_state_shape_t* shape,
  *   Sums, softmax statistics and scores are fp32; the softmax weights are
  *   rounded to dtype for the product with v.
  * Errors as for spec_verify_sample; SV_ERR_INVALID_ARGUMENT also for q_heads
- * no multiple of kv_heads and for rows of out that overlap; SV_ERR_UNSUPPORTED also for fp32, another head_dim,
- * more than 2^30 positions, or positions more than 32 MB apart.  A query, key
- * or value that is not finite reaches only the rows that see it, where a NaN
- * gives NaN (a value in its column alone).  Data preconditions: cu_draft and cu_groups prefix sums, no K_b above max_draft,
- * no group above max_group.  Where they are violated, out holds unspecified
- * values and nothing out of bounds is read or written.  out may be q itself;
- * it may not overlap the inputs otherwise.
+ * no multiple of kv_heads and for rows of out that overlap; SV_ERR_UNSUPPORTED
+ * also for fp32, another head_dim, more than 2^30 positions, positions more
+ * than 32 MB apart, or more than 2^32 threads.  A query, key or value that is
+ * not finite reaches only the rows that see it, where a NaN gives NaN (a value
+ * in its column alone).  Data preconditions: cu_draft and cu_groups prefix
+ * sums, no K_b above max_draft, no group above max_group.  Where they are
+ * violated, out holds unspecified values and nothing out of bounds is read or
+ * written.  out may be q itself; it may not overlap the inputs otherwise.
  */
 typedef struct {
     const void* data;

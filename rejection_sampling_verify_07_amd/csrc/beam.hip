@@ -30,6 +30,9 @@ int32_t dtype_of(const Shape* sh)
     return v;
 }
 
+// A launch counts its threads in 32 bits.
+bool launchable(double workgroups, int threads) { return workgroups * threads <= (double)UINT32_MAX; }
+
 // ---- beam selection
 
 // 16-byte loads per thread of the streaming pass: 29.8 us on 512 rows of 151936 bf16 logits, against 33.7 us with 2,
@@ -68,6 +71,9 @@ sv_status_t check_beam(const sv_beam_shape_t* sh, float temperature, int32_t pad
         return SV_ERR_UNSUPPORTED;
     const int64_t rows = (int64_t)sh->groups * sh->beams;
     if (rows * chunks_for(sh->vocab, vec_of(sh->dtype), 1) > INT32_MAX) return SV_ERR_UNSUPPORTED;
+    if (!launchable((double)rows * chunks_for(sh->vocab, vec_of(sh->dtype), kBeamLoads), sv::kThreads) ||
+        !launchable(sh->groups, sv::kPickThreads))
+        return SV_ERR_UNSUPPORTED;
     if ((int64_t)sh->row_stride > INT64_MAX / 8 / rows) return SV_ERR_UNSUPPORTED;
     return SV_OK;
 }
@@ -214,7 +220,7 @@ sv_status_t state_reorder_common(const sv_state_shape_t* sh, void* states, const
     const int64_t per = (int64_t)sv::kThreads * reorder_cols(sh, vecb);
     const int64_t tiles = (cols + per - 1) / per;
     const double grid = (double)tiles * sh->groups * sh->slabs * sh->heads;
-    if (grid > (double)INT32_MAX) return SV_ERR_UNSUPPORTED;
+    if (!launchable(grid, sv::kThreads)) return SV_ERR_UNSUPPORTED;
     const sv::ReorderArgs a{static_cast<char*>(states), parents, lengths, sh->beams, sh->heads, sh->positions,
                             sh->slab_stride, sh->beam_stride, sh->head_stride, sh->position_stride,
                             (uint32_t)pieces, (uint32_t)cols, (uint32_t)tiles, sh->slabs};
@@ -325,7 +331,8 @@ sv_status_t check_attention(const sv_attention_shape_t* sh, float scale)
     const int64_t per_group = sh->cu_groups != nullptr ? sh->max_group : sh->batch / sh->groups;
     if (per_group * (sh->max_draft + 1) > kMaxRows / (sh->q_heads / sh->kv_heads)) return SV_ERR_UNSUPPORTED;
     const AttnPlan p = attn_plan(sh);
-    if (p.grid > INT32_MAX || p.punits > INT32_MAX / 16) return SV_ERR_UNSUPPORTED;
+    const double join = ((double)p.rows * sh->q_heads + sv::kWaves - 1) / sv::kWaves;
+    if (!launchable((double)p.grid, sv::kAttnThreads) || !launchable(join, sv::kThreads)) return SV_ERR_UNSUPPORTED;
     return SV_OK;
 }
 

@@ -251,7 +251,23 @@ def test_attention_position_stride_limit(B, lib):
 
 def test_attention_row_limit(B, lib):
     """max_group * (max_draft + 1) rows of a key head may be far more than the batch holds."""
-    kw = dict(groups=1, batch=1 << 20, max_group=1 << 20, max_draft=128, total_draft=0, q_heads=64, kv_heads=1,
-              cu_draft=FAKE, cu_groups=FAKE)
+    kw = dict(groups=1, batch=1 << 19, max_group=1 << 19, max_draft=128, total_draft=0, q_heads=64, kv_heads=1,
+              cu_draft=FAKE, cu_groups=FAKE, max_suffix=0)
     assert _attend(B, lib, _attn_shape(B, **kw))[0] == 2
     assert _attend(B, lib, _attn_shape(B, **{**kw, "max_group": 1 << 10}))[0] == 0
+
+
+def test_launches_of_more_than_32_bits_of_threads_are_refused(B, lib):
+    """A launch counts its threads in 32 bits: 2^24 workgroups of 256 are one too many."""
+    kw = dict(beams=1, vocab=1, num_select=1, row_stride=1)
+    assert _select(lib, _beam_shape(B, groups=1 << 22, **kw))[0] == 2  # (1024 threads per group)
+    assert _select(lib, _beam_shape(B, groups=(1 << 22) - 1, **kw))[0] == 0
+    assert _select(lib, _beam_shape(B, groups=1 << 20, **{**kw, "beams": 16}))[0] == 2
+    assert _select(lib, _beam_shape(B, groups=1 << 20, **{**kw, "beams": 15}))[0] == 0
+    kw = dict(groups=1, beams=2, heads=1, positions=1, slab_stride=64, beam_stride=32)
+    assert _reorder(lib, _state_shape(B, slabs=1 << 24, **kw)) == 2
+    kw = dict(groups=1, max_draft=0, total_draft=0, max_prefix=0, head_dim=64)
+    assert _attend(B, lib, _attn_shape(B, batch=1 << 20, q_heads=64, kv_heads=1, max_suffix=0, **kw))[0] == 2
+    assert _attend(B, lib, _attn_shape(B, batch=(1 << 20) - 1, q_heads=64, kv_heads=1, max_suffix=0, **kw))[0] == 0
+    assert _attend(B, lib, _attn_shape(B, batch=1 << 24, q_heads=1, kv_heads=1, max_suffix=1, **kw))[0] == 2
+    assert _attend(B, lib, _attn_shape(B, batch=(1 << 24) - 1, q_heads=1, kv_heads=1, max_suffix=1, **kw))[0] == 0
