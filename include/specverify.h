@@ -338,7 +338,9 @@ SV_API sv_status_t spec_token_likelihood(const sv_shape_t* shape,
  *   out_scores float, out_tokens int32 and out_parents int32
  *   [groups * num_select]: the candidate's score, its token, and the beam it
  *   extends (0 .. beams - 1, within its group).  Places that no candidate
- *   fills hold -inf, -1, -1.
+ *   fills hold -inf, -1, -1.  Logits may be any finite value: a candidate whose
+ *   score lies below fp32's range (a masked token at the type's lowest value
+ *   and T < 1) keeps its place, with -inf for its score.
  *   1 <= beams <= SV_MAX_BEAMS, 1 <= num_select <= SV_MAX_SELECT.
  * out_scores may be `scores` itself when num_select == beams; other overlaps of
  * outputs with inputs are not allowed.  Memory, execution, workspace and errors

@@ -302,11 +302,14 @@ __global__ __launch_bounds__(kPickThreads) void beam_pick_kernel(PickArgs a)
         if (s_end[w] != 0) return blk == pad_block(w) ? off : ninf;
         return off + ((double)m - (double)s_top[w]) / T;
     };
+    // (fp32 may overflow where fp64 does not: only a logit of -inf is no candidate, so everything else stays finite here,
+    // and the fp64 scores decide)
     const float inv_t = 1.0f / a.temperature;
     auto block_score_f = [&](int32_t w, int32_t blk, float m) -> float {
         const BeamView v = s_view[w];
-        const float x = v.top == v.top ? (m - v.top) * inv_t : 0.0f;
-        return blk >= v.first && blk <= v.last ? v.off + x : neg_inf();
+        const bool ended = v.top != v.top;
+        const float x = ended ? 0.0f : (m - v.top) * inv_t;
+        return blk >= v.first && blk <= v.last && (ended || m > neg_inf()) ? fmaxf(v.off + x, -__FLT_MAX__) : neg_inf();
     };
     // The places of the first `count` entries (s, i) of two lists: place(entry, its place), called by one thread per
     // entry.  16 threads share an entry's comparisons.
@@ -409,7 +412,8 @@ __global__ __launch_bounds__(kPickThreads) void beam_pick_kernel(PickArgs a)
             // An fp32 score is off by less than e = 2^-21 (|score| + the largest |offset|): difference, 1 / T, product,
             // offset and sum each rounded once, (m - top) / T at most |score| + |offset|.  The n bins are at least
             // best - d in fp32 (two roundings here), so at least that less e in fp64, and a block that reaches this
-            // less the window has an fp32 score another e lower.
+            // less the window has an fp32 score another e lower.  (A bound near fp32's lowest value becomes -inf here:
+            // every block with a candidate passes.)
             const float d = __uint_as_float((cur << 18) | 0x3ffffu);
             float low = neg_inf();
             if (best != neg_inf() && d < __builtin_inff()) {

@@ -1,0 +1,45 @@
+"""spec_beam_select at scores of every size: masks of the type's lowest value,
+start scores of unused beams, scores whose fp64 steps are coarse.  Tokens and
+parents against the plain 64-bit form, bit for bit."""
+import numpy as np
+import pytest
+import torch
+
+from beam_util import DTYPES, select_ref, widen
+from test_gpu_beam import check, make_logits, sv  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+
+
+def masked(rows, V, dtype, live, seed):
+    """Rows whose logits are the type's lowest value but for `live` tokens from the middle of the row."""
+    x = torch.full((rows, V), torch.finfo(DTYPES[dtype]).min, dtype=DTYPES[dtype])
+    g = torch.Generator().manual_seed(seed)
+    at = V // 3 + torch.randint(0, V // 3, (rows, live), generator=g)
+    x.scatter_(1, at, torch.randn(rows, live, generator=g).to(DTYPES[dtype]))
+    return x.to(DEV)
+
+
+@pytest.mark.parametrize("T", [0.5, 0.75, 1.0, 1.5])
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("G,W,V,n,live", [(3, 2, 5000, 8, 1), (1, 4, 4001, 128, 3), (2, 1, 700, 64, 2)])
+def test_select_fewer_unmasked_tokens_than_places(sv, dtype, T, G, W, V, n, live):
+    """The places left go to masked tokens, lowest w * V + v first, also where (l - m) / T passes fp32's range."""
+    logits = masked(G * W, V, dtype, live, V + n)
+    scores = -torch.rand(G * W, generator=torch.Generator().manual_seed(n)) * 4
+    check(sv, logits, scores.to(DEV), W, n, T)
+
+
+def test_select_lowest_value_masks_past_the_lists(sv):
+    """More masked blocks than the pick's lists hold."""
+    logits = masked(4, 151936, "f32", 3, 1)
+    check(sv, logits, torch.tensor([-1.0, -1.5, -0.5, -4.0], device=DEV), 4, 16, 0.7)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("n", [6, 64])
+def test_select_smallest_temperature(sv, dtype, n):
+    """Every logit but the largest scores below fp32's range (f16 and bf16: with ties)."""
+    logits = make_logits(6, 3001, dtype, 13)
+    check(sv, logits, torch.tensor([-3.0, -2.0, -5.5, -0.5, -0.25, -4.0], device=DEV), 3, n, 1e-38)
