@@ -382,7 +382,7 @@ __global__ __launch_bounds__(kPickThreads) void beam_pick_kernel(PickArgs a)
             score_group(q0);
         }
         s_bin[tid] = km;
-        float most = lane < W && s_view[lane].first <= s_view[lane].last ? fabsf(s_view[lane].off) : 0.0f;
+        float most = lane < W && s_view[lane].first <= s_view[lane].last ? fmaxf(s_view[lane].off, 0.0f) : 0.0f;
         most = wave_max_dpp(most);
         __syncthreads();
         if (wave == 0) {
@@ -409,16 +409,18 @@ __global__ __launch_bounds__(kPickThreads) void beam_pick_kernel(PickArgs a)
                 for (int j = 0; j < KEYS; ++j) cnt += __popcll(__ballot(k[j] < t));
                 if (cnt < n) cur = t;
             }
-            // An fp32 score is off by less than e = 2^-21 (|score| + the largest |offset|): difference, 1 / T, product,
-            // offset and sum each rounded once, (m - top) / T at most |score| + |offset|.  The n bins are at least
-            // best - d in fp32 (two roundings here), so at least that less e in fp64, and a block that reaches this
-            // less the window has an fp32 score another e lower.  (A bound near fp32's lowest value becomes -inf here:
-            // every block with a candidate passes.)
+            // An fp32 score is off by less than 2^-21 (|score| + |offset|): difference, 1 / T, product, offset and sum each
+            // rounded once, (m - top) / T at most |score| + |offset| (a subnormal 1 / T keeps 2^-22).  No score exceeds its
+            // beam's offset, so an offset below 0 is at most |score|: e = 2^-21 (2 |score| + the largest offset above 0),
+            // and a beam at -1e9, a place not yet in use, widens no margin but its own.  The n bins are at least best - d
+            // in fp32 (two roundings here), so at least that less e in fp64, and a block that reaches this less the window
+            // has an fp32 score another e lower.  (A bound near fp32's lowest value becomes -inf here: every block with a
+            // candidate passes.)
             const float d = __uint_as_float((cur << 18) | 0x3ffffu);
             float low = neg_inf();
             if (best != neg_inf() && d < __builtin_inff()) {
                 const float bound = best - d;
-                low = bound - 0x1p-21f * (3.0f * fabsf(bound) + 3.0f * most + fabsf(best)) - 1e-30f -
+                low = bound - 0x1p-20f * (3.0f * fabsf(bound) + 2.0f * most + fabsf(best)) - 1e-30f -
                       (float)(win * 1.01);
             }
             if (lane == 0) s_bound = low;
@@ -492,7 +494,7 @@ __global__ __launch_bounds__(kPickThreads) void beam_pick_kernel(PickArgs a)
             const double elow = nblocks == n ? s_ss[n - 1] - win : ninf;
             // (fp32 scores first, with the margin of the bound above)
             const float elowf =
-                elow == ninf ? neg_inf() : (float)elow - 0x1p-20f * (fabsf((float)elow) + most) - 1e-30f;
+                elow == ninf ? neg_inf() : (float)elow - 0x1p-20f * (2.0f * fabsf((float)elow) + most) - 1e-30f;
             for (int32_t e0 = tid; e0 < nblocks * BE; e0 += 4 * kPickThreads) {
                 float x[4];
 #pragma unroll

@@ -43,3 +43,36 @@ def test_select_smallest_temperature(sv, dtype, n):
     """Every logit but the largest scores below fp32's range (f16 and bf16: with ties)."""
     logits = make_logits(6, 3001, dtype, 13)
     check(sv, logits, torch.tensor([-3.0, -2.0, -5.5, -0.5, -0.25, -4.0], device=DEV), 3, n, 1e-38)
+
+
+@pytest.mark.parametrize("start", [-1e9, -3e38, -1e4])
+@pytest.mark.parametrize("dtype,V", [("f32", 151936), ("bf16", 50304)])
+def test_select_start_scores(sv, dtype, V, start):
+    """The first step of a search: one beam in use, the others at a score that no candidate reaches."""
+    logits = make_logits(2 * 8, V, dtype, 17)
+    scores = torch.full((2, 8), start, device=DEV)
+    scores[0, 0], scores[1, 3] = 0.0, -1.0
+    check(sv, logits, scores.view(-1), 8, 16)
+
+
+def test_select_start_scores_cost_no_more_than_others(sv):
+    """The unused beams' scores leave the filters of the beam in use alone: a call with them takes the time of any
+    other (it took several times that when a group shared one error margin)."""
+    logits = make_logits(8, 151936, "f32", 19)
+
+    def us(scores):
+        plan = sv.BeamSelectPlan(logits, torch.tensor(scores, device=DEV), 8, 16)
+        times = []
+        for _ in range(9):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            for _ in range(10):
+                plan()
+            b.record()
+            torch.cuda.synchronize()
+            times.append(a.elapsed_time(b) * 100)
+        return min(times)
+
+    usual, start = us([-0.3 * i for i in range(8)]), us([0.0] + [-1e9] * 7)
+    print(f"select: usual scores {usual:.1f} us, start scores {start:.1f} us", flush=True)
+    assert start < 2 * usual
