@@ -29,7 +29,8 @@
 // (7 * 2^-24), everything after that in fp64.  The mean of x under the softmax
 // is at most ln V <= 13.9, so lse_w is off by at most
 // (3 * 13.9 + 9) 2^-24 < 3.1e-6.  Two candidates of different beams whose
-// scores lie within twice that (kBeamWindow) are not decided by these sums:
+// scores lie within twice that (kBeamWindow) and a few of the scores' own fp64
+// steps are not decided by these sums:
 // the pick then recomputes the log sums concerned in fp64 from the rows and
 // selects again, so the order is always the fp64 scores' order.  A group that
 // needs it takes 32 us more per beam of 151936 logits; on random logits that is
@@ -491,7 +492,12 @@ __global__ __launch_bounds__(kPickThreads) void beam_pick_kernel(PickArgs a)
         }
         // ---- the elements of those blocks that can be among the first n
         if (!overflow || pass > 0) {
-            const double elow = nblocks == n ? s_ss[n - 1] - win : ninf;
+            // What may lie ahead of a score: the window, and what the fp64 roundings of two offsets and two scores make of
+            // an offset that the window holds, half a step each (|offset| as in e above).
+            auto reach = [&](double s) {
+                return pass == 0 ? s - (kBeamWindow + 0x1p-50 * (2.0 * fabs(s) + (double)most)) : s;
+            };
+            const double elow = nblocks == n ? reach(s_ss[n - 1]) : ninf;
             // (fp32 scores first, with the margin of the bound above)
             const float elowf =
                 elow == ninf ? neg_inf() : (float)elow - 0x1p-20f * (2.0f * fabsf((float)elow) + most) - 1e-30f;
@@ -539,22 +545,22 @@ __global__ __launch_bounds__(kPickThreads) void beam_pick_kernel(PickArgs a)
                     // candidates of different beams closer than the window, in the list or just outside it
                     if (tid + 1 < nout) {
                         const int32_t w0 = s_si[tid] / V, w1 = s_si[tid + 1] / V;
-                        if (w0 != w1 && s_ss[tid] - s_ss[tid + 1] <= win) {
+                        if (w0 != w1 && s_ss[tid + 1] >= reach(s_ss[tid])) {
                             mark(w0);
                             mark(w1);
                         }
                     }
                     if (nout == n) {
-                        const double last = s_ss[n - 1];
+                        const double edge = reach(s_ss[n - 1]);
                         const int32_t wl = s_si[n - 1] / V;
                         for (int32_t c = tid; c < ecnt; c += kPickThreads)
-                            if (s_er[c] >= n && s_es[c] >= last - win && s_ei[c] / V != wl) {
+                            if (s_er[c] >= n && s_es[c] >= edge && s_ei[c] / V != wl) {
                                 mark(wl);
                                 mark(s_ei[c] / V);
                             }
                         // (a block that was not read: its largest element is outside)
                         for (int32_t c = tid; c < cnt; c += kPickThreads)
-                            if (s_br[c] >= n && s_bs[c] >= last - win && s_bi[c] >> 16 != wl) {
+                            if (s_br[c] >= n && s_bs[c] >= edge && s_bi[c] >> 16 != wl) {
                                 mark(wl);
                                 mark(s_bi[c] >> 16);
                             }

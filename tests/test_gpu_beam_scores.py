@@ -76,3 +76,19 @@ def test_select_start_scores_cost_no_more_than_others(sv):
     usual, start = us([-0.3 * i for i in range(8)]), us([0.0] + [-1e9] * 7)
     print(f"select: usual scores {usual:.1f} us, start scores {start:.1f} us", flush=True)
     assert start < 2 * usual
+
+
+def test_select_scores_of_coarse_steps(sv):
+    """Scores around -4e10, whose fp64 steps (7.6e-6) are coarser than the window of the near ties.  A group's second
+    beam holds the first one's logits in another order: the exact scores tie in pairs, while the two beams' fp32 sums
+    differ and may put their scores one step apart."""
+    G, V, n = 32768, 300, 4
+    g = torch.Generator().manual_seed(23)
+    x = torch.randn(G, V, generator=g) * 1.5
+    logits = torch.stack([x, x[:, torch.randperm(V, generator=g)]], 1).view(2 * G, V).to(DEV)
+    scores = (-4e10 - 1e9 * torch.rand(G, 1, generator=g)).repeat(1, 2).view(-1).to(DEV)
+    out = sv.beam_select(logits, scores, 2, n)
+    torch.cuda.synchronize()
+    _, rt, rp = select_ref(widen(logits), widen(scores), 2, n)
+    wrong = (out["tokens"].cpu().numpy() != rt).any(1) | (out["parents"].cpu().numpy() != rp).any(1)
+    assert not wrong.any(), f"{wrong.sum()} of {G} groups: {np.argwhere(wrong)[:5].ravel()}"
