@@ -18,11 +18,12 @@
 // operand of O^T = V^T P^T once both use the key order {4g..4g+3, 16+4g..+3}
 // of lane group g.  V is read in rows, 16 lanes over the D columns, and
 // pairs of keys are interleaved in registers; neither K, V nor P passes through LDS.
-// The reference m moves only when a score exceeds it by 8 (in log2): then p is
-// at most 2^8, and the accumulators are rescaled rarely.
+// The reference m moves only when a score exceeds it by some powers of 2
+// (Reference), so the accumulators are rescaled rarely.
 //
 // P is rounded to the element type for the second product, which takes no
-// other: at most half a step, 2^-8 (bf16) or 2^-11 (fp16) of each weight, and
+// other: at most half a step, 2^-8 (bf16) or 2^-11 (fp16) of each weight (fp16
+// weights below 2^-24 of the row's largest in a part: 2^-35 of that one), and
 // the weights' errors are independent, so the sum's is about that of rounding
 // out itself at the end (both together: 1.35 times the error of out's rounding
 // alone, measured).  The sum l takes the unrounded weights; scores,
@@ -51,7 +52,14 @@ constexpr int kAttnThreads = kAttnWaves * kWave;
 constexpr int kKeyBlock = 32;                            // keys per wave and step
 constexpr int kKeyRound = kAttnWaves * kKeyBlock;        // keys per workgroup and step
 constexpr float kNoReference = -1e30f;                   // m of a part without a visible key
-constexpr float kReferenceSlack = 8.0f;
+// The reference is set kBelow under a row's largest score and moves when a score exceeds it by kSlack more (in log2).
+// fp16 weights use the type's range: they reach 2^15, and those down to 2^-24 of the row's largest are normal numbers
+// (at 2^0 to 2^8, half of a weight 17 nats below a sink was lost); bf16 has fp32's range.
+template <int DT>
+struct Reference {
+    static constexpr float kBelow = DT == DT_F16 ? 10.0f : 0.0f;
+    static constexpr float kSlack = DT == DT_F16 ? 5.0f : 8.0f;
+};
 
 struct AttnArgs {
     const char *q, *pk, *pv, *sk, *sv;
@@ -265,7 +273,7 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const KeyRange& kr, in
 #pragma unroll
             for (int i = 2; i < 8; ++i) x = fmaxf(x, s[i / 4][mt][i & 3]);
             top[mt] = x * a.c;
-            over |= top[mt] > m[mt] + kReferenceSlack;
+            over |= top[mt] > m[mt] + (Reference<DT>::kBelow + Reference<DT>::kSlack);
         }
         if (__any(over)) {
 #pragma unroll
@@ -273,7 +281,7 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const KeyRange& kr, in
                 float x = top[mt];
                 x = fmaxf(x, __shfl_xor(x, 16, kWave));
                 x = fmaxf(x, __shfl_xor(x, 32, kWave));
-                x = fmaxf(x, m[mt]);
+                x = fmaxf(x - Reference<DT>::kBelow, m[mt]);
                 const float f = __builtin_amdgcn_exp2f(m[mt] - x);
                 m[mt] = x;
                 l[mt] *= f;
@@ -589,7 +597,7 @@ __device__ __forceinline__ void attend_tiles(const AttnArgs& a, const KeyRange& 
 #pragma unroll
             for (int i = 1; i < 8 * SUBS; ++i) x = fmaxf(x, s[i / 8][(i / 4) & 1][mt][i & 3]);
             top[mt] = x * a.c;
-            over |= top[mt] > m[mt] + kReferenceSlack;
+            over |= top[mt] > m[mt] + (Reference<DT>::kBelow + Reference<DT>::kSlack);
         }
         if (__any(over)) {
 #pragma unroll
@@ -597,7 +605,7 @@ __device__ __forceinline__ void attend_tiles(const AttnArgs& a, const KeyRange& 
                 float x = top[mt];
                 x = fmaxf(x, __shfl_xor(x, 16, kWave));
                 x = fmaxf(x, __shfl_xor(x, 32, kWave));
-                x = fmaxf(x, m[mt]);
+                x = fmaxf(x - Reference<DT>::kBelow, m[mt]);
                 const float f = __builtin_amdgcn_exp2f(m[mt] - x);
                 m[mt] = x;
                 l[mt] *= f;

@@ -1,0 +1,44 @@
+"""spec_prefix_attention at the edges of its types' ranges: weights far below a
+row's largest, scores far below zero, infinite values next to a cache's end."""
+import numpy as np
+import pytest
+import torch
+
+from beam_util import DTYPES, attention_ref, widen
+from test_gpu_attention import Case, sv  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+# (sizes, K, Hq, Hk): single rows that walk keys wave by wave, and rows past one wave that share tiles
+FEW, MANY = ([4], 0, 4, 2), ([10], 1, 8, 2)
+
+
+@pytest.mark.parametrize("gap", [9.0, 12.0, 15.0, 16.5, 18.0])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("sizes,K,Hq,Hk", [FEW, MANY])
+def test_attention_sink_keys_of_no_value(sv, sizes, K, Hq, Hk, dtype, D, gap):
+    """Keys that take nearly all of a row's weight and hold zeros, `gap` above all others: out is what is left of the
+    others, each of which has a weight of e^-gap.  In every run of 32 keys, so that no split or wave is without one."""
+    P = 2048
+    c = Case(sizes, [K] * sum(sizes), Hq, Hk, D, P, K + 1, dtype, seed=int(10 * gap) + D)
+    dt = DTYPES[dtype]
+    # score = scale * q . k = k[0] + noise of spread 0.1
+    c.q = torch.cat([torch.full_like(c.q[..., :1], D ** 0.5), c.q[..., 1:].float() * 0.05], -1).to(dt)
+    for k, v in ((c.pk, c.pv), (c.sk, c.sv)):
+        k[..., 0] = -gap
+        v.copy_((512 + 64 * v.float()).to(dt))
+    c.pk[:, ::32, :, 0], c.pv[:, ::32] = 0.0, 0.0
+    c.sk[:, ::32, :, 0], c.sv[:, ::32] = 0.0, 0.0
+    got = c.run(sv)
+    torch.cuda.synchronize()
+    # A weight is rounded where its row's largest is 2^10 at least (f16), half a step of the smallest being 2^-25;
+    # outputs are far above the smallest step.
+    tiny = 2.0 ** -35 if dtype == "f16" else 0.0
+    out, lse, b_out, b_lse = attention_ref(
+        *(widen(x) for x in (c.q, c.pk, c.pv, c.sk, c.sv)), c.plen, c.slen, c.drafts, c.groups,
+        float(np.float32(c.scale)), torch.finfo(dt).eps, tiny)
+    assert np.abs(out).min() > 2.0 ** -14
+    err = np.abs(widen(got["out"]) - out)
+    assert (err <= b_out).all(), (err.max(), (err / np.abs(out)).max())
+    assert (np.abs(widen(got["lse"]) - lse) <= b_lse).all()
