@@ -51,7 +51,7 @@ constexpr int kAttnWaves = 4;
 constexpr int kAttnThreads = kAttnWaves * kWave;
 constexpr int kKeyBlock = 32;                            // keys per wave and step
 constexpr int kKeyRound = kAttnWaves * kKeyBlock;        // keys per workgroup and step
-constexpr float kNoReference = -1e30f;                   // m of a part without a visible key
+constexpr float kNoReference = -__FLT_MAX__;             // m of a part without a visible key
 // The reference is set kBelow under a row's largest score and moves when a score exceeds it by kSlack more (in log2).
 // fp16 weights use the type's range: they reach 2^15, and those down to 2^-24 of the row's largest are normal numbers
 // (at 2^0 to 2^8, half of a weight 17 nats below a sink was lost); bf16 has fp32's range.
@@ -80,6 +80,24 @@ struct AttnArgs {
     float* acc;                // [slot][row][head][D]
     float2* ml;                // [row][head][slot]
 };
+
+// A score's distance from its reference is fma(s, c, -m): the exact product less the rounded m.  What m lost is common
+// to the row and cancels, but beyond 2^22 (|m| 2^-24 > 1/4) it would carry the weights out of their type's range; from
+// there on the product is rounded first, as m was.
+constexpr float kFarReference = 4194304.0f;
+template <int MT>
+__device__ __forceinline__ bool far_references(const float (&m)[MT])
+{
+    bool far = false;
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) far |= fabsf(m[mt]) > kFarReference && m[mt] != kNoReference;
+    return __any(far);
+}
+__device__ __forceinline__ float far_distance(float s, float c, float m)
+{
+#pragma clang fp contract(off)
+    return s * c - m;
+}
 
 template <int DT>
 __device__ __forceinline__ f32x4 mfma_16x16x32(u32x4 a, u32x4 b, f32x4 c)
@@ -233,6 +251,7 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const KeyRange& kr, in
     };
 
     bool wild = false;  // (uniform) a masked block held a value that is not finite
+    bool far = false;   // (uniform) a reference lies beyond kFarReference
     u32x4 kf[2][DC];  // the block at hand; the next one's is loaded once the scores have taken it
     auto next_k = [&](int32_t kb) {
         if (kb >= kr.end) return;
@@ -288,14 +307,23 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const KeyRange& kr, in
 #pragma unroll
                 for (int d = 0; d < DPL; ++d) o[mt][d] *= f;
             }
+            far = far_references<MT>(m);
         }
+        if (__builtin_expect(far, 0)) {
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) s[i / 4][mt][i & 3] = far_distance(s[i / 4][mt][i & 3], a.c, m[mt]);
+        }
+        const float c = far ? 1.0f : a.c;
         u32x4 pf[MT];
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
+            const float ref = far ? 0.0f : m[mt];
             float p[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i / 4][mt][i & 3], a.c, -m[mt]));
+                p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i / 4][mt][i & 3], c, -ref));
                 l[mt] += p[i];
             }
 #pragma unroll
@@ -542,6 +570,7 @@ __device__ __forceinline__ void attend_tiles(const AttnArgs& a, const KeyRange& 
     }
     __syncthreads();
     int buf = 0;
+    bool far = false;  // (uniform over the wave) a reference lies beyond kFarReference
     // one tile; MASKED: the range ends inside it
     auto use = [&](int32_t kb, auto masked) {
         constexpr bool MASKED = decltype(masked)::value;
@@ -612,16 +641,28 @@ __device__ __forceinline__ void attend_tiles(const AttnArgs& a, const KeyRange& 
 #pragma unroll
                 for (int d = 0; d < DT16; ++d) o[mt][d] *= f;
             }
+            far = far_references<MT>(m);
         }
+        if (__builtin_expect(far, 0)) {
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int i = 0; i < 8 * SUBS; ++i) {
+                    f32x4& x = s[i / 8][(i / 4) & 1][mt];
+                    x[i & 3] = far_distance(x[i & 3], a.c, m[mt]);
+                }
+        }
+        const float c = far ? 1.0f : a.c;
 #pragma unroll
         for (int u = 0; u < SUBS; ++u) {
             u32x4 pf[MT];
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
+                const float ref = far ? 0.0f : m[mt];
                 float p[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[u][i / 4][mt][i & 3], a.c, -m[mt]));
+                    p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[u][i / 4][mt][i & 3], c, -ref));
                     l[mt] += p[i];
                 }
 #pragma unroll
@@ -684,7 +725,11 @@ __global__ __launch_bounds__(kAttnThreads, D == 256 ? 1 : 2) void attn_part_kern
     constexpr size_t kLdsPrefix = TILES ? TileAttention<DT, D, MTP>::LDS : attn_lds_floats(D, MTP) * 4;
     constexpr size_t kLdsSuffix = attn_lds_floats(D, MTS) * 4;
     constexpr int kRowsPrefix = TILES ? TileAttention<DT, D, MTP>::ROWS : MTP * 16;
-    __shared__ __align__(16) char s_mem[kLdsPrefix > kLdsSuffix ? kLdsPrefix : kLdsSuffix];
+    constexpr size_t kLds = kLdsPrefix > kLdsSuffix ? kLdsPrefix : kLdsSuffix;
+    // The splits of tiled work count on two workgroups per CU: more than a third of the 160 KB keeps a third one out where
+    // the registers would hold it (58 against 48 us on 2 groups of 40 with K 0..6, 2 key heads of 64, 20000 positions).
+    constexpr size_t kLdsOfTwo = 56 * 1024;
+    __shared__ __align__(16) char s_mem[TILES && kLds < kLdsOfTwo ? kLdsOfTwo : kLds];
     KeyRange kr;
     if (blockIdx.x < a.pblocks) {
         // the tiles of one unit (the same keys) run on one XCD (workgroups go to the 8 XCDs in turn)

@@ -42,3 +42,41 @@ def test_attention_sink_keys_of_no_value(sv, sizes, K, Hq, Hk, dtype, D, gap):
     err = np.abs(widen(got["out"]) - out)
     assert (err <= b_out).all(), (err.max(), (err / np.abs(out)).max())
     assert (np.abs(widen(got["lse"]) - lse) <= b_lse).all()
+
+
+@pytest.mark.parametrize("power", [20, 56])
+@pytest.mark.parametrize("sign", [-1, 1])
+@pytest.mark.parametrize("P", [1, 300])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("sizes,K,Hq,Hk", [FEW, MANY])
+def test_attention_scores_far_from_zero(sv, sizes, K, Hq, Hk, D, P, sign, power):
+    """Every score at +-2^40 or +-2^112 and more: copies of one key, so that all weights are equal."""
+    c = Case(sizes, [K] * sum(sizes), Hq, Hk, D, P, 0, "bf16")
+    c.q.fill_(1.25 * 2.0 ** power)
+    c.pk.fill_(sign * 1.375 * 2.0 ** power)
+    score = sign * 1.25 * 1.375 * 2.0 ** (2 * power) * D * float(np.float32(c.scale))
+    got = c.run(sv)
+    torch.cuda.synchronize()
+    v = widen(c.pv)[0].repeat(Hq // Hk, axis=1)  # [P, Hq, D]
+    # equal weights (one power of 2, and an exact sum of them): P terms added in fp32, a reciprocal, a product and the
+    # rounding of out
+    want = np.broadcast_to(v.mean(0), got["out"].shape)
+    bound = (2.0 ** -8 * np.abs(want) + (P + 4) * 2.0 ** -24 * np.abs(v).mean(0)) * 1.01
+    assert (np.abs(widen(got["out"]) - want) <= bound).all()
+    # log2(e) scale, its product with the score, the sum with log2(l), ln 2 and its product: rounded once each
+    assert np.abs(widen(got["lse"]) / score - 1).max() <= 5 * 2.0 ** -24
+
+
+@pytest.mark.parametrize("sizes,K,Hq,Hk", [FEW, MANY])
+@pytest.mark.parametrize("dtype,power", [("bf16", 20), ("f16", 14)])
+def test_attention_far_scores_choose_one_key(sv, sizes, K, Hq, Hk, dtype, power):
+    """Scores of 2^30 and more that grow key by key: all weight is the last key's (or the first one's)."""
+    c = Case(sizes, [K] * sum(sizes), Hq, Hk, 64, 200, 0, dtype)
+    c.q.fill_(2.0 ** power)
+    grow = torch.arange(1, 201, device=DEV).view(1, 200, 1, 1).expand_as(c.pk)
+    for sign, at in ((1, 199), (-1, 0)):
+        c.pk.copy_(sign * 2.0 ** (power - 7) * grow)
+        got = c.run(sv)
+        torch.cuda.synchronize()
+        want = c.pv[0, at].repeat_interleave(Hq // Hk, 0).expand_as(got["out"])
+        assert torch.equal(got["out"], want), (sign, got["out"][0, 0, :4], want[0, 0, :4])
