@@ -454,7 +454,8 @@ SV_API sv_status_t spec_state_reorder(const sv_state_shape_t* shape,
  * also for fp32, another head_dim, more than 2^30 positions, positions more
  * than 32 MB apart, or more than 2^32 threads.  A query, key or value that is
  * not finite reaches only the rows that see it, where a NaN gives NaN (a value
- * in its column alone).  Data preconditions: cu_draft and cu_groups prefix
+ * in its column alone) and an infinite value itself, or NaN under a weight that
+ * dtype rounds to 0.  Data preconditions: cu_draft and cu_groups prefix
  * sums, no K_b above max_draft, no group above max_group.  Where they are
  * violated, out holds unspecified values and nothing out of bounds is read or
  * written.  out may be q itself; it may not overlap the inputs otherwise.

@@ -208,8 +208,8 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const KeyRange& kr, in
     }
 
     // a lane's keys inside a block: K rows l16 and 16 + l16; V rows 4 lg + j and 16 + 4 lg + j.
-    // Offsets of a whole block are kept; a block that the range ends in takes the last key for those past it
-    // (finite, and masked below).
+    // Offsets of a whole block are kept; a block that the range ends in takes the last key for those past it (masked
+    // below).
     uint32_t koff[2], voff[8];
 #pragma unroll
     for (int t = 0; t < 2; ++t) koff[t] = (uint32_t)((t * 16 + l16) * kr.k_pos + lg * 16);
@@ -330,6 +330,12 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const KeyRange& kr, in
             for (int i = 0; i < 4; ++i) pf[mt][i] = pack2<DT>(p[2 * i], p[2 * i + 1]);
         }
         if constexpr (MASKED) {
+            // the last key's value may be infinite: none for keys past the range
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+#pragma unroll
+                for (int x = 0; x < VW; ++x)
+                    vr[j][x] = kb + (j < 4 ? 0 : 12) + lg * 4 + j < kr.end ? vr[j][x] : 0u;
             // A value that is not finite times the weight 0 of a row that does not see it would be NaN: such values
             // count as 0 here, and reach the rows that see them after the last block.
             if (seen_short > 0) {
@@ -542,7 +548,7 @@ __device__ __forceinline__ void attend_tiles(const AttnArgs& a, const KeyRange& 
                 kreg[i] = *(const SV_GLOBAL u32x4*)(kbase + koff[i]);
                 vreg[i] = *(const SV_GLOBAL u32x4*)(vbase + voff[i]);
             }
-        } else {  // the range ends in this tile: the last key (finite) in place of those past it, masked below
+        } else {  // the range ends in this tile: the last key in place of those past it, masked below
 #pragma unroll
             for (int i = 0; i < TA::LOADS; ++i) {
                 const int32_t x = i * kAttnThreads + (int32_t)threadIdx.x;
@@ -552,8 +558,13 @@ __device__ __forceinline__ void attend_tiles(const AttnArgs& a, const KeyRange& 
             }
         }
     };
-    auto keep = [&](int buf) {
+    auto keep = [&](int buf, int32_t kb) {
         char* dst = s_kv + buf * (2 * TA::TILE);
+        if (kb + KT > kr.end) {  // the last key's value may be infinite: none for keys past the range
+#pragma unroll
+            for (int i = 0; i < TA::LOADS; ++i)
+                if (kb + (i * kAttnThreads + (int32_t)threadIdx.x) / TA::CH >= kr.end) vreg[i] = u32x4{0u, 0u, 0u, 0u};
+        }
 #pragma unroll
         for (int i = 0; i < TA::LOADS; ++i) {
             const int32_t x = i * kAttnThreads + (int32_t)threadIdx.x;
@@ -566,7 +577,7 @@ __device__ __forceinline__ void attend_tiles(const AttnArgs& a, const KeyRange& 
 
     if (kr.begin < kr.end) {
         fetch(kr.begin);
-        keep(0);
+        keep(0, kr.begin);
     }
     __syncthreads();
     int buf = 0;
@@ -679,7 +690,7 @@ __device__ __forceinline__ void attend_tiles(const AttnArgs& a, const KeyRange& 
     for (; kb + KT < kr.end; kb += KT, buf ^= 1) {
         fetch(kb + KT);
         if (!idle) use(kb, std::false_type{});
-        keep(buf ^ 1);
+        keep(buf ^ 1, kb + KT);
         __syncthreads();
     }
     if (kb < kr.end && !idle) use(kb, std::true_type{});

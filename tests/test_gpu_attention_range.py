@@ -80,3 +80,33 @@ def test_attention_far_scores_choose_one_key(sv, sizes, K, Hq, Hk, dtype, power)
         torch.cuda.synchronize()
         want = c.pv[0, at].repeat_interleave(Hq // Hk, 0).expand_as(got["out"])
         assert torch.equal(got["out"], want), (sign, got["out"][0, 0, :4], want[0, 0, :4])
+
+
+@pytest.mark.parametrize("wild", [float("inf"), float("-inf")])
+@pytest.mark.parametrize("P", [1, 70, 321])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("sizes,K,Hq,Hk", [FEW, MANY])
+def test_attention_infinite_value_of_the_last_position(sv, sizes, K, Hq, Hk, D, P, wild):
+    """The last position in use ends inside a block of keys: its infinite value is every row's, in its column alone."""
+    c = Case(sizes, [K] * sum(sizes), Hq, Hk, D, P + 9, 0, "bf16", plen=[P])
+    ref = c.run(sv)
+    c.pv[0, P - 1, 1, 5] = wild
+    got = c.run(sv)
+    torch.cuda.synchronize()
+    heads = slice(Hq // Hk, None)
+    assert (got["out"][:, heads, 5] == wild).all(), got["out"][:2, :, 5]
+    got["out"][:, heads, 5] = ref["out"][:, heads, 5]
+    assert torch.equal(got["out"], ref["out"]) and torch.equal(got["lse"], ref["lse"])
+
+
+def test_attention_infinite_value_of_the_newest_row(sv):
+    """The same in the suffix of a plain decode step."""
+    c = Case([3], [0] * 3, 4, 2, 64, 40, 9, "f16", slen=[9, 1, 5])
+    ref = c.run(sv)
+    for b in range(3):
+        c.sv[b, c.slen[b] - 1, 0, 7] = float("inf")
+    got = c.run(sv)
+    torch.cuda.synchronize()
+    assert (got["out"][:, :2, 7] == float("inf")).all()
+    got["out"][:, :2, 7] = ref["out"][:, :2, 7]
+    assert torch.equal(got["out"], ref["out"])
