@@ -46,8 +46,8 @@ class AttentionShapeT(C.Structure):
 
 
 def _on(dev, stream):
-    """A context whose allocations on `dev` belong to `stream` (default: the
-    device's current one)."""
+    """A context whose work and allocations on `dev` belong to `stream`
+    (default: the device's current one)."""
     if stream is None:
         return contextlib.nullcontext()
     if stream.device != dev:
@@ -317,10 +317,11 @@ class PrefixAttentionPlan(_DevicePlan):
         vectors = [None if t is None else _vector(t, n, c, torch.int32, dev) for n, t, c in (
             ("cu_draft", cu_draft, batch + 1), ("cu_groups", cu_groups, groups + 1),
             ("prefix_lengths", prefix_lengths, groups), ("suffix_lengths", suffix_lengths, batch))]
-        if max_draft is None:
-            max_draft = int((cu_draft[1:] - cu_draft[:-1]).max().item())
-        if cu_groups is not None and max_group is None:
-            max_group = int((cu_groups[1:] - cu_groups[:-1]).max().item())
+        with _on(dev, stream):  # (read back on the call's stream: work queued there may still write them)
+            if max_draft is None:
+                max_draft = int((cu_draft[1:] - cu_draft[:-1]).max().item())
+            if cu_groups is not None and max_group is None:
+                max_group = int((cu_groups[1:] - cu_groups[:-1]).max().item())
         lse = None
         with _on(dev, stream):
             if out is None:
@@ -365,8 +366,8 @@ def prefix_attention(q: torch.Tensor, prefix_k: torch.Tensor, prefix_v: torch.Te
     positions, kv_heads, D], the newest rows' keys and values written; lengths
     int32, the positions in use (None: all).  cu_draft int32 [batch + 1] or None
     (uniform K); cu_groups int32 [groups + 1], the groups' first sequences, or
-    None (equal groups).  max_draft and max_group are read back from the device
-    where they are needed and not given.  scale defaults to D ** -0.5.
+    None (equal groups).  max_draft and max_group are read back from the device,
+    on the call's stream, where they are needed and not given.  scale defaults to D ** -0.5.
     Returns out [rows, q_heads, D] and, with return_lse, lse [rows, q_heads].
     """
     return PrefixAttentionPlan(q, prefix_k, prefix_v, suffix_k, suffix_v, prefix_lengths, suffix_lengths, cu_draft,
