@@ -326,8 +326,8 @@ class PrefixAttentionPlan(_DevicePlan):
         with _on(dev, stream):
             if out is None:
                 out = {"out": torch.empty((rows, q_heads, dim), dtype=dtype, device=dev)}
-                if return_lse:
-                    out["lse"] = torch.empty((rows, q_heads), dtype=torch.float32, device=dev)
+            if return_lse and out.get("lse") is None:
+                out = {**out, "lse": torch.empty((rows, q_heads), dtype=torch.float32, device=dev)}
         o = out["out"]
         if tuple(o.shape) != (rows, q_heads, dim) or o.dtype != dtype or o.device != dev:
             raise ValueError(f"out['out'] must be {dtype} [{rows}, {q_heads}, {dim}] on {dev}")
@@ -368,7 +368,8 @@ def prefix_attention(q: torch.Tensor, prefix_k: torch.Tensor, prefix_v: torch.Te
     (uniform K); cu_groups int32 [groups + 1], the groups' first sequences, or
     None (equal groups).  max_draft and max_group are read back from the device,
     on the call's stream, where they are needed and not given.  scale defaults to D ** -0.5.
-    Returns out [rows, q_heads, D] and, with return_lse, lse [rows, q_heads].
+    Returns out [rows, q_heads, D] and, with return_lse, lse [rows, q_heads]; `out`
+    may hold both, or out alone.
     """
     return PrefixAttentionPlan(q, prefix_k, prefix_v, suffix_k, suffix_v, prefix_lengths, suffix_lengths, cu_draft,
                                max_draft, cu_groups, max_group, scale, return_lse, out, workspace, stream)()

@@ -46,3 +46,16 @@ def test_attention_reads_sizes_back_on_its_stream(sv, what):
                               return_lse=True, stream=s)
     torch.cuda.synchronize()
     assert torch.equal(got["out"], ref["out"]) and torch.equal(got["lse"], ref["lse"])
+
+
+def test_attention_lse_beside_a_given_out(sv):
+    """return_lse with an out that holds none: the call adds one and leaves the caller's dict alone."""
+    c = Case([3], [1] * 3, 4, 2, 64, 100, 8, "bf16")
+    ref = c.run(sv)
+    for given in ({}, {"lse": None}):
+        mine = {"out": torch.empty_like(ref["out"]), **given}
+        got = c.run(sv, out=mine)
+        torch.cuda.synchronize()
+        assert got["out"] is mine["out"] and mine.get("lse") is None
+        assert torch.equal(got["out"], ref["out"]) and torch.equal(got["lse"], ref["lse"])
+    assert "lse" not in c.run(sv, return_lse=False)
