@@ -59,3 +59,29 @@ def test_attention_lse_beside_a_given_out(sv):
         assert got["out"] is mine["out"] and mine.get("lse") is None
         assert torch.equal(got["out"], ref["out"]) and torch.equal(got["lse"], ref["lse"])
     assert "lse" not in c.run(sv, return_lse=False)
+
+
+def test_memory_of_plans_outlives_their_work_on_other_streams(sv):
+    """Plans made for one stream, called on another that is busy, and dropped: none of their memory is handed out
+    before that stream has done its work, and the results are those of a quiet call."""
+    g = torch.Generator().manual_seed(4)
+    logits = torch.randn(32, 20000, generator=g).to(DEV)
+    scores = -torch.rand(32, generator=g).to(DEV)
+    c = Case([4], [1] * 4, 8, 2, 64, 900, 20, "bf16")
+    select, attn = sv.beam_select(logits, scores, 4, 8), c.run(sv)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    done = busy(s)
+    plans = [sv.BeamSelectPlan(logits, scores, 4, 8), sv.PrefixAttentionPlan(c.q, c.pk, c.pv, c.sk, c.sv,
+                                                                             return_lse=True)]
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        got = [{k: v.clone() for k, v in p().items()} for p in plans]
+    blocks = {t.data_ptr(): t.numel() * t.element_size() for p in plans for t in (p.workspace, *p.out.values())}
+    del plans
+    fresh = [torch.full((size,), 7, dtype=torch.uint8, device=DEV) for size in blocks.values() for _ in range(4)]
+    assert not done.query()  # (otherwise this shows nothing)
+    assert not blocks.keys() & {t.data_ptr() for t in fresh}
+    torch.cuda.synchronize()
+    assert all(torch.equal(got[0][k], select[k]) for k in select)
+    assert all(torch.equal(got[1][k], attn[k]) for k in attn)
