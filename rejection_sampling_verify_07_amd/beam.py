@@ -8,14 +8,13 @@ arguments once, for tight loops and graph capture.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes as C
 from typing import Optional
 
 import torch
 
 from . import binding as _b
-from .binding import SpecVerifyError, _check, _dtype_code, _Plan, load_library
+from .binding import SpecVerifyError, _check, _dtype_code, _longest, _on, _Plan, load_library
 
 
 class BeamShapeT(C.Structure):
@@ -43,16 +42,6 @@ class AttentionShapeT(C.Structure):
                                           "kv_heads", "head_dim", "max_prefix", "max_suffix", "dtype")]
                 + [(n, C.c_int64) for n in ("q_row_stride", "q_head_stride", "out_row_stride", "out_head_stride")]
                 + [(n, C.c_void_p) for n in ("cu_draft", "cu_groups", "prefix_lengths", "suffix_lengths")])
-
-
-def _on(dev, stream):
-    """A context whose work and allocations on `dev` belong to `stream`
-    (default: the device's current one)."""
-    if stream is None:
-        return contextlib.nullcontext()
-    if stream.device != dev:
-        raise ValueError(f"stream is on {stream.device} but the tensors are on {dev}")
-    return torch.cuda.stream(stream)
 
 
 def _vector(t, name, numel, dtype, dev):
@@ -317,11 +306,10 @@ class PrefixAttentionPlan(_DevicePlan):
         vectors = [None if t is None else _vector(t, n, c, torch.int32, dev) for n, t, c in (
             ("cu_draft", cu_draft, batch + 1), ("cu_groups", cu_groups, groups + 1),
             ("prefix_lengths", prefix_lengths, groups), ("suffix_lengths", suffix_lengths, batch))]
-        with _on(dev, stream):  # (read back on the call's stream: work queued there may still write them)
-            if max_draft is None:
-                max_draft = int((cu_draft[1:] - cu_draft[:-1]).max().item())
-            if cu_groups is not None and max_group is None:
-                max_group = int((cu_groups[1:] - cu_groups[:-1]).max().item())
+        if max_draft is None:
+            max_draft = _longest(cu_draft, stream)
+        if cu_groups is not None and max_group is None:
+            max_group = _longest(cu_groups, stream)
         lse = None
         with _on(dev, stream):
             if out is None:

@@ -6,6 +6,7 @@ is no fallback: if the library is missing, loading raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes as C
 import os
 from typing import Optional
@@ -118,6 +119,16 @@ def _check(status: int, where: str):
         raise SpecVerifyError(status, where)
 
 
+def _on(dev, stream):
+    """A context whose work and allocations on `dev` belong to `stream`
+    (default: the device's current one)."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if stream.device != dev:
+        raise ValueError(f"stream is on {stream.device} but the tensors are on {dev}")
+    return torch.cuda.stream(stream)
+
+
 def _dtype_code(t: torch.Tensor) -> int:
     if t.dtype == torch.float32:
         return SV_DTYPE_F32
@@ -172,7 +183,13 @@ def make_shape(target: torch.Tensor, draft: Optional[torch.Tensor], batch: int, 
     )
 
 
-def _batch_geometry(target, draft_ids, cu_draft, max_draft):
+def _longest(cu, stream):
+    """The largest K_b, read back on the call's stream (work queued there may still write cu)."""
+    with _on(cu.device, stream):
+        return int((cu[1:] - cu[:-1]).max().item())
+
+
+def _batch_geometry(target, draft_ids, cu_draft, max_draft, stream=None):
     total = draft_ids.numel()
     if cu_draft is None:
         batch = target.shape[0] - total  # rows_t = sum(K_b) + B
@@ -191,7 +208,7 @@ def _batch_geometry(target, draft_ids, cu_draft, max_draft):
         raise ValueError(f"target_logits has {target.shape[0]} rows; {batch} sequences with {total} draft ids "
                          f"need {total + batch}")
     if max_draft is None:
-        max_draft = int((cu_draft[1:] - cu_draft[:-1]).max().item()) if batch > 0 else 0
+        max_draft = _longest(cu_draft, stream)
     return batch, max_draft, total
 
 
@@ -217,7 +234,7 @@ def verify_sample(target_logits: torch.Tensor, draft_logits: torch.Tensor, draft
     lib = load_library()
     fn = lib.spec_verify_argmax if argmax else lib.spec_verify_sample
     name = "spec_verify_argmax" if argmax else "spec_verify_sample"
-    batch, kmax, total = _batch_geometry(target_logits, draft_ids, cu_draft, max_draft)
+    batch, kmax, total = _batch_geometry(target_logits, draft_ids, cu_draft, max_draft, stream)
     if draft_ids.dtype != torch.int32:
         raise TypeError("draft_ids must be int32")
     shape = make_shape(target_logits, draft_logits, batch, kmax, total, cu_draft, total + batch, total)
@@ -257,7 +274,7 @@ def verify_sample_noalloc(target_logits: torch.Tensor, draft_logits: torch.Tenso
     calls that overlap on one GPU race).  `out` (tokens, num_accepted, probs,
     residual_mass) may be preallocated; otherwise it is allocated here."""
     lib = load_library()
-    batch, kmax, total = _batch_geometry(target_logits, draft_ids, cu_draft, max_draft)
+    batch, kmax, total = _batch_geometry(target_logits, draft_ids, cu_draft, max_draft, stream)
     if draft_ids.dtype != torch.int32:
         raise TypeError("draft_ids must be int32")
     shape = make_shape(target_logits, draft_logits, batch, kmax, total, cu_draft, total + batch, total)
@@ -288,7 +305,7 @@ def verify_greedy(target_logits: torch.Tensor, draft_ids: torch.Tensor, cu_draft
                   out: Optional[dict] = None, stream=None) -> dict:
     """Greedy argmax-compare verify on the GPU (spec_verify_greedy)."""
     lib = load_library()
-    batch, kmax, total = _batch_geometry(target_logits, draft_ids, cu_draft, max_draft)
+    batch, kmax, total = _batch_geometry(target_logits, draft_ids, cu_draft, max_draft, stream)
     if draft_ids.dtype != torch.int32:
         raise TypeError("draft_ids must be int32")
     shape = make_shape(target_logits, None, batch, kmax, total, cu_draft, total + batch)
@@ -312,7 +329,7 @@ def verify_greedy(target_logits: torch.Tensor, draft_ids: torch.Tensor, cu_draft
     return out
 
 
-def _draft_geometry(draft_logits, cu_draft, batch, max_draft):
+def _draft_geometry(draft_logits, cu_draft, batch, max_draft, stream=None):
     total = draft_logits.shape[0]
     if cu_draft is None:
         if batch is None or batch <= 0 or total % batch != 0:
@@ -325,7 +342,7 @@ def _draft_geometry(draft_logits, cu_draft, batch, max_draft):
         raise ValueError("cu_draft must be a 1-D int32 tensor")
     b = cu_draft.numel() - 1
     if max_draft is None:
-        max_draft = int((cu_draft[1:] - cu_draft[:-1]).max().item()) if b > 0 else 0
+        max_draft = _longest(cu_draft, stream) if b > 0 else 0
     return b, max_draft, total
 
 
@@ -340,7 +357,7 @@ def draft_sample(draft_logits: torch.Tensor, cu_draft: Optional[torch.Tensor] = 
     the int32 ids [sum(K_b)].
     """
     lib = load_library()
-    b, kmax, total = _draft_geometry(draft_logits, cu_draft, batch, max_draft)
+    b, kmax, total = _draft_geometry(draft_logits, cu_draft, batch, max_draft, stream)
     shape = make_shape(draft_logits, draft_logits, b, kmax, total, cu_draft, total)
     dev = draft_logits.device
     need = C.c_size_t(0)
@@ -394,7 +411,7 @@ def token_likelihood(target_logits: torch.Tensor, draft_logits: torch.Tensor, to
         raise TypeError("tokens must be int32")
     if target_logits.shape[0] != draft_logits.shape[0] or target_logits.shape[0] != tokens.numel():
         raise ValueError("target_logits, draft_logits and tokens need one row per position")
-    b, kmax, total = _draft_geometry(draft_logits, cu_draft, batch, max_draft)
+    b, kmax, total = _draft_geometry(draft_logits, cu_draft, batch, max_draft, stream)
     shape = make_shape(target_logits, draft_logits, b, kmax, total, cu_draft, total, total)
     dev = target_logits.device
     need = C.c_size_t(0)
@@ -517,7 +534,7 @@ class SamplePlan(_Plan):
                  offset=0, max_draft=None, out=None, workspace=None, stream=None, probs=True, argmax=False,
                  top_p=1.0):
         self.lib = load_library()
-        batch, kmax, total = _batch_geometry(target_logits, draft_ids, cu_draft, max_draft)
+        batch, kmax, total = _batch_geometry(target_logits, draft_ids, cu_draft, max_draft, stream)
         self.shape = make_shape(target_logits, draft_logits, batch, kmax, total, cu_draft, total + batch, total)
         dev = target_logits.device
         need = C.c_size_t(0)
@@ -553,7 +570,7 @@ class GreedyPlan(_Plan):
     def __init__(self, target_logits, draft_ids, cu_draft=None, max_draft=None, out=None, workspace=None,
                  stream=None):
         self.lib = load_library()
-        batch, kmax, total = _batch_geometry(target_logits, draft_ids, cu_draft, max_draft)
+        batch, kmax, total = _batch_geometry(target_logits, draft_ids, cu_draft, max_draft, stream)
         self.shape = make_shape(target_logits, None, batch, kmax, total, cu_draft, total + batch)
         dev = target_logits.device
         need = C.c_size_t(0)
@@ -581,7 +598,7 @@ class LikelihoodPlan(_Plan):
     def __init__(self, target_logits, draft_logits, tokens, cu_draft=None, batch=None, temperature=1.0, top_k=0,
                  max_draft=None, terms=True, beta=True, nll=True, workspace=None, stream=None, top_p=1.0):
         self.lib = load_library()
-        b, kmax, total = _draft_geometry(draft_logits, cu_draft, batch, max_draft)
+        b, kmax, total = _draft_geometry(draft_logits, cu_draft, batch, max_draft, stream)
         self.shape = make_shape(target_logits, draft_logits, b, kmax, total, cu_draft, total, total)
         dev = target_logits.device
         need = C.c_size_t(0)
@@ -610,7 +627,7 @@ class DraftPlan(_Plan):
     def __init__(self, draft_logits, cu_draft=None, batch=None, temperature=1.0, top_k=0, seed=0, offset=0,
                  max_draft=None, out=None, workspace=None, stream=None, top_p=1.0):
         self.lib = load_library()
-        b, kmax, total = _draft_geometry(draft_logits, cu_draft, batch, max_draft)
+        b, kmax, total = _draft_geometry(draft_logits, cu_draft, batch, max_draft, stream)
         self.shape = make_shape(draft_logits, draft_logits, b, kmax, total, cu_draft, total)
         dev = draft_logits.device
         need = C.c_size_t(0)
