@@ -242,16 +242,17 @@ def verify_sample(target_logits: torch.Tensor, draft_logits: torch.Tensor, draft
     need = C.c_size_t(0)
     _check(fn(C.byref(shape), None, None, None, float(temperature), int(top_k), float(top_p), int(seed),
               int(offset), None, None, None, None, None, C.byref(need), None), name + "(workspace query)")
-    if workspace is None or workspace.numel() < need.value:
-        workspace = torch.empty(max(need.value, 1), dtype=torch.uint8, device=dev)
-    if out is None:
-        out = dict(
-            tokens=torch.empty(total + batch, dtype=torch.int32, device=dev),
-            num_accepted=torch.empty(batch, dtype=torch.int32, device=dev),
-        )
-        if return_probs:
-            out["probs"] = torch.empty((max(total, 1), 2), dtype=torch.float32, device=dev)[:total]
-            out["residual_mass"] = torch.empty(batch, dtype=torch.float32, device=dev)
+    with _on(dev, stream):
+        if workspace is None or workspace.numel() < need.value:
+            workspace = torch.empty(max(need.value, 1), dtype=torch.uint8, device=dev)
+        if out is None:
+            out = dict(
+                tokens=torch.empty(total + batch, dtype=torch.int32, device=dev),
+                num_accepted=torch.empty(batch, dtype=torch.int32, device=dev),
+            )
+            if return_probs:
+                out["probs"] = torch.empty((max(total, 1), 2), dtype=torch.float32, device=dev)[:total]
+                out["residual_mass"] = torch.empty(batch, dtype=torch.float32, device=dev)
     have = C.c_size_t(workspace.numel())
     st = fn(
         C.byref(shape), target_logits.data_ptr(), draft_logits.data_ptr() if draft_logits.numel() else None,
@@ -279,11 +280,12 @@ def verify_sample_noalloc(target_logits: torch.Tensor, draft_logits: torch.Tenso
         raise TypeError("draft_ids must be int32")
     shape = make_shape(target_logits, draft_logits, batch, kmax, total, cu_draft, total + batch, total)
     dev = target_logits.device
-    if out is None:
-        out = dict(tokens=torch.empty(total + batch, dtype=torch.int32, device=dev),
-                   num_accepted=torch.empty(batch, dtype=torch.int32, device=dev),
-                   probs=torch.empty((max(total, 1), 2), dtype=torch.float32, device=dev)[:total],
-                   residual_mass=torch.empty(batch, dtype=torch.float32, device=dev))
+    with _on(dev, stream):
+        if out is None:
+            out = dict(tokens=torch.empty(total + batch, dtype=torch.int32, device=dev),
+                       num_accepted=torch.empty(batch, dtype=torch.int32, device=dev),
+                       probs=torch.empty((max(total, 1), 2), dtype=torch.float32, device=dev)[:total],
+                       residual_mass=torch.empty(batch, dtype=torch.float32, device=dev))
     st = lib.spec_verify_sample_noalloc(
         C.byref(shape), target_logits.data_ptr(), draft_logits.data_ptr() if draft_logits.numel() else None,
         draft_ids.data_ptr() if draft_ids.numel() else None, float(temperature), int(top_k), float(top_p), int(seed),
@@ -313,13 +315,14 @@ def verify_greedy(target_logits: torch.Tensor, draft_ids: torch.Tensor, cu_draft
     need = C.c_size_t(0)
     _check(lib.spec_verify_greedy(C.byref(shape), None, None, None, None, None, C.byref(need), None),
            "spec_verify_greedy(workspace query)")
-    if workspace is None or workspace.numel() < need.value:
-        workspace = torch.empty(max(need.value, 1), dtype=torch.uint8, device=dev)
-    if out is None:
-        out = dict(
-            tokens=torch.empty(total + batch, dtype=torch.int32, device=dev),
-            num_accepted=torch.empty(batch, dtype=torch.int32, device=dev),
-        )
+    with _on(dev, stream):
+        if workspace is None or workspace.numel() < need.value:
+            workspace = torch.empty(max(need.value, 1), dtype=torch.uint8, device=dev)
+        if out is None:
+            out = dict(
+                tokens=torch.empty(total + batch, dtype=torch.int32, device=dev),
+                num_accepted=torch.empty(batch, dtype=torch.int32, device=dev),
+            )
     have = C.c_size_t(workspace.numel())
     st = lib.spec_verify_greedy(C.byref(shape), target_logits.data_ptr(),
                                 draft_ids.data_ptr() if draft_ids.numel() else None, out["tokens"].data_ptr(),
@@ -363,10 +366,11 @@ def draft_sample(draft_logits: torch.Tensor, cu_draft: Optional[torch.Tensor] = 
     need = C.c_size_t(0)
     _check(lib.spec_draft_sample(C.byref(shape), None, float(temperature), int(top_k), float(top_p), int(seed),
                                  int(offset), None, None, C.byref(need), None), "spec_draft_sample(workspace query)")
-    if workspace is None or workspace.numel() < need.value:
-        workspace = torch.empty(max(need.value, 1), dtype=torch.uint8, device=dev)
-    if out is None:
-        out = torch.empty(max(total, 1), dtype=torch.int32, device=dev)[:total]
+    with _on(dev, stream):
+        if workspace is None or workspace.numel() < need.value:
+            workspace = torch.empty(max(need.value, 1), dtype=torch.uint8, device=dev)
+        if out is None:
+            out = torch.empty(max(total, 1), dtype=torch.int32, device=dev)[:total]
     have = C.c_size_t(workspace.numel())
     st = lib.spec_draft_sample(C.byref(shape), draft_logits.data_ptr() if total else None, float(temperature),
                                int(top_k), float(top_p), int(seed), int(offset), out.data_ptr() if total else None,
@@ -418,9 +422,10 @@ def token_likelihood(target_logits: torch.Tensor, draft_logits: torch.Tensor, to
     _check(lib.spec_token_likelihood(C.byref(shape), None, None, None, float(temperature), int(top_k), float(top_p),
                                      None, None, None, None, C.byref(need), None),
            "spec_token_likelihood(workspace query)")
-    if workspace is None or workspace.numel() < need.value:
-        workspace = torch.empty(max(need.value, 1), dtype=torch.uint8, device=dev)
-    out = _likelihood_outputs(total, b, dev, terms, beta, nll)
+    with _on(dev, stream):
+        if workspace is None or workspace.numel() < need.value:
+            workspace = torch.empty(max(need.value, 1), dtype=torch.uint8, device=dev)
+        out = _likelihood_outputs(total, b, dev, terms, beta, nll)
     have = C.c_size_t(workspace.numel())
     st = lib.spec_token_likelihood(
         C.byref(shape), target_logits.data_ptr() if total else None, draft_logits.data_ptr() if total else None,
@@ -541,12 +546,13 @@ class SamplePlan(_Plan):
         _check(self.lib.spec_verify_sample(C.byref(self.shape), None, None, None, float(temperature), int(top_k),
                                            float(top_p), int(seed), int(offset), None, None, None, None, None,
                                            C.byref(need), None), "workspace query")
-        self.workspace = workspace if workspace is not None and workspace.numel() >= need.value else \
-            torch.empty(max(need.value, 1), dtype=torch.uint8, device=dev)
-        self.out = out or dict(tokens=torch.empty(total + batch, dtype=torch.int32, device=dev),
-                               num_accepted=torch.empty(batch, dtype=torch.int32, device=dev),
-                               probs=torch.empty((max(total, 1), 2), dtype=torch.float32, device=dev),
-                               residual_mass=torch.empty(batch, dtype=torch.float32, device=dev))
+        with _on(dev, stream):
+            self.workspace = workspace if workspace is not None and workspace.numel() >= need.value else \
+                torch.empty(max(need.value, 1), dtype=torch.uint8, device=dev)
+            self.out = out or dict(tokens=torch.empty(total + batch, dtype=torch.int32, device=dev),
+                                   num_accepted=torch.empty(batch, dtype=torch.int32, device=dev),
+                                   probs=torch.empty((max(total, 1), 2), dtype=torch.float32, device=dev),
+                                   residual_mass=torch.empty(batch, dtype=torch.float32, device=dev))
         self.have = C.c_size_t(self.workspace.numel())
         self._keep = (target_logits, draft_logits, draft_ids, cu_draft)
         self.args = (C.byref(self.shape), C.c_void_p(target_logits.data_ptr()),
@@ -576,10 +582,11 @@ class GreedyPlan(_Plan):
         need = C.c_size_t(0)
         _check(self.lib.spec_verify_greedy(C.byref(self.shape), None, None, None, None, None, C.byref(need), None),
                "workspace query")
-        self.workspace = workspace if workspace is not None and workspace.numel() >= need.value else \
-            torch.empty(max(need.value, 1), dtype=torch.uint8, device=dev)
-        self.out = out or dict(tokens=torch.empty(total + batch, dtype=torch.int32, device=dev),
-                               num_accepted=torch.empty(batch, dtype=torch.int32, device=dev))
+        with _on(dev, stream):
+            self.workspace = workspace if workspace is not None and workspace.numel() >= need.value else \
+                torch.empty(max(need.value, 1), dtype=torch.uint8, device=dev)
+            self.out = out or dict(tokens=torch.empty(total + batch, dtype=torch.int32, device=dev),
+                                   num_accepted=torch.empty(batch, dtype=torch.int32, device=dev))
         self.have = C.c_size_t(self.workspace.numel())
         self._keep = (target_logits, draft_ids, cu_draft)
         self.args = (C.byref(self.shape), C.c_void_p(target_logits.data_ptr()),
@@ -605,9 +612,10 @@ class LikelihoodPlan(_Plan):
         _check(self.lib.spec_token_likelihood(C.byref(self.shape), None, None, None, float(temperature), int(top_k),
                                               float(top_p), None, None, None, None, C.byref(need), None),
                "workspace query")
-        self.workspace = workspace if workspace is not None and workspace.numel() >= need.value else \
-            torch.empty(max(need.value, 1), dtype=torch.uint8, device=dev)
-        self.out = _likelihood_outputs(total, b, dev, terms, beta, nll)
+        with _on(dev, stream):
+            self.workspace = workspace if workspace is not None and workspace.numel() >= need.value else \
+                torch.empty(max(need.value, 1), dtype=torch.uint8, device=dev)
+            self.out = _likelihood_outputs(total, b, dev, terms, beta, nll)
         self.have = C.c_size_t(self.workspace.numel())
         self._keep = (target_logits, draft_logits, tokens, cu_draft)
         self.args = (C.byref(self.shape), C.c_void_p(target_logits.data_ptr()), C.c_void_p(draft_logits.data_ptr()),
@@ -633,9 +641,10 @@ class DraftPlan(_Plan):
         need = C.c_size_t(0)
         _check(self.lib.spec_draft_sample(C.byref(self.shape), None, float(temperature), int(top_k), float(top_p),
                                           int(seed), int(offset), None, None, C.byref(need), None), "workspace query")
-        self.workspace = workspace if workspace is not None and workspace.numel() >= need.value else \
-            torch.empty(max(need.value, 1), dtype=torch.uint8, device=dev)
-        self.out = out if out is not None else torch.empty(max(total, 1), dtype=torch.int32, device=dev)
+        with _on(dev, stream):
+            self.workspace = workspace if workspace is not None and workspace.numel() >= need.value else \
+                torch.empty(max(need.value, 1), dtype=torch.uint8, device=dev)
+            self.out = out if out is not None else torch.empty(max(total, 1), dtype=torch.int32, device=dev)
         self.have = C.c_size_t(self.workspace.numel())
         self._keep = (draft_logits, cu_draft)
         self.args = (C.byref(self.shape), C.c_void_p(draft_logits.data_ptr()), C.c_float(temperature),

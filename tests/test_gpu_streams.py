@@ -64,3 +64,39 @@ def test_sizes_read_back_on_the_stream_of_the_call(sv, name):
     torch.cuda.synchronize()
     for k in ref:
         assert torch.equal(got[k], ref[k]), k
+
+
+def stream_beside_the_current_one():
+    """A stream whose work does not hold the current one's up (several streams may share one hardware queue)."""
+    for _ in range(8):
+        s = torch.cuda.Stream()
+        torch.cuda.synchronize()
+        done = busy(s, 6)
+        torch.zeros(1, device=DEV)
+        torch.cuda.current_stream().synchronize()
+        if not done.query():
+            return s
+    pytest.skip("no stream runs beside the current one")
+
+
+@pytest.mark.parametrize("name", ["sample", "greedy", "draft", "likelihood"])
+def test_workspace_allocated_on_the_stream_of_the_call(sv, name):
+    """A workspace that the call allocates and drops is not handed out to others while its stream still works."""
+    args = inputs()
+    call, plan = calls(sv, *args, max_draft=9)[name]
+    ref, size = call(None), plan(None).workspace.numel()
+    s = stream_beside_the_current_one()
+    warm = [torch.empty(size, dtype=torch.uint8, device=DEV) for _ in range(9)]  # (nothing below waits for memory)
+    with torch.cuda.stream(s):
+        warm.append(torch.empty(size, dtype=torch.uint8, device=DEV))
+    del warm
+    torch.cuda.synchronize()
+    done = busy(s)
+    got = call(s)
+    fresh = [torch.full((size,), 7, dtype=torch.uint8, device=DEV) for _ in range(8)]
+    torch.cuda.current_stream().synchronize()
+    assert not done.query()  # (otherwise this shows nothing)
+    torch.cuda.synchronize()
+    assert all(bool((f == 7).all()) for f in fresh)
+    for k in ref:
+        assert torch.equal(got[k], ref[k]), k
