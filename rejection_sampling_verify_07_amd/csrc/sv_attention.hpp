@@ -25,15 +25,16 @@
 // other: at most half a step, 2^-8 (bf16) or 2^-11 (fp16) of each weight (fp16
 // weights below 2^-24 of the row's largest in a part: 2^-35 of that one), and
 // the weights' errors are independent, so the sum's is about that of rounding
-// out itself at the end (both together: 1.35 times the error of out's rounding
-// alone, measured).  The sum l takes the unrounded weights; scores,
+// out itself at the end (both together: up to 1.35 times the error of out's
+// rounding alone in bf16, 1.15 times in fp16, measured).  The sum l takes the unrounded weights; scores,
 // statistics and accumulators are fp32.
 //
 // What bounds it.  A group with few rows per key/value head reads its caches:
 // 4 groups of 8 beams, 8 key heads of 128, 65536 shared positions: 185 us,
 // 5.9 TB/s with the join.  Many rows are bound by the products and the
 // exponentials beside them (attend_tiles).  Small calls are two launches and
-// their memory latencies: 4 rows of 8 heads on 500 positions 7.4 us.
+// their memory latencies: 4 rows of 8 heads on 500 positions 7.5 us in a row of
+// calls on a few inputs, 8.1 to 8.6 us on inputs new to the caches.
 #pragma once
 
 #include <type_traits>
@@ -468,15 +469,17 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const KeyRange& kr, in
 // l16 of tile d holds four keys of column d * 16 + l16.
 // The next tile travels in registers while the present one is used.
 //
-// 320 rows of 32 heads on 65536 positions (8 key heads of 128): 376 us, 0.91
-// PFLOP/s with the join.  Per 64 keys and 32 rows a wave spends 1024 cycles of
-// matrix instructions and about 1250 of vector ones (32 exponentials at a
-// quarter rate, 32 each of scale-and-subtract, sum, maximum), and the two
-// waves of a SIMD overlap them little: counters show the vector units busy 47%
-// and the matrix units 33% of the time, LDS 33%.  Three waves per SIMD leave
-// 168 registers, which spills; 64 rows per wave leave one wave.  Scores of the
-// next 32 keys formed beside the exponentials of the present ones (keys a tile
-// ahead of values, 80 KB of LDS) took 400 us, however the two were interleaved.
+// 320 rows of 32 heads on 65536 positions (8 key heads of 128): 366 to 379 us,
+// 0.91 to 0.94 PFLOP/s with the join.  Per 64 keys and 32 rows a wave spends
+// 1024 cycles of matrix instructions and about 1250 of vector ones (32
+// exponentials at a quarter rate, 32 each of scale-and-subtract, sum, maximum),
+// and the two waves of a SIMD overlap them little: counters show the vector
+// units busy 47% and the matrix units 33% of the time, LDS 33%.  (128 columns
+// hold all 256 registers; 8 more are spilled, outside the loop.)  Three waves
+// per SIMD leave 168 registers, which spills inside it; 64 rows per wave leave
+// one wave.  Scores of the next 32 keys formed beside the exponentials of the
+// present ones (keys a tile ahead of values, 80 KB of LDS) took 400 us, however
+// the two were interleaved.
 template <int DT, int D, int MT>
 struct TileAttention {
     static constexpr int DC = D / 32, DT16 = D / 16;
@@ -793,7 +796,7 @@ __global__ __launch_bounds__(kAttnThreads, D == 256 ? 1 : 2) void attn_part_kern
 // of a part, so kWave / (D / 4) parts are read side by side, kJoinRounds times
 // without waiting: those loads go out before the parts' (m, l), one per lane,
 // have arrived, and before it is known which parts hold anything (a part
-// without a visible key has l = 0 and old bytes for o, which are dropped; l is NaN where a row sees a NaN).
+// without a visible key has l = 0 and is dropped; l is NaN where a row sees a NaN).
 // 10240 (row, head) pairs of 128 columns in 7 parts: 9.6 us, 4.1 TB/s; 32 pairs
 // of 4 parts: 3.5 us, latency.
 constexpr int kJoinRounds = 4;

@@ -16,8 +16,8 @@
 // largest logit and S_w = sum_u exp((l_wu - m_w) / T): the difference is exact
 // in fp64 and no large terms cancel.
 //
-// 512 rows of 151936 bf16 logits (64 groups of 8, 16 kept): streaming pass 30 us,
-// 5.2 TB/s; pick 12.5 us.  4 rows of 50304 fp32: 3 and 9 us.  The pick is a
+// 512 rows of 151936 bf16 logits (64 groups of 8, 16 kept): streaming pass 31 us,
+// 5.0 TB/s; pick 13 us.  4 rows of 50304 fp32: 3 and 9 us.  The pick is a
 // chain of latencies: offsets 2 us (two memory rounds, one fp64 log), then
 // scores, bound, gather, block ranking, element loads and ranking, 0.7 to 1 us each.
 //
@@ -150,7 +150,9 @@ __device__ __forceinline__ bool ahead(double sa, int32_t ia, double sb, int32_t 
 
 // exp(x) in fp64 for x <= 0 (and NaN): 2^(n / 32) from a table and exp of the
 // rest, at most ln 2 / 64 = 0.0109, by its series to the 6th power (the next
-// term is below 4e-18 relative).  About a dozen fp64 instructions; the library's
+// term is below 4e-18 relative).  The form of P. T. P. Tang, "Table-driven
+// implementation of the exponential function in IEEE floating-point
+// arithmetic", ACM TOMS 15 (1989), with a Taylor series for its polynomial.  About a dozen fp64 instructions; the library's
 // exp took four times as long over a row.
 constexpr int kExpTable = 32;
 static __device__ const double kExp2Of32nds[kExpTable] = {  // 2^(j / 32)

@@ -9,8 +9,9 @@
 // each distinct parent's bytes come from HBM once (a parent that several
 // places take is read again from L1), and places that keep their state cost
 // nothing.  Bound by HBM: distinct moved parents read, moved places written.
-// 4.3 GB of caches (8 groups of 8, 5 distinct parents each): 900 us, 6.0 TB/s;
-// 162 MB with rows of 180 bytes: 40 us, 5.4 TB/s; 0.9 MB: 4.9 us, the launch.
+// 4.3 GB of caches (8 groups of 8, 5 distinct parents each, of which 4.9 GB are
+// read and written): 900 to 960 us, 5.1 to 5.4 TB/s; 162 MB with rows of 180
+// bytes (188 MB): 41 us, 4.6 TB/s; 0.9 MB: 4.9 us, the launch.
 #pragma once
 
 #include "sv_common.hpp"
