@@ -26,8 +26,8 @@
 // weights below 2^-24 of the row's largest in a part: 2^-35 of that one), and
 // the weights' errors are independent, so the sum's is about that of rounding
 // out itself at the end (both together: up to 1.35 times the error of out's
-// rounding alone in bf16, 1.15 times in fp16, measured).  The sum l takes the unrounded weights; scores,
-// statistics and accumulators are fp32.
+// rounding alone in bf16, 1.15 times in fp16, measured).  The sum l takes the
+// unrounded weights; scores, statistics and accumulators are fp32.
 //
 // What bounds it.  A group with few rows per key/value head reads its caches:
 // 4 groups of 8 beams, 8 key heads of 128, 65536 shared positions: 185 us,

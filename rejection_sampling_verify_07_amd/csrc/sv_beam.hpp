@@ -30,9 +30,9 @@
 // is at most ln V <= 13.9, so lse_w is off by at most
 // (3 * 13.9 + 9) 2^-24 < 3.1e-6.  Two candidates of different beams whose
 // scores lie within twice that (kBeamWindow) and a few of the scores' own fp64
-// steps are not decided by these sums:
-// the pick then recomputes the log sums concerned in fp64 from the rows and
-// selects again, so the order is always the fp64 scores' order.  A group that
+// steps are not decided by these sums: the pick then recomputes the log sums
+// concerned in fp64 from the rows and selects again, so the order is always the
+// fp64 scores' order.  A group that
 // needs it takes 32 us more per beam of 151936 logits; on random logits that is
 // rare (two scores of different beams have to lie within the window).
 #pragma once
@@ -152,8 +152,9 @@ __device__ __forceinline__ bool ahead(double sa, int32_t ia, double sb, int32_t 
 // rest, at most ln 2 / 64 = 0.0109, by its series to the 6th power (the next
 // term is below 4e-18 relative).  The form of P. T. P. Tang, "Table-driven
 // implementation of the exponential function in IEEE floating-point
-// arithmetic", ACM TOMS 15 (1989), with a Taylor series for its polynomial.  About a dozen fp64 instructions; the library's
-// exp took four times as long over a row.
+// arithmetic", ACM TOMS 15 (1989), with a Taylor series for its polynomial.
+// About a dozen fp64 instructions; the library's exp took four times as long
+// over a row.
 constexpr int kExpTable = 32;
 static __device__ const double kExp2Of32nds[kExpTable] = {  // 2^(j / 32)
     0x1.0000000000000p+0, 0x1.059b0d3158574p+0, 0x1.0b5586cf9890fp+0, 0x1.11301d0125b51p+0,

@@ -10,8 +10,8 @@ pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
 
 
-def busy(stream, n=24):
-    """Some tens of milliseconds of work queued on `stream`; an event behind it."""
+def busy(stream, n=80):
+    """About n milliseconds of work queued on `stream`; an event behind it."""
     with torch.cuda.stream(stream):
         x = torch.full((8192, 8192), 2.0 ** -13, dtype=torch.bfloat16, device=DEV)
         for _ in range(n):
