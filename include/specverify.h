@@ -500,6 +500,139 @@ SV_API sv_status_t spec_prefix_attention(const sv_attention_shape_t* shape,
                                    size_t* workspace_bytes,
                                    hipStream_t stream);
 
+/*
+ * Caches in pages.  A pool holds the states of many sequences in pages of
+ * page_size positions,
+ *     pool[slab][page][head][position in page][0 .. row_bytes)
+ * with any strides whose places are distinct: [layers, pages, page_size, heads *
+ * dim] has heads = 1 and one slab per layer (keys and values in one allocation:
+ * two), [layers, pages, heads, page_size, dim] has its heads.  A sequence's page
+ * table lists its pages: position p lies in page table[b][p / page_size].  A table
+ * entry outside [0, pages) is no page (-1 where a table ends).
+ */
+typedef struct {
+    int32_t slabs;           /* >= 1: layers, or layers * 2      */
+    int32_t pages;           /* >= 1                             */
+    int32_t page_size;       /* >= 1 positions per page          */
+    int32_t heads;           /* >= 1                             */
+    int64_t row_bytes;       /* >= 1, contiguous, per position (and head) */
+    int64_t slab_stride;     /* bytes                            */
+    int64_t page_stride;     /* bytes                            */
+    int64_t head_stride;     /* bytes                            */
+    int64_t position_stride; /* bytes                            */
+} sv_pool_t;
+
+/*
+ * The step of a paged cache after a verify: the rows of the accepted guesses move
+ * to the places that follow the context, in place, and the sequence's new length
+ * is formed.  Sequence b's cache holds lengths[b] positions, the last K_b + 1 of
+ * them its newest rows (row 0 the newest token accepted before, row j + 1 guess j,
+ * as spec_tree_attention read them); with first = lengths[b] - 1 - K_b,
+ *     position first + i takes the state of position first + path[i], i = 1 .. n,
+ *     out_lengths[b] = first + 1 + n,
+ * n = num_accepted[b], path = the sequence's rows of out_path (spec_verify_tree_*).
+ * Other positions keep their states: those from the new length on hold what they
+ * held, or a row that moved.
+ *   A path rises strictly from path[0] = 0 to at most K_b; at an entry that does not,
+ *   the moves end.  n outside [0, K_b], as a verify's -1, and cu_draft entries out
+ *   of range move nothing and give out_lengths[b] = lengths[b].  A move from or to
+ *   a position below 0, or one without a page, is left out.  Lengths below 0
+ *   count as 0, above max_pages * page_size as that; NULL lengths are that.
+ *   out_lengths is at least 0.
+ * Arguments
+ *   data: the pool, read and written.  page_table int32 [batch][max_pages] with
+ *   table_stride entries between rows, or NULL: sequence b's one page is page b
+ *   (max_pages = 1, a cache with one piece per sequence).  path int32
+ *   [total_draft + batch]; num_accepted, out_lengths int32 [batch].  None of
+ *   these lies among the pool's bytes; out_lengths overlaps no input.  The pages
+ *   that hold newest rows belong to one sequence each.
+ * Errors: SV_ERR_INVALID_ARGUMENT (null or misaligned pointer, a count < 1, a
+ * stride < 0, places that overlap, an overlap as above), SV_ERR_UNSUPPORTED
+ * (max_draft > SV_MAX_DRAFT, a position of all slabs and heads of more than 2^31 - 1
+ * pieces, a piece being 16, 4, 2 or 1 bytes as the alignment of data, row_bytes and
+ * the strides allows, more than 2^30 positions of a sequence, or more than 2^32 threads), SV_ERR_HIP.
+ * Execution as for spec_verify_sample; no workspace.
+ */
+typedef struct {
+    sv_pool_t pool;
+    int32_t batch;             /* B >= 1                                      */
+    int32_t max_draft;         /* K, or the largest K_b when cu_draft != NULL */
+    int32_t total_draft;       /* sum_b K_b                                   */
+    int32_t max_pages;         /* entries of a sequence's table               */
+    int64_t table_stride;      /* entries between the tables' rows            */
+    const int32_t* cu_draft;   /* device [B+1], or NULL                       */
+    const int32_t* page_table; /* device [B][max_pages], or NULL              */
+} sv_compact_shape_t;
+
+SV_API sv_status_t spec_cache_compact(const sv_compact_shape_t* shape,
+                                void* data,
+                                const int32_t* lengths,
+                                const int32_t* path,
+                                const int32_t* num_accepted,
+                                int32_t* out_lengths,
+                                hipStream_t stream);
+
+/*
+ * The page tables of sequences that continue others: beams after a selection,
+ * samples of one prompt, or the same sequences with more or fewer positions.  Place w
+ * continues sequence s = parents[w] of the old tables: it takes over the
+ * lengths[s] positions that s holds, and pages for max(lengths[s],
+ * new_lengths[w]) positions (at most max_pages of them).
+ *   Whole pages below the length are shared: the place's table lists the parent's.
+ *   The page that the length ends in will be written by its place.  The lowest
+ *   place that takes it keeps it, unless anyone else holds it (a table outside this
+ *   call, or a place for which it is a whole page); every other one gets a free page
+ *   and a copy of the used positions, in all slabs and heads.
+ *   Pages behind the length are free ones.  Free pages are given in rising order to
+ *   the places in rising order, each place's in the order of its table.
+ *   refs[page] counts the holders of each page: every entry of an old table is one,
+ *   besides holders outside this call.  out_refs has the old tables' taken away and the new ones'
+ *   added; a page is free if it has none after the old tables' have gone and the
+ *   shared and kept ones have been added.  Sequences that nobody continues are
+ *   thereby freed.
+ *   A parent outside the old tables (-1) gives an empty table.  With beams > 0,
+ *   parents[w] counts within w's group of `beams` sequences, as
+ *   spec_beam_select returns them.  NULL parents: place w continues sequence w.
+ *   Entries behind a table's last page are -1.  out_free = free pages left; below
+ *   0, so many were missing: the last entries that found none are -1, and a copy into
+ *   them is left out.
+ * Arguments
+ *   data: the pool, read and written (fresh pages only).  page_table int32
+ *   [old][max_pages], out_table int32 [batch][max_pages], strides in entries; lengths
+ *   int32 [old] (below 0 counts as 0, above max_pages * page_size as that); parents
+ *   and new_lengths (nullable) int32 [batch]; refs and out_refs int32 [pages], which
+ *   may be one array; out_free int32 [1].  The other outputs overlap no input, and
+ *   none of these lies among the pool's bytes.
+ * Memory, execution, workspace and errors as for spec_verify_sample;
+ * SV_ERR_INVALID_ARGUMENT also as for spec_cache_compact, and for beams > 0 with batch or
+ * old no multiple of it; SV_ERR_UNSUPPORTED also for more than 2^31 - 1 table entries,
+ * old or new, more than 2^30 positions of a sequence, and pools as for
+ * spec_cache_compact.
+ */
+typedef struct {
+    sv_pool_t pool;
+    int32_t old;              /* sequences of page_table, >= 1               */
+    int32_t batch;            /* places of out_table, >= 1                   */
+    int32_t beams;            /* 0: parents count over all old sequences     */
+    int32_t max_pages;        /* entries of a sequence's table, old and new  */
+    int64_t table_stride;     /* entries between rows of page_table          */
+    int64_t out_table_stride; /* entries between rows of out_table           */
+} sv_fork_shape_t;
+
+SV_API sv_status_t spec_page_fork(const sv_fork_shape_t* shape,
+                            void* data,
+                            const int32_t* page_table,
+                            const int32_t* lengths,
+                            const int32_t* parents,
+                            const int32_t* new_lengths,
+                            const int32_t* refs,
+                            int32_t* out_table,
+                            int32_t* out_refs,
+                            int32_t* out_free,
+                            void* workspace,
+                            size_t* workspace_bytes,
+                            hipStream_t stream);
+
 /* A static, human-readable name for a status code. */
 SV_API const char* spec_verify_status_string(sv_status_t status);
 

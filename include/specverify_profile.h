@@ -78,6 +78,16 @@ SV_API sv_status_t spec_prefix_attention_profiled(const sv_profile_events_t* eve
                                                   const sv_cache_t* suffix_v, float scale, void* out, float* out_lse,
                                                   void* workspace, size_t* workspace_bytes, hipStream_t stream);
 
+SV_API sv_status_t spec_cache_compact_profiled(const sv_profile_events_t* events, const sv_compact_shape_t* shape,
+                                               void* data, const int32_t* lengths, const int32_t* path,
+                                               const int32_t* num_accepted, int32_t* out_lengths, hipStream_t stream);
+
+SV_API sv_status_t spec_page_fork_profiled(const sv_profile_events_t* events, const sv_fork_shape_t* shape, void* data,
+                                           const int32_t* page_table, const int32_t* lengths, const int32_t* parents,
+                                           const int32_t* new_lengths, const int32_t* refs, int32_t* out_table,
+                                           int32_t* out_refs, int32_t* out_free, void* workspace,
+                                           size_t* workspace_bytes, hipStream_t stream);
+
 /*
  * A plain streaming read, the practical roof the streaming passes are
  * measured against: every 16-byte block of [data, data + bytes) is loaded

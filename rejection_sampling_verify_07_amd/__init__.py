@@ -30,3 +30,9 @@ from .beam import (  # noqa: F401
     prefix_attention,
     reorder_states,
 )
+from .pages import (  # noqa: F401
+    CompactCachePlan,
+    ForkPagesPlan,
+    compact_cache,
+    fork_pages,
+)

@@ -95,13 +95,18 @@ def load_library(path: Optional[str] = None):
     lib.spec_state_reorder.argtypes = [VP, VP, VP, VP, VP]
     lib.spec_prefix_attention.restype = C.c_int
     lib.spec_prefix_attention.argtypes = [VP, VP, VP, VP, VP, VP, C.c_float, VP, VP, VP, C.POINTER(C.c_size_t), VP]
+    lib.spec_cache_compact.restype = C.c_int
+    lib.spec_cache_compact.argtypes = [VP, VP, VP, VP, VP, VP, VP]
+    lib.spec_page_fork.restype = C.c_int
+    lib.spec_page_fork.argtypes = [VP] * 11 + [C.POINTER(C.c_size_t), VP]
     lib.spec_profile_stream_read.restype = C.c_int
     lib.spec_profile_stream_read.argtypes = [C.POINTER(ProfileEventsT), VP, C.c_size_t, VP, VP]
     lib.spec_verify_status_string.restype = C.c_char_p
     lib.spec_verify_status_string.argtypes = [C.c_int]
     # benchmark entry points: the same calls with a leading events argument
     for name in ("spec_verify_sample", "spec_verify_argmax", "spec_verify_greedy", "spec_draft_sample",
-                 "spec_token_likelihood", "spec_beam_select", "spec_state_reorder", "spec_prefix_attention"):
+                 "spec_token_likelihood", "spec_beam_select", "spec_state_reorder", "spec_prefix_attention",
+                 "spec_cache_compact", "spec_page_fork"):
         f = getattr(lib, name + "_profiled")
         f.restype = C.c_int
         f.argtypes = [C.POINTER(ProfileEventsT)] + list(getattr(lib, name).argtypes)

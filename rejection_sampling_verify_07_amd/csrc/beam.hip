@@ -20,19 +20,6 @@ static_assert(SV_MAX_SELECT == sv::kBeamMaxSelect, "selection limit mismatch");
 
 namespace {
 
-// The caller's dtype field as an integer (any int may be stored there by a C caller).
-template <class Shape>
-int32_t dtype_of(const Shape* sh)
-{
-    static_assert(sizeof(sh->dtype) == sizeof(int32_t), "sv_dtype_t is an int-sized enum");
-    int32_t v;
-    memcpy(&v, &sh->dtype, sizeof v);
-    return v;
-}
-
-// A launch counts its threads in 32 bits.
-bool launchable(double workgroups, int threads) { return workgroups * threads <= (double)UINT32_MAX; }
-
 // ---- beam selection
 
 // 16-byte loads per thread of the streaming pass: 29.8 us on 512 rows of 151936 bf16 logits, against 33.7 us with 2,
@@ -118,28 +105,6 @@ sv_status_t beam_select_common(const sv_beam_shape_t* sh, const void* logits, co
 
 // ---- state reorder
 
-// Whether the places of [slabs][beams][heads][positions][row_bytes] with these
-// strides are all distinct: every stride clears the extent of the dimensions
-// inside it.  *bytes: the extent of all of them.
-bool distinct_places(const sv_state_shape_t* sh, int64_t beams, int64_t* bytes)
-{
-    int64_t size[4] = {sh->slabs, beams, sh->heads, sh->positions};
-    int64_t stride[4] = {sh->slab_stride, sh->beam_stride, sh->head_stride, sh->position_stride};
-    int64_t& extent = *bytes;
-    extent = sh->row_bytes;
-    bool done[4] = {};
-    for (int k = 0; k < 4; ++k) {
-        int at = -1;  // the smallest stride left, of the dimensions that have more than one place
-        for (int i = 0; i < 4; ++i)
-            if (!done[i] && size[i] > 1 && (at < 0 || stride[i] < stride[at])) at = i;
-        if (at < 0) return true;
-        done[at] = true;
-        if (stride[at] < extent || stride[at] > (INT64_MAX - extent) / (size[at] - 1)) return false;
-        extent += stride[at] * (size[at] - 1);
-    }
-    return true;
-}
-
 // Columns per thread of the reorder.  4-byte pieces: 2 (60 us against 71 us with 1 and 60 us with 4 on 325 MB moved
 // between 6 places, 211 / 206 / 220 us on 868 MB between 16); 16-byte pieces: 1 (77 us against 84 us with 2 on 629 MB
 // between 4 places, equal on 8 and more).
@@ -190,7 +155,10 @@ sv_status_t state_reorder_common(const sv_state_shape_t* sh, void* states, const
     const bool empty = sh->positions == 0 || sh->row_bytes == 0;
     const int64_t batch = (int64_t)sh->groups * sh->beams;
     int64_t extent = 0;
-    if (!empty && !distinct_places(sh, batch, &extent)) return SV_ERR_INVALID_ARGUMENT;
+    if (!empty && !distinct_places<4>({sh->slabs, batch, sh->heads, sh->positions},
+                                  {sh->slab_stride, sh->beam_stride, sh->head_stride, sh->position_stride},
+                                  sh->row_bytes, &extent))
+        return SV_ERR_INVALID_ARGUMENT;
     if ((states == nullptr && !empty) || parents == nullptr || !aligned(parents, 4) || !aligned(lengths, 4))
         return SV_ERR_INVALID_ARGUMENT;
     if (empty) return SV_OK;

@@ -8,7 +8,9 @@
 #include <hip/hip_ext.h>
 
 #include <stdint.h>
+#include <string.h>
 
+#include <array>
 #include <type_traits>
 
 #include "sv_common.hpp"
@@ -21,6 +23,40 @@ inline size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 
 inline int vec_of(sv_dtype_t dt) { return dt == SV_DTYPE_F32 ? 4 : 8; }
 inline size_t esize_of(sv_dtype_t dt) { return dt == SV_DTYPE_F32 ? 4 : 2; }
+
+// The caller's dtype field as an integer (any int may be stored there by a C caller).
+template <class Shape>
+int32_t dtype_of(const Shape* sh)
+{
+    static_assert(sizeof(sh->dtype) == sizeof(int32_t), "sv_dtype_t is an int-sized enum");
+    int32_t v;
+    memcpy(&v, &sh->dtype, sizeof v);
+    return v;
+}
+
+// A launch counts its threads in 32 bits.
+inline bool launchable(double workgroups, int threads) { return workgroups * threads <= (double)UINT32_MAX; }
+
+// Whether the places of N dimensions of `size` with these strides, `width` bytes each, are all distinct: every stride
+// clears the extent of the dimensions inside it.  *bytes: the extent of all of them.
+template <int N>
+bool distinct_places(const std::array<int64_t, N>& size, const std::array<int64_t, N>& stride, int64_t width,
+                     int64_t* bytes)
+{
+    int64_t& extent = *bytes;
+    extent = width;
+    bool done[N] = {};
+    for (int k = 0; k < N; ++k) {
+        int at = -1;  // the smallest stride left, of the dimensions that have more than one place
+        for (int i = 0; i < N; ++i)
+            if (!done[i] && size[i] > 1 && (at < 0 || stride[i] < stride[at])) at = i;
+        if (at < 0) return true;
+        done[at] = true;
+        if (stride[at] < extent || stride[at] > (INT64_MAX - extent) / (size[at] - 1)) return false;
+        extent += stride[at] * (size[at] - 1);
+    }
+    return true;
+}
 
 // Calls fn with std::integral_constant<int, DT> for the element type
 // (the shape check has already rejected any other value).

@@ -1,0 +1,127 @@
+"""Plain forms of the calls on trees of guesses and paged caches (numpy, loops),
+and input makers of their tests."""
+import numpy as np
+
+INT_MAX = 2 ** 31 - 1
+
+
+# --------------------------------------------------------------------------
+# paged caches: pools as numpy arrays [slabs, pages, heads, page_size, row]
+# --------------------------------------------------------------------------
+def compact_ref(pool, table, lengths, path, nacc, cu, kmax):
+    """The pool after spec_cache_compact (a copy) and the new lengths."""
+    out, (_, pages, _, size, _) = pool.copy(), pool.shape
+    total = len(path) - len(nacc)
+    new = np.zeros(len(nacc), np.int64)
+    for b in range(len(nacc)):
+        cap = size if table is None else table.shape[1] * size
+        length = cap if lengths is None else min(max(int(lengths[b]), 0), cap)
+        k0, k1 = (b * kmax, (b + 1) * kmax) if cu is None else (int(cu[b]), int(cu[b + 1]))
+        kb, n = k1 - k0, int(nacc[b])
+        bad = k0 < 0 or kb < 0 or kb > kmax or k1 > total
+        if bad or n < 0 or n > kb:
+            new[b] = length
+            continue
+        first = length - 1 - kb
+        new[b] = max(first + 1 + n, 0)
+        own = path[k0 + b:k0 + b + n + 1]
+        moves = []
+        for i in range(1, n + 1):
+            if own[i] <= own[i - 1] or own[i] > kb or own[0] != 0:
+                break
+            at = []
+            for p in (first + own[i], first + i):
+                page = -1 if p < 0 else (b if table is None else table[b, p // size])
+                at.append((int(page), int(p) % size) if 0 <= page < pages else None)
+            if own[i] != i and first + i >= 0 and None not in at:
+                moves.append(at)
+        was = pool
+        for (sp, so), (tp, to) in moves:
+            out[:, tp, :, to] = was[:, sp, :, so]
+    return out, new
+
+
+def fork_ref(pool, table, lengths, parents, refs, new_lengths=None, beams=0, places=None):
+    """spec_page_fork: the pool (a copy), the new tables, counts and free pages."""
+    out, (_, pages, _, size, _) = pool.copy(), pool.shape
+    old, most = table.shape
+    places = (len(parents) if parents is not None else old) if places is None else places
+    refs = refs.astype(np.int64).copy()
+    new = np.full((places, most), -1, np.int64)
+    for p in table.reshape(-1):
+        if 0 <= p < pages:
+            refs[p] -= 1
+    plan = []
+    for w in range(places):
+        s = w if parents is None else int(parents[w])
+        if beams and parents is not None:
+            s = w // beams * beams + s if 0 <= s < beams else -1
+        if not 0 <= s < old:
+            plan.append(None)
+            continue
+        length = min(max(int(lengths[s]), 0), most * size)
+        want = length if new_lengths is None else max(length, int(new_lengths[w]))
+        plan.append((s, length // size, length % size, min(-(-want // size), most)))
+        for i in range(length // size):
+            new[w, i] = table[s, i]
+            if 0 <= table[s, i] < pages:
+                refs[table[s, i]] += 1
+    opened, begin = {}, {}
+    for w, pl in enumerate(plan):
+        if pl is None:
+            continue
+        s, full, rest, _ = pl
+        begin[w] = full
+        if rest and 0 <= table[s, full] < pages:
+            page = int(table[s, full])
+            if page not in opened:
+                opened[page] = refs[page] == 0
+                if opened[page]:
+                    new[w, full] = page
+                    begin[w] += 1
+    for page, kept in opened.items():
+        if kept:
+            refs[page] = 1
+    free = [p for p in range(pages) if refs[p] == 0]
+    left = len(free)
+    for w, pl in enumerate(plan):
+        if pl is None:
+            continue
+        s, full, rest, need = pl
+        for i in range(begin[w], need):
+            left -= 1
+            if free:
+                new[w, i] = free.pop(0)
+                refs[new[w, i]] = 1
+        if rest and begin[w] == full and 0 <= table[s, full] < pages and new[w, full] >= 0:
+            out[:, new[w, full], :, :rest] = pool[:, table[s, full], :, :rest]
+    return out, new, refs, left
+
+
+def random_tables(rng, sequences, most, pages, lengths, size, share=0.4):
+    """Tables of sequences that hold `lengths`, some pages shared between neighbours, and their counts."""
+    spare = list(rng.permutation(pages))
+    table, refs = np.full((sequences, most), -1, np.int64), np.zeros(pages, np.int64)
+    for b in range(sequences):
+        for i in range(-(-int(lengths[b]) // size)):
+            if b > 0 and table[b - 1, i] >= 0 and (i == 0 or table[b, i - 1] == table[b - 1, i - 1]) and rng.random() < share:
+                table[b, i] = table[b - 1, i]
+            else:
+                table[b, i] = spare.pop()
+            refs[table[b, i]] += 1
+    return table, refs
+
+
+# --------------------------------------------------------------------------
+# trees: parents[j] is the row (0 .. j) that guess j extends
+# --------------------------------------------------------------------------
+def random_tree(rng, k, wide=4):
+    return np.array([max(0, j - int(rng.integers(0, wide))) for j in range(k)], np.int64)
+
+
+def way_up(parents, row):
+    """Rows from `row` up to row 0."""
+    way = [row]
+    while way[-1] > 0:
+        way.append(int(parents[way[-1] - 1]))
+    return way
