@@ -501,6 +501,60 @@ SV_API sv_status_t spec_prefix_attention(const sv_attention_shape_t* shape,
                                    hipStream_t stream);
 
 /*
+ * Verify of trees of guesses.  The guesses of a sequence may branch: guess j
+ * extends row parents[cu_draft[b] + j] of its sequence, 0 <= parent <= j, where row
+ * 0 is the newest token accepted before and row j + 1 is guess j's own, so a parent
+ * comes before its guesses.  parents (device int32 [total_draft]) NULL is the chain
+ * (parent j).  Rows are laid out as in spec_verify_sample; the row after a guess
+ * scores what follows it.
+ *   Every row r has its own token y_r.  From row 0 on, the first guess (lowest j)
+ * that extends the row and equals y of the row is accepted and its row is next; at
+ * a row without one the walk ends, and y of that row is the new token.
+ *   spec_verify_tree_greedy: y_r is the lowest index among the maxima of row r (on a
+ * chain this is spec_verify_greedy).
+ *   spec_verify_tree_sample: y_r is the inverse-CDF draw from the row's softmax at
+ * temperature T over its top-k kept set and top-p nucleus, as in
+ * spec_verify_sample, with U(b, r, 4).  Each token that the call emits is thereby
+ * drawn from the target's distribution behind the tokens before it, however the
+ * tree was made ("CS3602_FINAL_SpeDec", section 2, asks that of a speculative
+ * step; a chain of guesses x ~ q may use spec_verify_sample's test instead, which accepts more).  A row with no finite logit in its kept set has the token
+ * -1, which no guess equals.
+ * Outputs: out_tokens and out_num_accepted as for spec_verify_sample, the accepted
+ *   guesses in the order of the path; out_path (nullable) int32 [total_draft + B]:
+ *   slot cu_draft[b] + b + i holds the row of the i-th accepted guess, 0 at i = 0,
+ *   -1 behind the n-th.  A sequence whose cu_draft entries, draft ids or parents are
+ *   out of range reports num_accepted = -1 and leaves its other slots untouched.
+ * draft_row_stride is ignored.  Memory, execution, workspace and errors as for
+ * spec_verify_sample.
+ */
+SV_API sv_status_t spec_verify_tree_greedy(const sv_shape_t* shape,
+                               const void* target_logits,
+                               const int32_t* draft_ids,
+                               const int32_t* parents,
+                               int32_t* out_tokens,
+                               int32_t* out_num_accepted,
+                               int32_t* out_path,
+                               void* workspace,
+                               size_t* workspace_bytes,
+                               hipStream_t stream);
+
+SV_API sv_status_t spec_verify_tree_sample(const sv_shape_t* shape,
+                               const void* target_logits,
+                               const int32_t* draft_ids,
+                               const int32_t* parents,
+                               float temperature,
+                               int32_t top_k,
+                               float top_p,
+                               uint64_t seed,
+                               uint32_t offset,
+                               int32_t* out_tokens,
+                               int32_t* out_num_accepted,
+                               int32_t* out_path,
+                               void* workspace,
+                               size_t* workspace_bytes,
+                               hipStream_t stream);
+
+/*
  * Caches in pages.  A pool holds the states of many sequences in pages of
  * page_size positions,
  *     pool[slab][page][head][position in page][0 .. row_bytes)

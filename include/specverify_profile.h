@@ -78,6 +78,17 @@ SV_API sv_status_t spec_prefix_attention_profiled(const sv_profile_events_t* eve
                                                   const sv_cache_t* suffix_v, float scale, void* out, float* out_lse,
                                                   void* workspace, size_t* workspace_bytes, hipStream_t stream);
 
+SV_API sv_status_t spec_verify_tree_greedy_profiled(const sv_profile_events_t* events, const sv_shape_t* shape, const void* target_logits,
+                                                    const int32_t* draft_ids,
+                                                    const int32_t* parents, int32_t* out_tokens, int32_t* out_num_accepted,
+                                                    int32_t* out_path, void* workspace, size_t* workspace_bytes, hipStream_t stream);
+
+SV_API sv_status_t spec_verify_tree_sample_profiled(const sv_profile_events_t* events, const sv_shape_t* shape, const void* target_logits,
+                                                    const int32_t* draft_ids,
+                                                    const int32_t* parents, float temperature, int32_t top_k, float top_p, uint64_t seed,
+                                                    uint32_t offset, int32_t* out_tokens, int32_t* out_num_accepted, int32_t* out_path,
+                                                    void* workspace, size_t* workspace_bytes, hipStream_t stream);
+
 SV_API sv_status_t spec_cache_compact_profiled(const sv_profile_events_t* events, const sv_compact_shape_t* shape,
                                                void* data, const int32_t* lengths, const int32_t* path,
                                                const int32_t* num_accepted, int32_t* out_lengths, hipStream_t stream);

@@ -36,3 +36,9 @@ from .pages import (  # noqa: F401
     compact_cache,
     fork_pages,
 )
+from .tree import (  # noqa: F401
+    TreeGreedyPlan,
+    TreeSamplePlan,
+    verify_tree_greedy,
+    verify_tree_sample,
+)

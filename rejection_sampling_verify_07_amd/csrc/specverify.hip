@@ -20,8 +20,10 @@
 #include "sv_verify.hpp"
 #include "sv_likelihood.hpp"
 #include "sv_nucleus.hpp"
+#include "sv_tree_verify.hpp"
 
 static_assert(SV_MAX_DRAFT == sv::kMaxDraft, "draft limit mismatch");
+static_assert(SV_MAX_DRAFT + 1 == sv::kTreeMostRows && SV_MAX_DRAFT <= 2 * sv::kWave, "draft limit mismatch");
 static_assert(SV_MAX_VOCAB == sv::kMaxSeg * sv::kSeg, "vocab limit mismatch");
 static_assert(sv::kKeepCap == sv::kKeepCapList, "kept-list capacity mismatch");
 // the per-row top-p kernel groups a row's 16-byte blocks by at most 64 (adjacent lanes)
@@ -87,7 +89,7 @@ constexpr int32_t kDraftSmallRowsMin = 512;  // draft rows from which full-row d
 constexpr int32_t kXcds = SV_XCDS;
 
 enum PlanMode { PLAN_FULL = 0, PLAN_TOPK_FAST = 1, PLAN_TOPK_EXACT = 2, PLAN_GREEDY = 3 };
-enum CallKind { CALL_SAMPLE = 0, CALL_GREEDY = 1, CALL_DRAFT = 2, CALL_LIKE = 3 };
+enum CallKind { CALL_SAMPLE = 0, CALL_GREEDY = 1, CALL_DRAFT = 2, CALL_LIKE = 3, CALL_TREE = 4 };
 
 struct Plan {
     PlanMode mode;
@@ -119,7 +121,7 @@ int32_t dtype_field(const sv_shape_t* sh)
 
 sv_status_t check_shape(const sv_shape_t* sh, CallKind kind)
 {
-    const bool need_draft_rows = kind != CALL_GREEDY;
+    const bool need_draft_rows = kind != CALL_GREEDY && kind != CALL_TREE;
     if (sh == nullptr) return SV_ERR_INVALID_ARGUMENT;
     if (sh->batch < 1 || sh->vocab < 1 || sh->max_draft < 0 || sh->total_draft < 0)
         return SV_ERR_INVALID_ARGUMENT;
@@ -375,34 +377,36 @@ sv_status_t run_sample(const sv_shape_t* sh, const Plan& p, const void* tgt, con
     return launch_status();
 }
 
-template <int DT>
-sv_status_t run_draft(const sv_shape_t* sh, const Plan& p, const void* drf, float c, uint64_t seed, uint32_t offset,
-                      int32_t* out_ids, void* ws, hipStream_t stream, const sv_profile_events_t* prof)
+// One draw per streamed row: the draft rows, or (TREE) the target rows of trees of guesses.
+template <int DT, bool TREE>
+sv_status_t run_draws(const sv_shape_t* sh, const Plan& p, const void* rows, int64_t row_stride, float c, uint64_t seed,
+                      uint32_t offset, int32_t* out_ids, void* ws, hipStream_t stream, const sv_profile_events_t* prof)
 {
     const size_t es = esize_of(sh->dtype);
-    // the draft rows are the streamed rows
-    const sv::RowSet rs{static_cast<const char*>(drf), nullptr, (int64_t)(sh->draft_row_stride * (int64_t)es), 0,
-                        p.rows_t};
+    // the drawn rows are the streamed rows
+    const sv::RowSet rs{static_cast<const char*>(rows), nullptr, (int64_t)(row_stride * (int64_t)es), 0, p.rows_t};
     sv::VerifyArgs va = base_args(sh, p, rs, c, seed, offset);
     va.out_tokens = out_ids;
     if (run_stats<DT>(sh, p, rs, c, ws, stream, va, prof) != SV_OK) return SV_ERR_HIP;
-    const dim3 grid((uint32_t)sh->batch, (uint32_t)sh->max_draft);  // max_draft <= SV_MAX_DRAFT fits grid y
+    // max_draft <= SV_MAX_DRAFT fits grid y
+    const dim3 grid((uint32_t)sh->batch, (uint32_t)sh->max_draft + (TREE ? 1u : 0u));
     if (!p.desc) {
         // one chunk per row is walked: with many rows, smaller workgroups,
         // two per CU (measured: 150 -> 130 us on 2048 rows of 128256; slower
         // on 256 rows of 50304, which do not fill the chip either way)
-        if (sh->total_draft >= kDraftSmallRowsMin) {
-            hipLaunchKernelGGL((sv::draft_draw_kernel<DT, false, sv::kDraftChunkThreads>), grid,
+        if (p.rows_t >= kDraftSmallRowsMin) {
+            hipLaunchKernelGGL((sv::draft_draw_kernel<DT, false, sv::kDraftChunkThreads, TREE>), grid,
                                dim3(sv::kDraftChunkThreads), 0, stream, va);
         } else {
-            hipLaunchKernelGGL((sv::draft_draw_kernel<DT, false, kVerifyFullThreads>), grid, dim3(kVerifyFullThreads),
-                               0, stream, va);
+            hipLaunchKernelGGL((sv::draft_draw_kernel<DT, false, kVerifyFullThreads, TREE>), grid,
+                               dim3(kVerifyFullThreads), 0, stream, va);
         }
     } else if (p.mode == PLAN_FULL) {
-        hipLaunchKernelGGL((sv::draft_draw_kernel<DT, true, kVerifyFullThreads>), grid, dim3(kVerifyFullThreads), 0,
-                           stream, va);
+        hipLaunchKernelGGL((sv::draft_draw_kernel<DT, true, kVerifyFullThreads, TREE>), grid, dim3(kVerifyFullThreads),
+                           0, stream, va);
     } else {
-        hipLaunchKernelGGL((sv::draft_draw_kernel<DT, true, sv::kThreads>), grid, dim3(sv::kThreads), 0, stream, va);
+        hipLaunchKernelGGL((sv::draft_draw_kernel<DT, true, sv::kThreads, TREE>), grid, dim3(sv::kThreads), 0, stream,
+                           va);
     }
     return launch_status();
 }
@@ -459,9 +463,9 @@ sv_status_t run_likelihood(const sv_shape_t* sh, const Plan& p, const void* tgt,
     return launch_status();
 }
 
+// The argmax pass over the target rows: per-chunk maxima in the workspace.
 template <int DT>
-sv_status_t run_greedy(const sv_shape_t* sh, const Plan& p, const void* tgt, const int32_t* ids,
-                       int32_t* out_tokens, int32_t* out_nacc, void* ws, hipStream_t stream,
+sv_status_t run_argmax(const sv_shape_t* sh, const Plan& p, const void* tgt, void* ws, hipStream_t stream,
                        const sv_profile_events_t* prof)
 {
     const size_t es = esize_of(sh->dtype);
@@ -476,9 +480,17 @@ sv_status_t run_greedy(const sv_shape_t* sh, const Plan& p, const void* tgt, con
         launch_stream(prof, sv::row_stats_kernel<DT, sv::MODE_ARGMAX, kLoads, kNT>, grid_stream, stream, rs,
                       sh->vocab, p.nchunk, (int32_t)grid_stream, 0.0f, (void*)part, (int32_t*)nullptr, (int32_t)0);
     }
-    if (launch_status() != SV_OK) return SV_ERR_HIP;
-    sv::GreedyArgs ga{sh->cu_draft, sh->batch, sh->max_draft, sh->total_draft, sh->vocab, ids, part, p.nchunk,
-                      out_tokens, out_nacc};
+    return launch_status();
+}
+
+template <int DT>
+sv_status_t run_greedy(const sv_shape_t* sh, const Plan& p, const void* tgt, const int32_t* ids,
+                       int32_t* out_tokens, int32_t* out_nacc, void* ws, hipStream_t stream,
+                       const sv_profile_events_t* prof)
+{
+    if (run_argmax<DT>(sh, p, tgt, ws, stream, prof) != SV_OK) return SV_ERR_HIP;
+    sv::GreedyArgs ga{sh->cu_draft, sh->batch, sh->max_draft, sh->total_draft, sh->vocab, ids,
+                      ws_at<sv::PartialArg>(ws, p.off_partials), p.nchunk, out_tokens, out_nacc};
     hipLaunchKernelGGL(sv::greedy_kernel, dim3((sh->batch + sv::kWaves - 1) / sv::kWaves), dim3(sv::kThreads), 0,
                        stream, ga);
     return launch_status();
@@ -584,6 +596,86 @@ sv_status_t verify_greedy_common(const sv_shape_t* shape, const void* target_log
     });
 }
 
+// Checks that both tree verifies share; *done: a workspace query was answered.
+sv_status_t tree_checks(const sv_shape_t* shape, const void* target_logits, const int32_t* draft_ids,
+                        const int32_t* parents, const int32_t* out_tokens, const int32_t* out_num_accepted,
+                        const int32_t* out_path, size_t need, void* workspace, size_t* workspace_bytes, bool* done)
+{
+    *done = workspace == nullptr;
+    if (*done) {
+        *workspace_bytes = need;
+        return SV_OK;
+    }
+    if (target_logits == nullptr || out_tokens == nullptr || out_num_accepted == nullptr ||
+        (shape->total_draft > 0 && draft_ids == nullptr))
+        return SV_ERR_INVALID_ARGUMENT;
+    if (!aligned(target_logits, esize_of(shape->dtype)) || !aligned(out_tokens, 4) || !aligned(out_num_accepted, 4) ||
+        !aligned(out_path, 4) || !aligned(draft_ids, 4) || !aligned(parents, 4) || !aligned(workspace, kAlign))
+        return SV_ERR_INVALID_ARGUMENT;
+    return *workspace_bytes < need ? SV_ERR_WORKSPACE_TOO_SMALL : SV_OK;
+}
+
+sv::TreeWalkArgs walk_args(const sv_shape_t* sh, const Plan& p, const int32_t* ids, const int32_t* parents,
+                           int32_t* out_tokens, int32_t* out_num_accepted, int32_t* out_path)
+{
+    return sv::TreeWalkArgs{sh->cu_draft, ids, parents, sh->batch, sh->max_draft, sh->total_draft, sh->vocab, p.nchunk,
+                            nullptr, nullptr, out_tokens, out_num_accepted, out_path};
+}
+
+sv_status_t tree_greedy_common(const sv_shape_t* shape, const void* target_logits, const int32_t* draft_ids,
+                               const int32_t* parents, int32_t* out_tokens, int32_t* out_num_accepted,
+                               int32_t* out_path, void* workspace, size_t* workspace_bytes, hipStream_t stream,
+                               const sv_profile_events_t* prof)
+{
+    if (workspace_bytes == nullptr) return SV_ERR_INVALID_ARGUMENT;
+    sv_status_t st = check_shape(shape, CALL_GREEDY);
+    if (st != SV_OK) return st;
+    const Plan p = make_plan(shape, CALL_GREEDY, 0);
+    if ((int64_t)p.rows_t * p.nchunk > INT32_MAX) return SV_ERR_UNSUPPORTED;
+    bool done;
+    st = tree_checks(shape, target_logits, draft_ids, parents, out_tokens, out_num_accepted, out_path, p.bytes,
+                     workspace, workspace_bytes, &done);
+    if (st != SV_OK || done) return st;
+    st = by_dtype(shape->dtype, [&](auto dt) {
+        return run_argmax<decltype(dt)::value>(shape, p, target_logits, workspace, stream, prof);
+    });
+    if (st != SV_OK) return st;
+    sv::TreeWalkArgs a = walk_args(shape, p, draft_ids, parents, out_tokens, out_num_accepted, out_path);
+    a.partials = ws_at<sv::PartialArg>(workspace, p.off_partials);
+    hipLaunchKernelGGL((sv::tree_walk_kernel<true>), dim3(shape->batch), dim3(sv::kThreads), 0, stream, a);
+    return launch_status();
+}
+
+sv_status_t tree_sample_common(const sv_shape_t* shape, const void* target_logits, const int32_t* draft_ids,
+                               const int32_t* parents, float temperature, int32_t top_k, float top_p, uint64_t seed,
+                               uint32_t offset, int32_t* out_tokens, int32_t* out_num_accepted, int32_t* out_path,
+                               void* workspace, size_t* workspace_bytes, hipStream_t stream,
+                               const sv_profile_events_t* prof)
+{
+    if (workspace_bytes == nullptr) return SV_ERR_INVALID_ARGUMENT;
+    sv_status_t st = check_shape(shape, CALL_TREE);
+    if (st != SV_OK) return st;
+    if (!filters_ok(shape, temperature, top_k, top_p)) return SV_ERR_INVALID_ARGUMENT;
+    const Plan p = make_plan(shape, CALL_TREE, top_k, top_p);
+    if (((int64_t)p.rows + kXcds) * p.nchunk > INT32_MAX) return SV_ERR_UNSUPPORTED;
+    const size_t need = align_up(p.bytes + (size_t)p.rows_t * sizeof(int32_t));  // the rows' tokens last
+    bool done;
+    st = tree_checks(shape, target_logits, draft_ids, parents, out_tokens, out_num_accepted, out_path, need, workspace,
+                     workspace_bytes, &done);
+    if (st != SV_OK || done) return st;
+    int32_t* tokens = ws_at<int32_t>(workspace, p.bytes);
+    const float c = scale_of(temperature);
+    st = by_dtype(shape->dtype, [&](auto dt) {
+        return run_draws<decltype(dt)::value, true>(shape, p, target_logits, shape->target_row_stride, c, seed, offset,
+                                                    tokens, workspace, stream, prof);
+    });
+    if (st != SV_OK) return st;
+    sv::TreeWalkArgs a = walk_args(shape, p, draft_ids, parents, out_tokens, out_num_accepted, out_path);
+    a.row_tokens = tokens;
+    hipLaunchKernelGGL((sv::tree_walk_kernel<false>), dim3(shape->batch), dim3(sv::kThreads), 0, stream, a);
+    return launch_status();
+}
+
 sv_status_t draft_sample_common(const sv_shape_t* shape, const void* draft_logits, float temperature, int32_t top_k,
                               float top_p, uint64_t seed, uint32_t offset, int32_t* out_ids, void* workspace,
                               size_t* workspace_bytes, hipStream_t stream,
@@ -609,8 +701,8 @@ sv_status_t draft_sample_common(const sv_shape_t* shape, const void* draft_logit
 
     const float c = scale_of(temperature);
     return by_dtype(shape->dtype, [&](auto dt) {
-        return run_draft<decltype(dt)::value>(shape, p, draft_logits, c, seed, offset, out_ids, workspace, stream,
-                                              prof);
+        return run_draws<decltype(dt)::value, false>(shape, p, draft_logits, shape->draft_row_stride, c, seed, offset,
+                                                     out_ids, workspace, stream, prof);
     });
 }
 
@@ -749,6 +841,23 @@ sv_status_t spec_token_likelihood(const sv_shape_t* shape, const void* target_lo
                                    out_beta, out_nll, workspace, workspace_bytes, stream, nullptr);
 }
 
+sv_status_t spec_verify_tree_greedy(const sv_shape_t* shape, const void* target_logits, const int32_t* draft_ids,
+                                    const int32_t* parents, int32_t* out_tokens, int32_t* out_num_accepted,
+                                    int32_t* out_path, void* workspace, size_t* workspace_bytes, hipStream_t stream)
+{
+    return tree_greedy_common(shape, target_logits, draft_ids, parents, out_tokens, out_num_accepted, out_path, workspace,
+                              workspace_bytes, stream, nullptr);
+}
+
+sv_status_t spec_verify_tree_sample(const sv_shape_t* shape, const void* target_logits, const int32_t* draft_ids,
+                                    const int32_t* parents, float temperature, int32_t top_k, float top_p, uint64_t seed,
+                                    uint32_t offset, int32_t* out_tokens, int32_t* out_num_accepted, int32_t* out_path,
+                                    void* workspace, size_t* workspace_bytes, hipStream_t stream)
+{
+    return tree_sample_common(shape, target_logits, draft_ids, parents, temperature, top_k, top_p, seed, offset, out_tokens,
+                              out_num_accepted, out_path, workspace, workspace_bytes, stream, nullptr);
+}
+
 const char* spec_verify_status_string(sv_status_t status)
 {
     switch (status) {
@@ -814,6 +923,25 @@ sv_status_t spec_token_likelihood_profiled(const sv_profile_events_t* events, co
 {
     return token_likelihood_common(shape, target_logits, draft_logits, tokens, temperature, top_k, top_p, out_terms,
                                    out_beta, out_nll, workspace, workspace_bytes, stream, events);
+}
+
+sv_status_t spec_verify_tree_greedy_profiled(const sv_profile_events_t* events, const sv_shape_t* shape, const void* target_logits,
+                                             const int32_t* draft_ids,
+                                             const int32_t* parents, int32_t* out_tokens, int32_t* out_num_accepted,
+                                             int32_t* out_path, void* workspace, size_t* workspace_bytes, hipStream_t stream)
+{
+    return tree_greedy_common(shape, target_logits, draft_ids, parents, out_tokens, out_num_accepted, out_path, workspace,
+                              workspace_bytes, stream, events);
+}
+
+sv_status_t spec_verify_tree_sample_profiled(const sv_profile_events_t* events, const sv_shape_t* shape, const void* target_logits,
+                                             const int32_t* draft_ids,
+                                             const int32_t* parents, float temperature, int32_t top_k, float top_p, uint64_t seed,
+                                             uint32_t offset, int32_t* out_tokens, int32_t* out_num_accepted, int32_t* out_path,
+                                             void* workspace, size_t* workspace_bytes, hipStream_t stream)
+{
+    return tree_sample_common(shape, target_logits, draft_ids, parents, temperature, top_k, top_p, seed, offset, out_tokens,
+                              out_num_accepted, out_path, workspace, workspace_bytes, stream, events);
 }
 
 sv_status_t spec_profile_stream_read(const sv_profile_events_t* events, const void* data, size_t bytes, uint32_t* sink,

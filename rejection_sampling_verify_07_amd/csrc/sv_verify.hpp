@@ -1135,8 +1135,10 @@ __global__ __launch_bounds__(NT) void verify_split_kernel(SplitArgs sa)
 // the same streaming passes as the verify's, and the draw is the verify's
 // extra-token draw: over the kept list after a top-k select, over the full
 // row (16 waves keep its re-read in flight) otherwise.
+//   TREE: the rows are the target rows of a tree of guesses, row cu[b] + b + k
+// for k = 0 .. K_b, each with its own draw by U(b, k, 4).
 // ---------------------------------------------------------------------------
-template <int DT, bool FROM_DESC, int NT>
+template <int DT, bool FROM_DESC, int NT, bool TREE = false>
 __global__ __launch_bounds__(NT, NT == kDraftChunkThreads ? 4 : 1) void draft_draw_kernel(VerifyArgs a)
 {
     __shared__ DrawLds<NT> s_draw;
@@ -1154,9 +1156,9 @@ __global__ __launch_bounds__(NT, NT == kDraftChunkThreads ? 4 : 1) void draft_dr
         k0 = b * a.kmax;
         kb = a.kmax;
     }
-    if (k >= kb) return;
-    const int32_t row = k0 + k;
-    const double u = uniform24(a.seed, (uint32_t)b, (uint32_t)k, 3u, a.offset);
+    if (TREE ? k > kb : k >= kb) return;
+    const int32_t row = TREE ? k0 + b + k : k0 + k;
+    const double u = uniform24(a.seed, (uint32_t)b, (uint32_t)k, TREE ? 4u : 3u, a.offset);
 
     if constexpr (FROM_DESC) {
         if (threadIdx.x == 0) {

@@ -1,0 +1,89 @@
+"""Argument checks of the calls on trees of guesses: no GPU is needed, nothing
+here reaches a launch."""
+import ctypes as C
+
+import pytest
+import torch
+
+from tree_util import walk_ref
+
+FAKE = 1 << 40  # never dereferenced
+
+
+@pytest.fixture(scope="module")
+def T():
+    import os
+
+    from rejection_sampling_verify_07_amd import binding, tree
+
+    if not os.path.exists(binding.LIB_PATH):
+        from rejection_sampling_verify_07_amd import build
+
+        build.build()
+    binding.load_library()
+    return tree
+
+
+@pytest.fixture(scope="module")
+def lib(T):
+    return T.load_library()
+
+
+def _verify(T, lib, name, logits=FAKE, ids=FAKE, parents=FAKE, filters=(1.0, 0, 1.0, 0, 0), o=(FAKE, FAKE, FAKE), ws=None,
+            have=0, **kw):
+    d = dict(batch=2, max_draft=4, total_draft=8, vocab=1000, dtype=1, target_row_stride=1000, draft_row_stride=0)
+    d.update(kw)
+    n = C.c_size_t(have)
+    f = filters if name == "spec_verify_tree_sample" else ()
+    st = getattr(lib, name)(C.byref(T._b.ShapeT(**d)), logits, ids, parents, *f, *o, ws, C.byref(n), None)
+    return st, n.value
+
+
+CALLS = ("spec_verify_tree_greedy", "spec_verify_tree_sample")
+
+
+@pytest.mark.parametrize("name", CALLS)
+@pytest.mark.parametrize("kw,code", [
+    (dict(), 0), (dict(batch=0), 1), (dict(vocab=0), 1), (dict(max_draft=-1), 1), (dict(total_draft=7), 1),
+    (dict(total_draft=9, cu_draft=FAKE), 1), (dict(cu_draft=FAKE + 2), 1), (dict(target_row_stride=999), 1),
+    (dict(dtype=3), 1), (dict(max_draft=129, total_draft=258), 2), (dict(max_draft=128, total_draft=256), 0),
+    (dict(vocab=(1 << 20) + 1, target_row_stride=1 << 21), 2), (dict(max_draft=0, total_draft=0), 0)])
+def test_verify_shapes(T, lib, name, kw, code):
+    st, need = _verify(T, lib, name, **kw)
+    assert st == code and (code or (need > 0 and need % 256 == 0))
+
+
+@pytest.mark.parametrize("filters,code", [((0.0, 0, 1.0, 0, 0), 1), ((float("nan"), 0, 1.0, 0, 0), 1), ((1.0, -1, 1.0, 0, 0), 1),
+                                          ((1.0, 1001, 1.0, 0, 0), 1), ((1.0, 0, 0.0, 0, 0), 1), ((1.0, 0, 1.1, 0, 0), 1),
+                                          ((1e-39, 0, 1.0, 0, 0), 1), ((0.7, 50, 0.9, 0, 0), 0)])
+def test_verify_filters(T, lib, filters, code):
+    assert _verify(T, lib, "spec_verify_tree_sample", filters=filters)[0] == code
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_verify_pointers(T, lib, name):
+    need = _verify(T, lib, name)[1]
+    ok = dict(ws=FAKE, have=need)
+    for bad in (dict(logits=None), dict(logits=FAKE + 1), dict(ids=None), dict(ids=FAKE + 2), dict(parents=FAKE + 2),
+                dict(o=(None, FAKE, FAKE)), dict(o=(FAKE, None, FAKE)), dict(o=(FAKE, FAKE, FAKE + 1)),
+                dict(o=(FAKE + 2, FAKE, FAKE)), dict(ws=FAKE + 128)):
+        assert _verify(T, lib, name, **{**ok, **bad})[0] == 1, bad
+    assert _verify(T, lib, name, ws=FAKE, have=need - 1)[0] == 3
+
+
+def test_verify_binding_refusals(T):
+    x, i = torch.zeros(10, 100), torch.zeros(8, dtype=torch.int32)
+    with pytest.raises(ValueError, match="2-D"):
+        T.verify_tree_greedy(x[0], i)
+    with pytest.raises(ValueError, match="GPU"):
+        T.verify_tree_greedy(x, i)
+    with pytest.raises(ValueError, match="B\\*\\(K\\+1\\)"):
+        T.verify_tree_greedy(x, i[:7])
+    with pytest.raises(ValueError, match="max_draft"):
+        T.verify_tree_sample(x, i, max_draft=3)
+
+
+def test_oracle_of_walks():
+    assert walk_ref([5, 1, 7, 2], [5, 6, 7], [0, 0, 2], 9) == ([5, 1, -1, -1], 1, [0, 1, -1, -1])
+    assert walk_ref([6, 1, 7, 2], [5, 6, 7], [0, 0, 2], 9) == ([6, 7, 2, -1], 2, [0, 2, 3, -1])
+    assert walk_ref([6], [], [], 9) == ([6], 0, [0]) and walk_ref([6, 1], [9], [0], 9) is None

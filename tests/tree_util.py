@@ -125,3 +125,19 @@ def way_up(parents, row):
     while way[-1] > 0:
         way.append(int(parents[way[-1] - 1]))
     return way
+
+
+def walk_ref(tokens, ids, parents, vocab):
+    """The walk over one sequence: tokens [K + 1], ids and parents [K].  (tokens out, accepted, path), or None."""
+    k = len(ids)
+    if any(not 0 <= int(x) < vocab for x in ids) or any(not 0 <= int(p) <= j for j, p in enumerate(parents)):
+        return None
+    path = [0]
+    while True:
+        follow = [j + 1 for j in range(k) if parents[j] == path[-1] and ids[j] == tokens[path[-1]]]
+        if not follow:
+            break
+        path.append(follow[0])
+    n = len(path) - 1
+    out = [int(tokens[r]) for r in path] + [-1] * (k - n)
+    return out, n, path + [-1] * (k - n)
