@@ -555,6 +555,81 @@ SV_API sv_status_t spec_verify_tree_sample(const sv_shape_t* shape,
                                hipStream_t stream);
 
 /*
+ * Edits of logits before a verify, a draft's draw or a selection: penalties for
+ * tokens already written, biases and grammar masks.  The rows are those of
+ * spec_verify_sample's target (row cu_draft[b] + b + k, k = 0 .. K_b; K = 0: one row
+ * per sequence, as a plain step or a draft model's step has).
+ *   Of a token v in row k of sequence b: seen(v) if it is among the first lengths[b] tokens
+ * of tokens[b], or a guess on the row's way up (the guesses that rows 1 .. k of
+ * a chain, or of the tree given by parents, have put behind the newest token, the
+ * row's own included); n(v) how often it is among tokens[b][prompt_lengths[b] ..] up to the length and those guesses.
+ *     x = l > 0 ? l / repetition[b] : l * repetition[b]      if seen(v)
+ *     x = x - frequency[b] * n(v) - presence[b]              if n(v) > 0
+ *     x = x + bias(v)                                        if v has one
+ *     x = -inf                                               if the row's mask lacks v
+ * in this order, in fp32, rounded to dtype once (as to any other value: a
+ * result beyond the type's range becomes infinite).  Elements that none of this
+ * concerns keep their bits.
+ *   bias: entries cu_bias[b] .. cu_bias[b+1] - 1 of bias_ids and bias_values; of an id given twice the last
+ * entry counts.  Tokens, guesses and bias ids outside [0, vocab) are ignored, and a parent
+ * outside [0, j] counts as 0.  Lengths below 0 count as 0, above max_tokens as that.
+ * A sequence with repetition 1, presence 0 and frequency 0 has no penalties.  A sequence whose cu_draft entries
+ * are out of range has its rows left as they were.
+ *   masks: row m allows v where bit v % 32 of masks[m * mask_stride + v / 32] is
+ * set.  Row r of the logits goes by mask mask_rows[r], or r where mask_rows is
+ * NULL; an index outside [0, num_masks), as -1, is no mask.
+ * Arguments
+ *   logits and out [total_draft + batch, stride] in shape->dtype; out may be logits itself (with the same
+ *   stride), otherwise they lie apart and every element of the vocabulary is
+ *   written.  In place only what changes is written.  NULL in sv_adjust_t: tokens
+ *   none, lengths max_tokens, prompt_lengths 0, repetition 1, presence and frequency 0,
+ *   cu_bias all entries for every sequence, masks none; draft_ids NULL: no guess
+ *   counts.  out overlaps no other input.  repetition > 0.
+ * Errors: SV_ERR_INVALID_ARGUMENT (null or misaligned pointer, counts or strides as in spec_verify_sample,
+ * token_stride < max_tokens, a mask_stride or num_masks too small, logits and out that
+ * overlap), SV_ERR_UNSUPPORTED (limits as in spec_verify_sample, more than 2^30
+ * tokens of a sequence, more than 2^32 threads), SV_ERR_HIP.  Execution as for
+ * spec_verify_sample; no workspace.
+ */
+typedef struct {
+    int32_t batch;             /* B >= 1                                      */
+    int32_t max_draft;         /* K, or the largest K_b when cu_draft != NULL */
+    int32_t total_draft;       /* sum_b K_b                                   */
+    int32_t vocab;             /* V >= 1                                      */
+    sv_dtype_t dtype;          /* element type of logits and out              */
+    int64_t row_stride;        /* elements between rows of logits, >= V       */
+    int64_t out_row_stride;    /* elements between rows of out, >= V          */
+    const int32_t* cu_draft;   /* device [B+1], or NULL                       */
+    const int32_t* draft_ids;  /* device [total_draft], or NULL               */
+    const int32_t* parents;    /* device [total_draft], or NULL: chains       */
+} sv_adjust_shape_t;
+
+typedef struct {
+    const int32_t* tokens;         /* device [B][max_tokens], or NULL      */
+    int64_t token_stride;          /* entries between its rows             */
+    int32_t max_tokens;
+    int32_t total_bias;            /* entries of bias_ids and bias_values  */
+    const int32_t* lengths;        /* device [B], or NULL                  */
+    const int32_t* prompt_lengths; /* device [B], or NULL                  */
+    const float* repetition;       /* device [B], or NULL                  */
+    const float* presence;         /* device [B], or NULL                  */
+    const float* frequency;        /* device [B], or NULL                  */
+    const int32_t* bias_ids;       /* device [total_bias], or NULL         */
+    const float* bias_values;      /* device [total_bias], or NULL         */
+    const int32_t* cu_bias;        /* device [B+1], or NULL                */
+    const uint32_t* masks;         /* device [num_masks][mask_stride], or NULL */
+    int64_t mask_stride;           /* words between masks, >= (V + 31) / 32 */
+    int32_t num_masks;
+    const int32_t* mask_rows;      /* device [total_draft + B], or NULL    */
+} sv_adjust_t;
+
+SV_API sv_status_t spec_adjust_logits(const sv_adjust_shape_t* shape,
+                               const sv_adjust_t* adjust,
+                               const void* logits,
+                               void* out,
+                               hipStream_t stream);
+
+/*
  * Caches in pages.  A pool holds the states of many sequences in pages of
  * page_size positions,
  *     pool[slab][page][head][position in page][0 .. row_bytes)

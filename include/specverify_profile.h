@@ -89,6 +89,10 @@ SV_API sv_status_t spec_verify_tree_sample_profiled(const sv_profile_events_t* e
                                                     uint32_t offset, int32_t* out_tokens, int32_t* out_num_accepted, int32_t* out_path,
                                                     void* workspace, size_t* workspace_bytes, hipStream_t stream);
 
+SV_API sv_status_t spec_adjust_logits_profiled(const sv_profile_events_t* events, const sv_adjust_shape_t* shape,
+                                               const sv_adjust_t* adjust, const void* logits, void* out,
+                                               hipStream_t stream);
+
 SV_API sv_status_t spec_cache_compact_profiled(const sv_profile_events_t* events, const sv_compact_shape_t* shape,
                                                void* data, const int32_t* lengths, const int32_t* path,
                                                const int32_t* num_accepted, int32_t* out_lengths, hipStream_t stream);

@@ -37,8 +37,10 @@ from .pages import (  # noqa: F401
     fork_pages,
 )
 from .tree import (  # noqa: F401
+    AdjustLogitsPlan,
     TreeGreedyPlan,
     TreeSamplePlan,
+    adjust_logits,
     verify_tree_greedy,
     verify_tree_sample,
 )

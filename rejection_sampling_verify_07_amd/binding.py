@@ -100,6 +100,8 @@ def load_library(path: Optional[str] = None):
     lib.spec_verify_tree_sample.restype = C.c_int
     lib.spec_verify_tree_sample.argtypes = [VP, VP, VP, VP, C.c_float, C.c_int32, C.c_float, C.c_uint64, C.c_uint32,
                                             VP, VP, VP, VP, C.POINTER(C.c_size_t), VP]
+    lib.spec_adjust_logits.restype = C.c_int
+    lib.spec_adjust_logits.argtypes = [VP, VP, VP, VP, VP]
     lib.spec_cache_compact.restype = C.c_int
     lib.spec_cache_compact.argtypes = [VP, VP, VP, VP, VP, VP, VP]
     lib.spec_page_fork.restype = C.c_int
@@ -111,7 +113,8 @@ def load_library(path: Optional[str] = None):
     # benchmark entry points: the same calls with a leading events argument
     for name in ("spec_verify_sample", "spec_verify_argmax", "spec_verify_greedy", "spec_draft_sample",
                  "spec_token_likelihood", "spec_beam_select", "spec_state_reorder", "spec_prefix_attention",
-                 "spec_cache_compact", "spec_page_fork", "spec_verify_tree_greedy", "spec_verify_tree_sample"):
+                 "spec_cache_compact", "spec_page_fork", "spec_verify_tree_greedy", "spec_verify_tree_sample",
+                 "spec_adjust_logits"):
         f = getattr(lib, name + "_profiled")
         f.restype = C.c_int
         f.argtypes = [C.POINTER(ProfileEventsT)] + list(getattr(lib, name).argtypes)

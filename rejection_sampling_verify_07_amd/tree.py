@@ -1,6 +1,6 @@
-"""ctypes binding of the calls on trees of guesses (spec_verify_tree_greedy,
-spec_verify_tree_sample; include/specverify.h): argument marshalling only.
-Streams, devices and plans are as in beam.py.
+"""ctypes binding of the calls on trees of guesses (spec_adjust_logits,
+spec_verify_tree_greedy, spec_verify_tree_sample; include/specverify.h): argument
+marshalling only.  Streams, devices and plans are as in beam.py.
 """
 from __future__ import annotations
 
@@ -12,6 +12,141 @@ import torch
 from . import binding as _b
 from .beam import _DevicePlan, _vector, _workspace
 from .binding import _check, _on, load_library
+
+
+class AdjustShapeT(C.Structure):
+    """sv_adjust_shape_t."""
+    _fields_ = [("batch", C.c_int32), ("max_draft", C.c_int32), ("total_draft", C.c_int32), ("vocab", C.c_int32),
+                ("dtype", C.c_int32), ("row_stride", C.c_int64), ("out_row_stride", C.c_int64), ("cu_draft", C.c_void_p),
+                ("draft_ids", C.c_void_p), ("parents", C.c_void_p)]
+
+
+class AdjustT(C.Structure):
+    """sv_adjust_t."""
+    _fields_ = ([("tokens", C.c_void_p), ("token_stride", C.c_int64), ("max_tokens", C.c_int32),
+                 ("total_bias", C.c_int32)]
+                + [(n, C.c_void_p) for n in ("lengths", "prompt_lengths", "repetition", "presence", "frequency",
+                                             "bias_ids", "bias_values", "cu_bias", "masks")]
+                + [("mask_stride", C.c_int64), ("num_masks", C.c_int32), ("mask_rows", C.c_void_p)])
+
+
+def _matrix(t, name, dtype, dev):
+    """Row stride of a 2-D tensor whose rows are contiguous."""
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D, got {tuple(t.shape)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device} but the call runs on {dev}")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have unit stride in its last dimension")
+    # (a single row may report any stride)
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+class AdjustLogitsPlan(_DevicePlan):
+    """spec_adjust_logits with every argument marshalled once: __call__ enqueues
+    one call and returns `out`, the same tensor every time.  See adjust_logits."""
+
+    name = "spec_adjust_logits"
+
+    def __init__(self, logits, tokens=None, lengths=None, prompt_lengths=None, repetition=None, presence=None,
+                 frequency=None, bias_ids=None, bias_values=None, cu_bias=None, masks=None, mask_rows=None,
+                 draft_ids=None, parents=None, cu_draft=None, max_draft=None, out=None, stream=None):
+        lib = load_library()
+        if logits.dim() != 2 or logits.shape[0] < 1 or logits.shape[1] < 1:
+            raise ValueError("logits must be a 2-D tensor [sum(K_b + 1), vocab]")
+        dev = logits.device
+        if dev.type != "cuda":
+            raise ValueError("logits must be on a GPU")
+        rows, vocab = logits.shape
+        # sequences: what tells their number first
+        counts = [("cu_draft", cu_draft, -1), ("tokens", tokens, 0), ("lengths", lengths, 0), ("repetition", repetition, 0),
+                  ("presence", presence, 0), ("frequency", frequency, 0), ("cu_bias", cu_bias, -1)]
+        batch = next((t.shape[0] + extra for _, t, extra in counts if t is not None),
+                     rows if draft_ids is None else rows - draft_ids.numel())
+        if batch < 1 or batch > rows:
+            raise ValueError(f"{rows} rows do not fit {batch} sequences")
+        total = rows - batch
+        if cu_draft is None:
+            if total % batch != 0:
+                raise ValueError("logits must have batch * (K + 1) rows; pass cu_draft for ragged K")
+            if max_draft is not None and max_draft != total // batch:
+                raise ValueError("max_draft does not match the uniform draft length")
+            max_draft = total // batch
+        sizes = {"cu_draft": batch + 1, "draft_ids": total, "parents": total, "lengths": batch, "prompt_lengths": batch,
+                 "repetition": batch, "presence": batch, "frequency": batch, "cu_bias": batch + 1, "mask_rows": rows}
+        real = ("repetition", "presence", "frequency")
+        given = dict(cu_draft=cu_draft, draft_ids=draft_ids, parents=parents, lengths=lengths,
+                     prompt_lengths=prompt_lengths, repetition=repetition, presence=presence, frequency=frequency,
+                     cu_bias=cu_bias, mask_rows=mask_rows)
+        at = {n: None if t is None else _vector(t, n, sizes[n], torch.float32 if n in real else torch.int32, dev)
+              for n, t in given.items()}
+        if max_draft is None:
+            max_draft = _b._longest(cu_draft, stream)
+        adjust = AdjustT(**{n: at[n] for n in ("lengths", "prompt_lengths", *real, "cu_bias", "mask_rows")})
+        if tokens is not None:
+            if tokens.dim() == 2 and tokens.shape[0] != batch:
+                raise ValueError(f"tokens holds {tokens.shape[0]} sequences; {batch} are needed")
+            adjust.token_stride = _matrix(tokens, "tokens", torch.int32, dev)
+            adjust.tokens, adjust.max_tokens = tokens.data_ptr(), tokens.shape[1]
+        if (bias_ids is None) != (bias_values is None):
+            raise ValueError("bias_ids and bias_values go together")
+        if bias_ids is not None:
+            n = bias_ids.numel()
+            adjust.bias_ids = _vector(bias_ids, "bias_ids", n, torch.int32, dev)
+            adjust.bias_values = _vector(bias_values, "bias_values", n, torch.float32, dev)
+            adjust.total_bias = n
+        if masks is not None:
+            adjust.mask_stride = _matrix(masks, "masks", torch.int32, dev)
+            if masks.shape[1] < (vocab + 31) // 32:
+                raise ValueError(f"masks has {masks.shape[1]} words a row; {(vocab + 31) // 32} are needed")
+            if mask_rows is None and masks.shape[0] < rows:
+                raise ValueError(f"masks has {masks.shape[0]} rows; {rows} are needed without mask_rows")
+            adjust.masks, adjust.num_masks = masks.data_ptr(), masks.shape[0]
+        elif mask_rows is not None:
+            raise ValueError("mask_rows needs masks")
+        with _on(dev, stream):
+            if out is None:
+                out = torch.empty((rows, vocab), dtype=logits.dtype, device=dev)
+        if tuple(out.shape) != (rows, vocab):
+            raise ValueError(f"out must be [{rows}, {vocab}], got {tuple(out.shape)}")
+        code = _b._dtype_code(logits)
+        shape = AdjustShapeT(batch, int(max_draft), total, vocab, code, _matrix(logits, "logits", logits.dtype, dev),
+                             _matrix(out, "out", logits.dtype, dev), at["cu_draft"], at["draft_ids"], at["parents"])
+        self.out, self.shape = out, shape
+        self._own(dev, stream, out)
+        self._keep = (logits, tokens, bias_ids, bias_values, masks, *given.values(), adjust)
+        self.args = (C.byref(shape), C.byref(adjust), C.c_void_p(logits.data_ptr()), C.c_void_p(out.data_ptr()))
+        self.fn, self.fn_profiled = lib.spec_adjust_logits, lib.spec_adjust_logits_profiled
+
+
+def adjust_logits(logits: torch.Tensor, tokens: Optional[torch.Tensor] = None, lengths: Optional[torch.Tensor] = None,
+                  prompt_lengths: Optional[torch.Tensor] = None, repetition: Optional[torch.Tensor] = None,
+                  presence: Optional[torch.Tensor] = None, frequency: Optional[torch.Tensor] = None,
+                  bias_ids: Optional[torch.Tensor] = None, bias_values: Optional[torch.Tensor] = None,
+                  cu_bias: Optional[torch.Tensor] = None, masks: Optional[torch.Tensor] = None,
+                  mask_rows: Optional[torch.Tensor] = None, draft_ids: Optional[torch.Tensor] = None,
+                  parents: Optional[torch.Tensor] = None, cu_draft: Optional[torch.Tensor] = None,
+                  max_draft: Optional[int] = None, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Penalties, biases and grammar masks on logits, on the GPU (spec_adjust_logits).
+
+    logits [sum(K_b + 1), V] float32, bfloat16 or float16, rows packed as the
+    target rows of a verify (one row per sequence at a plain step).  tokens int32
+    [batch, max_tokens], each sequence's text so far, lengths int32 [batch] of it
+    in use (None: all), prompt_lengths int32 [batch] of those that count for
+    repetition alone (None: 0); draft_ids int32 [sum(K_b)]: the guesses, which count as written in
+    the rows behind them, along parents (as for verify_tree_greedy; None: chains).
+    repetition, presence, frequency float32 [batch].  bias_ids int32 and bias_values
+    float32 [n], sequence b's at cu_bias[b] .. cu_bias[b + 1] (None: all for every
+    sequence).  masks int32 [num_masks, words], bit v % 32 of word v // 32 set
+    where token v is allowed; mask_rows int32 [rows], each row's mask (-1: none;
+    None: row r goes by mask r).  cu_draft int32 [batch + 1] or None (uniform K);
+    max_draft is read back from the device where it is needed and not given.
+    Returns `out` (may be `logits` itself: in place; None: a new tensor).
+    """
+    return AdjustLogitsPlan(logits, tokens, lengths, prompt_lengths, repetition, presence, frequency, bias_ids,
+                            bias_values, cu_bias, masks, mask_rows, draft_ids, parents, cu_draft, max_draft, out, stream)()
 
 
 class _TreeVerifyPlan(_DevicePlan):

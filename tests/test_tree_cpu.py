@@ -87,3 +87,42 @@ def test_oracle_of_walks():
     assert walk_ref([5, 1, 7, 2], [5, 6, 7], [0, 0, 2], 9) == ([5, 1, -1, -1], 1, [0, 1, -1, -1])
     assert walk_ref([6, 1, 7, 2], [5, 6, 7], [0, 0, 2], 9) == ([6, 7, 2, -1], 2, [0, 2, 3, -1])
     assert walk_ref([6], [], [], 9) == ([6], 0, [0]) and walk_ref([6, 1], [9], [0], 9) is None
+
+
+# ---- spec_adjust_logits
+def _adjust(T, lib, logits=FAKE, out=FAKE, **kw):
+    sh = dict(batch=2, max_draft=4, total_draft=8, vocab=1000, dtype=1, row_stride=1000, out_row_stride=1000)
+    ad = dict(tokens=FAKE, token_stride=50, max_tokens=50, mask_stride=32, num_masks=10)
+    for k, v in kw.items():
+        (sh if k in {n for n, _ in T.AdjustShapeT._fields_} else ad)[k] = v
+    return lib.spec_adjust_logits(C.byref(T.AdjustShapeT(**sh)), C.byref(T.AdjustT(**ad)), logits, out, None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(batch=0), 1), (dict(vocab=0), 1), (dict(max_draft=-1), 1), (dict(total_draft=7), 1), (dict(total_draft=-1), 1),
+    (dict(total_draft=9, cu_draft=FAKE), 1), (dict(dtype=3), 1), (dict(row_stride=999), 1), (dict(out_row_stride=999), 1),
+    (dict(cu_draft=FAKE + 2), 1), (dict(draft_ids=FAKE + 1), 1), (dict(parents=FAKE + 2), 1), (dict(tokens=FAKE + 2), 1),
+    (dict(token_stride=49), 1), (dict(max_tokens=-1), 1), (dict(total_bias=-1), 1), (dict(total_bias=3), 1),
+    (dict(total_bias=3, bias_ids=FAKE), 1), (dict(total_bias=3, bias_ids=FAKE, bias_values=FAKE + 2), 1),
+    (dict(masks=FAKE, mask_stride=31), 1), (dict(masks=FAKE, num_masks=9), 1), (dict(masks=FAKE, num_masks=0, mask_rows=FAKE), 1),
+    (dict(masks=FAKE + 2), 1), (dict(repetition=FAKE + 1), 1), (dict(mask_rows=FAKE + 2), 1), (dict(lengths=FAKE + 3), 1),
+    (dict(logits=None), 1), (dict(out=None), 1), (dict(logits=FAKE + 1), 1), (dict(out=FAKE + 1), 1),
+    (dict(out=FAKE + 2), 1), (dict(out=FAKE + 19998), 1), (dict(out_row_stride=1008), 1), (dict(logits=FAKE + 19998), 1),
+    (dict(vocab=(1 << 20) + 1, row_stride=1 << 21, out_row_stride=1 << 21), 2), (dict(max_draft=129, total_draft=258), 2),
+    (dict(max_tokens=(1 << 30) + 1, token_stride=1 << 31), 2), (dict(row_stride=1 << 62, out_row_stride=1 << 62), 2),
+    (dict(token_stride=1 << 62), 2), (dict(masks=FAKE, mask_stride=1 << 62), 2)])
+def test_adjust_refusals(T, lib, kw, code):
+    assert _adjust(T, lib, **kw) == code
+
+
+def test_adjust_null(T, lib):
+    assert lib.spec_adjust_logits(None, C.byref(T.AdjustT()), FAKE, FAKE, None) == 1
+    assert lib.spec_adjust_logits(C.byref(T.AdjustShapeT()), None, FAKE, FAKE, None) == 1
+
+
+def test_adjust_binding_refusals(T):
+    x, i = torch.zeros(10, 100), torch.zeros(8, dtype=torch.int32)
+    with pytest.raises(ValueError, match="GPU"):
+        T.adjust_logits(x)
+    with pytest.raises(ValueError, match="2-D"):
+        T.adjust_logits(x[0], draft_ids=i)

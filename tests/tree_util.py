@@ -141,3 +141,53 @@ def walk_ref(tokens, ids, parents, vocab):
     n = len(path) - 1
     out = [int(tokens[r]) for r in path] + [-1] * (k - n)
     return out, n, path + [-1] * (k - n)
+
+
+# --------------------------------------------------------------------------
+# edits of logits, in 64 bits
+# --------------------------------------------------------------------------
+def adjust_ref(logits, cu, tokens=None, lengths=None, prompt=None, rep=None, pres=None, freq=None, bias_ids=None,
+               bias_values=None, cu_bias=None, masks=None, mask_rows=None, ids=None, parents=None):
+    """logits float64 [rows, V].  The edited logits, how large the terms of each are together (0: nothing touches it)."""
+    out, size = logits.copy(), np.zeros(logits.shape)
+    V, batch = logits.shape[1], len(cu) - 1
+    for b in range(batch):
+        k = int(cu[b + 1] - cu[b])
+        r_, p_, f_ = (1.0 if x is None and i == 0 else 0.0 if x is None else float(x[b])
+                      for i, x in enumerate((rep, pres, freq)))
+        text = [] if tokens is None else [int(t) for t in tokens[b]]
+        if lengths is not None:
+            text = text[:max(0, int(lengths[b]))]
+        first = 0 if prompt is None else int(prompt[b])
+        bias = {}
+        if bias_ids is not None:
+            lo, hi = (0, len(bias_ids)) if cu_bias is None else (int(cu_bias[b]), int(cu_bias[b + 1]))
+            bias = {int(t): float(v) for t, v in zip(bias_ids[lo:hi], bias_values[lo:hi]) if 0 <= t < V}
+        up = [j if parents is None else int(parents[cu[b] + j]) for j in range(k)]
+        up = [u if 0 <= u <= j else 0 for j, u in enumerate(up)]
+        for r in range(k + 1):
+            row = int(cu[b]) + b + r
+            path = [] if ids is None else [int(ids[cu[b] + x - 1]) for x in way_up(up, r) if x > 0]
+            n = np.zeros(V)
+            seen = np.zeros(V, bool)
+            for i, t in enumerate(text + path):
+                if 0 <= t < V:
+                    seen[t] = True
+                    n[t] += i >= first or i >= len(text)
+            if (r_, p_, f_) != (1.0, 0.0, 0.0):
+                x = out[row]
+                x[seen] = np.where(x[seen] > 0, x[seen] / r_, x[seen] * r_)
+                size[row][seen] += np.abs(x[seen])
+                met = n > 0
+                x[met] -= f_ * n[met]
+                x[met] -= p_
+                size[row][met] += np.abs(f_ * n[met]) + abs(p_)
+            for t, v in bias.items():
+                out[row, t] += v
+                size[row, t] += abs(logits[row, t]) + abs(v)
+            if masks is not None:
+                m = row if mask_rows is None else int(mask_rows[row])
+                if 0 <= m < len(masks):
+                    bits = np.unpackbits(np.ascontiguousarray(masks[m]).view(np.uint8), bitorder="little")[:V]
+                    out[row, bits == 0] = -np.inf
+    return out, size
