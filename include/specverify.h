@@ -630,6 +630,74 @@ SV_API sv_status_t spec_adjust_logits(const sv_adjust_shape_t* shape,
                                hipStream_t stream);
 
 /*
+ * Attention of the newest rows of every sequence over its cache in pages: a plain
+ * decode step (K_b = 0), the scoring rows of a chain of guesses, or a tree of them.
+ *   The rows are those of spec_verify_sample's target: sequence b has K_b + 1, row
+ * cu_draft[b] + b + k. Its cache holds lengths[b] positions, the keys and values
+ * of those rows last: row k's own is position lengths[b] - 1 - K_b + k.  Position p
+ * lies in page page_table[b][p / page_size], at p % page_size.  Row k sees every
+ * position before row 0's, its own, and those of the rows on its way up
+ * (parents as for spec_verify_tree_greedy; a parent out of range counts as 0;
+ * NULL: chains, where row k sees rows 0 .. k):
+ *     a_j = scale * q . k_j,  lse = log sum_j exp(a_j),  out = sum_j exp(a_j - lse) v_j,
+ * where query head h reads key/value head h / (q_heads / kv_heads).  Positions in
+ * a page outside [0, pages) are not seen.  A row that sees nothing gets zeros and
+ * lse = -inf.  Lengths below 0 count as 0, above max_pages * page_size as that;
+ * NULL lengths are that.  Positions behind a length are not seen; where they
+ * share a page with others they may be read.
+ * Arguments
+ *   q and out [total_draft + batch][q_heads][head_dim]; k and v
+ *   data[page][position in page][head][head_dim] (batch_stride: elements between pages), all of
+ *   shape->dtype, strides in elements, the last dimension contiguous.
+ *   page_table int32 [batch][max_pages] with table_stride entries between rows, or NULL:
+ *   sequence b's one page is page b (max_pages = 1, pages >= batch).  page_size is a
+ *   multiple of 16 with a page_table, any number without.
+ *   q and the caches lie on 16-byte places (pointers, and strides of a multiple of 8
+ *   elements), out on 8-byte ones.  out_lse (nullable) float [total_draft +
+ *   batch][q_heads].  scale > 0 and finite.
+ *   dtype SV_DTYPE_BF16 or SV_DTYPE_F16; head_dim 64, 128 or 256.
+ *   Sums, softmax statistics and scores are fp32; the softmax weights are
+ *   rounded to dtype for the product with v.
+ * The workspace depends on the shape's rows, not on the caches' size.  Values that
+ * are not finite and bad cu_draft entries are met as in spec_prefix_attention.
+ * Errors as for spec_verify_sample; SV_ERR_INVALID_ARGUMENT also for q_heads no
+ * multiple of kv_heads and for rows of out that overlap; SV_ERR_UNSUPPORTED also
+ * for fp32, another head_dim, a page_size with a page_table that is no multiple of 16, more than 2^30 positions of a
+ * sequence, positions more than 32 MB apart, batch * kv_heads * positions / 64 of 2^31 or more, or more than 2^32 threads.  out may be q
+ * itself; it may not overlap the inputs otherwise.
+ */
+typedef struct {
+    int32_t batch;             /* B >= 1                                      */
+    int32_t max_draft;         /* K, or the largest K_b when cu_draft != NULL */
+    int32_t total_draft;       /* sum_b K_b                                   */
+    int32_t q_heads;
+    int32_t kv_heads;
+    int32_t head_dim;
+    int32_t pages;             /* pages of k and v                            */
+    int32_t page_size;         /* positions per page                          */
+    int32_t max_pages;         /* entries of a sequence's table               */
+    sv_dtype_t dtype;
+    int64_t table_stride;      /* entries between the tables' rows            */
+    int64_t q_row_stride, q_head_stride;
+    int64_t out_row_stride, out_head_stride;
+    const int32_t* cu_draft;   /* device [B+1], or NULL          */
+    const int32_t* parents;    /* device [total_draft], or NULL  */
+    const int32_t* lengths;    /* device [B], or NULL            */
+    const int32_t* page_table; /* device [B][max_pages], or NULL */
+} sv_tree_shape_t;
+
+SV_API sv_status_t spec_tree_attention(const sv_tree_shape_t* shape,
+                                 const void* q,
+                                 const sv_cache_t* k,
+                                 const sv_cache_t* v,
+                                 float scale,
+                                 void* out,
+                                 float* out_lse,
+                                 void* workspace,
+                                 size_t* workspace_bytes,
+                                 hipStream_t stream);
+
+/*
  * Caches in pages.  A pool holds the states of many sequences in pages of
  * page_size positions,
  *     pool[slab][page][head][position in page][0 .. row_bytes)

@@ -93,6 +93,11 @@ SV_API sv_status_t spec_adjust_logits_profiled(const sv_profile_events_t* events
                                                const sv_adjust_t* adjust, const void* logits, void* out,
                                                hipStream_t stream);
 
+SV_API sv_status_t spec_tree_attention_profiled(const sv_profile_events_t* events, const sv_tree_shape_t* shape,
+                                                const void* q, const sv_cache_t* k, const sv_cache_t* v, float scale,
+                                                void* out, float* out_lse, void* workspace, size_t* workspace_bytes,
+                                                hipStream_t stream);
+
 SV_API sv_status_t spec_cache_compact_profiled(const sv_profile_events_t* events, const sv_compact_shape_t* shape,
                                                void* data, const int32_t* lengths, const int32_t* path,
                                                const int32_t* num_accepted, int32_t* out_lengths, hipStream_t stream);

@@ -38,9 +38,11 @@ from .pages import (  # noqa: F401
 )
 from .tree import (  # noqa: F401
     AdjustLogitsPlan,
+    TreeAttentionPlan,
     TreeGreedyPlan,
     TreeSamplePlan,
     adjust_logits,
+    tree_attention,
     verify_tree_greedy,
     verify_tree_sample,
 )

@@ -102,6 +102,8 @@ def load_library(path: Optional[str] = None):
                                             VP, VP, VP, VP, C.POINTER(C.c_size_t), VP]
     lib.spec_adjust_logits.restype = C.c_int
     lib.spec_adjust_logits.argtypes = [VP, VP, VP, VP, VP]
+    lib.spec_tree_attention.restype = C.c_int
+    lib.spec_tree_attention.argtypes = [VP, VP, VP, VP, C.c_float, VP, VP, VP, C.POINTER(C.c_size_t), VP]
     lib.spec_cache_compact.restype = C.c_int
     lib.spec_cache_compact.argtypes = [VP, VP, VP, VP, VP, VP, VP]
     lib.spec_page_fork.restype = C.c_int
@@ -114,7 +116,7 @@ def load_library(path: Optional[str] = None):
     for name in ("spec_verify_sample", "spec_verify_argmax", "spec_verify_greedy", "spec_draft_sample",
                  "spec_token_likelihood", "spec_beam_select", "spec_state_reorder", "spec_prefix_attention",
                  "spec_cache_compact", "spec_page_fork", "spec_verify_tree_greedy", "spec_verify_tree_sample",
-                 "spec_adjust_logits"):
+                 "spec_adjust_logits", "spec_tree_attention"):
         f = getattr(lib, name + "_profiled")
         f.restype = C.c_int
         f.argtypes = [C.POINTER(ProfileEventsT)] + list(getattr(lib, name).argtypes)

@@ -199,8 +199,6 @@ sv_status_t state_reorder_common(const sv_state_shape_t* sh, void* states, const
 
 // ---- shared-prefix attention
 
-constexpr int32_t kMaxPosStride = 1 << 25;  // bytes: 64 positions stay within a 31-bit offset
-constexpr int32_t kMaxPositions = 1 << 30;
 constexpr int64_t kMaxRows = INT32_MAX / 2;  // query rows of one key/value head in one group
 
 // Workgroups that the splits of the keys aim at.  Work whose rows fit one workgroup is bound by reading the caches, and
@@ -302,25 +300,6 @@ sv_status_t check_attention(const sv_attention_shape_t* sh, float scale)
     const double join = ((double)p.rows * sh->q_heads + sv::kWaves - 1) / sv::kWaves;
     if (!launchable((double)p.grid, sv::kAttnThreads) || !launchable(join, sv::kThreads)) return SV_ERR_UNSUPPORTED;
     return SV_OK;
-}
-
-// A cache's pointer and strides (elements of 2 bytes): 16-byte places.
-bool cache_ok(const sv_cache_t* c)
-{
-    if (c == nullptr || c->data == nullptr || !aligned(c->data, 16)) return false;
-    return c->batch_stride >= 0 && c->head_stride >= 0 && c->position_stride >= 0 && c->batch_stride % 8 == 0 &&
-           c->head_stride % 8 == 0 && c->position_stride % 8 == 0;
-}
-
-// Whether rows of `width` elements at two strides lie apart.
-bool distinct_rows(int64_t s0, int64_t n0, int64_t s1, int64_t n1, int64_t width)
-{
-    if (n0 < 2) s0 = 0;
-    if (n1 < 2) s1 = 0;
-    const bool first = n1 < 2 || (n0 > 1 && s0 < s1);  // the inner of the two
-    const int64_t si = first ? s0 : s1, ni = first ? n0 : n1, so = first ? s1 : s0, no = first ? n1 : n0;
-    if (ni > 1 && si < width) return false;
-    return no < 2 || (ni < 2 ? so >= width : so >= width && (so - width) / si >= ni - 1);
 }
 
 template <int DT, int D>

@@ -15,8 +15,6 @@ static_assert(SV_MAX_DRAFT == sv::kCompactMost, "draft limit mismatch");
 
 namespace {
 
-constexpr int64_t kMaxPositions = 1 << 30;
-
 // The pool's checks, its extent in bytes, and the widest piece that every row divides into (16-byte pieces need rows
 // on 4-byte places only).
 sv_status_t check_pool(const sv_pool_t& p, const void* data, int64_t* extent, int* vecb)

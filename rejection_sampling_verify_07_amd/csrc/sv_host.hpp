@@ -114,6 +114,29 @@ inline sv_status_t launch_status()
     return e == hipSuccess ? SV_OK : SV_ERR_HIP;
 }
 
+// Limits of the attention calls.
+constexpr int32_t kMaxPosStride = 1 << 25;  // bytes: 64 positions stay within a 31-bit offset
+constexpr int32_t kMaxPositions = 1 << 30;
+
+// A cache's pointer and strides (elements of 2 bytes): 16-byte places.
+inline bool cache_ok(const sv_cache_t* c)
+{
+    if (c == nullptr || c->data == nullptr || !aligned(c->data, 16)) return false;
+    return c->batch_stride >= 0 && c->head_stride >= 0 && c->position_stride >= 0 && c->batch_stride % 8 == 0 &&
+           c->head_stride % 8 == 0 && c->position_stride % 8 == 0;
+}
+
+// Whether rows of `width` elements at two strides lie apart.
+inline bool distinct_rows(int64_t s0, int64_t n0, int64_t s1, int64_t n1, int64_t width)
+{
+    if (n0 < 2) s0 = 0;
+    if (n1 < 2) s1 = 0;
+    const bool first = n1 < 2 || (n0 > 1 && s0 < s1);  // the inner of the two
+    const int64_t si = first ? s0 : s1, ni = first ? n0 : n1, so = first ? s1 : s0, no = first ? n1 : n0;
+    if (ni > 1 && si < width) return false;
+    return no < 2 || (ni < 2 ? so >= width : so >= width && (so - width) / si >= ni - 1);
+}
+
 // c = fl32(log2(e) / T): the softmax's exp(l / T) is computed as exp2(l * c).
 inline float scale_of(float temperature) { return (float)(1.4426950408889634 / (double)temperature); }
 

@@ -1,0 +1,953 @@
+// Attention of every sequence's newest rows, a tree of guesses, over the
+// sequence's cache in pages.
+//
+// Row k of sequence b (head h, key/value head h / rep) sees the positions before
+// the newest rows and, of those rows, the ones on its way up to row 0:
+//     a_j = scale * q . k_j,   out = sum_j exp(a_j - z) v_j,   z = log sum_j exp(a_j).
+// Sums over parts of the keys join as in sv_attention.hpp, whose products,
+// references and fragment orders are used here.
+//
+// Work is dealt by what the lengths say on the device, not by what the tables could
+// hold: the rounds (KB keys) of all (sequence, key head) pairs form one line, and
+// each of a fixed number of workgroups takes an equal stretch of it.  A pair that lies within
+// one stretch is finished there; one that crosses borders leaves parts, at most
+// two per workgroup, which the join adds up.  The workspace therefore does not
+// grow with the caches, and sequences of any mix of lengths keep all CUs busy.
+//
+// Positions come in grains of 16, which never cross a page: a wave finds a
+// grain's page with scalar loads, one step before the keys' own loads.
+//   Few rows per key head (up to 16 or 32): each wave walks its own 32 keys of a
+// round with all rows, K and V straight from memory to registers (attend_rows).
+//   More: the four waves share the rows and take tiles of 64 keys through LDS
+// (attend_tree_tiles).
+#pragma once
+
+#include "sv_attention.hpp"
+
+namespace sv {
+
+constexpr int kTreeMostGuesses = 128;
+constexpr int kTreeWords = 8;  // a row's view of the newest rows: one word of ones before them, 129 bits, zeros
+
+struct TreeArgs {
+    const char *q, *k, *v;
+    char* out;
+    float* lse;
+    int64_t q_row, q_head, out_row, out_head;        // bytes
+    int64_t k_page, k_head, v_page, v_head;          // bytes
+    int32_t k_pos, v_pos;                            // bytes
+    const int32_t *cu, *parents, *lengths, *table;
+    int64_t table_stride;
+    int32_t batch, rows, kmax, pages, capacity;      // capacity: positions a sequence's pages hold
+    int32_t grains_shift;                            // grains per page as a multiplication: (g * mul) >> shift
+    uint32_t grains_mul, grains;
+    int32_t q_heads, kv_heads, rep;
+    float c;                                         // scale * log2(e)
+    int32_t groups, tiles;                           // stretches of the line; row tiles
+    int32_t* plan;                                   // [batch + 1] rounds before each sequence, then the stretch
+    float* acc;                                      // [2 * groups][tile][row][D]
+    float2* ml;                                      // [2 * groups][tile][row]
+};
+
+// First packed row of sequence b; entries of cu outside the batch are clamped.
+__device__ __forceinline__ int32_t tree_row(const TreeArgs& a, int32_t b)
+{
+    if (b >= a.batch) return a.rows;
+    if (a.cu == nullptr) return b * (a.kmax + 1);
+    return min(max(a.cu[b], 0), a.rows - a.batch) + b;
+}
+
+__device__ __forceinline__ int32_t tree_length(const TreeArgs& a, int32_t b)
+{
+    return a.lengths != nullptr ? min(max(a.lengths[b], 0), a.capacity) : a.capacity;
+}
+
+// A scalar load: the tables are not written while a kernel reads them.
+__device__ __forceinline__ int32_t scalar_load(const int32_t* p)
+{
+    return *(const __attribute__((address_space(4))) int32_t*)p;
+}
+
+// What one workgroup works on: a stretch of one (sequence, key head) pair.
+struct Stretch {
+    const char *k, *v;       // the key head's first page
+    const int32_t* table;    // the sequence's row, or nullptr: its one page is `b`
+    const int32_t* parents;  // its guesses' parents, or nullptr
+    int32_t b, hk, row0, nrows;
+    int32_t begin, end;      // keys
+    int32_t total;           // positions of the sequence
+    int32_t context;         // those before the newest rows (below 0 if the newest rows are not all there)
+    bool past;               // read past the caches
+};
+
+// The page of grain g (-1: none; keys at or past `total` have none).
+__device__ __forceinline__ int32_t grain_page(const TreeArgs& a, const Stretch& s, int32_t g)
+{
+    if (g * 16 >= s.total) return -1;
+    if (s.table == nullptr) return s.b;
+    const uint32_t at = (uint32_t)(((uint64_t)(uint32_t)g * a.grains_mul) >> a.grains_shift);
+    const int32_t page = scalar_load(s.table + at);
+    return (uint32_t)page < (uint32_t)a.pages ? page : -1;
+}
+__device__ __forceinline__ int32_t grain_in_page(const TreeArgs& a, const Stretch& s, int32_t g)
+{
+    if (s.table == nullptr) return g;
+    const uint32_t at = (uint32_t)(((uint64_t)(uint32_t)g * a.grains_mul) >> a.grains_shift);
+    return g - (int32_t)(at * a.grains);
+}
+
+// The rows that rows t0 .. t0 + n - 1 of the sequence see among the newest ones, as
+// bits from the sequence's row 0 on.  All threads of the workgroup call it.
+__device__ __forceinline__ void tree_views(const Stretch& s, int32_t t0, int32_t n, int32_t* s_up, uint32_t* s_view)
+{
+    const int tid = (int)threadIdx.x;
+    if (s.parents != nullptr) {
+        for (int32_t j = tid; j < s.nrows - 1; j += kAttnThreads) s_up[j] = s.parents[j];
+        __syncthreads();
+    }
+    for (int32_t i = tid; i < n; i += kAttnThreads) {
+        uint32_t w[kTreeWords] = {~0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+        int32_t r = t0 + i;
+        while (true) {
+#pragma unroll
+            for (int x = 0; x < 5; ++x) w[x + 1] |= r / 32 == x ? 1u << (r % 32) : 0u;
+            if (r == 0) break;
+            const int32_t up = s.parents != nullptr ? s_up[r - 1] : r - 1;
+            r = up >= 0 && up < r ? up : 0;
+        }
+#pragma unroll
+        for (int x = 0; x < kTreeWords; ++x) s_view[i * kTreeWords + x] = w[x];
+    }
+    __syncthreads();
+}
+
+// Four bits: whether a row with view `w` sees keys e .. e + 3, counted from the newest rows' first.
+__device__ __forceinline__ uint32_t sees4(const uint32_t* w, int32_t e)
+{
+    if (e < -3) return 15u;  // before the newest rows: every row sees them
+    const int32_t at = min((e >> 5) + 1, kTreeWords - 2);
+    return (uint32_t)((((uint64_t)w[at + 1] << 32) | w[at]) >> (e & 31)) & 15u;
+}
+__device__ __forceinline__ bool sees(const uint32_t* w, int32_t e) { return e < 0 || (sees4(w, e) & 1u) != 0; }
+
+template <int D, int MT>
+constexpr size_t tree_rows_lds()
+{
+    return attn_lds_floats(D, MT) * 4;
+}
+
+// Where a finished or partial result of a workgroup goes.
+struct TreeOut {
+    bool whole;     // no other workgroup has keys of the pair
+    int64_t slot;   // (part * tiles + tile) otherwise
+};
+
+// Columns n .. n + 3 of a row, normalised and rounded.
+template <int DT>
+__device__ __forceinline__ void store4(char* p, float x0, float x1, float x2, float x3)
+{
+    u32x2 w;
+    w.x = pack2<DT>(x0, x1);
+    w.y = pack2<DT>(x2, x3);
+    *(SV_GLOBAL u32x2*)p = w;
+}
+
+// MT tiles of 16 query rows in every wave, 32 keys of each round per wave.
+template <int DT, int D, int MT>
+__device__ __forceinline__ void attend_rows(const TreeArgs& a, const Stretch& st, int32_t tile, const TreeOut& to,
+                                            const uint32_t* s_view, float* s_mem)
+{
+    constexpr int DC = D / 32;   // 32-wide chunks of the score product
+    constexpr int DPL = D / 16;  // columns of V per lane
+    constexpr int VW = DPL / 2;  // 32-bit words of a lane's V row
+    const int lane = lane_id(), l16 = lane & 15, lg = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(wave_id());
+    const int32_t m_total = st.nrows * a.rep;
+    const int32_t r0 = tile * (MT * 16), t0 = r0 / a.rep;
+
+    u32x4 qf[MT][DC];  // query rows: column l16 of each tile; rows past the matrix are zero
+    const uint32_t* view[MT];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+        const int32_t r = r0 + mt * 16 + l16;
+        const int32_t t = r / a.rep, h = st.hk * a.rep + (r - t * a.rep);
+        const char* qp = a.q + (int64_t)(st.row0 + t) * a.q_row + (int64_t)h * a.q_head + lg * 16;
+#pragma unroll
+        for (int c = 0; c < DC; ++c)
+            qf[mt][c] = r < m_total ? *(const SV_GLOBAL u32x4*)(qp + c * 64) : u32x4{0u, 0u, 0u, 0u};
+        view[mt] = s_view + (r < m_total ? t - t0 : 0) * kTreeWords;
+    }
+    f32x4 o[MT][DPL];
+    float m[MT], l[MT];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+        m[mt] = kNoReference;
+        l[mt] = 0.0f;
+#pragma unroll
+        for (int d = 0; d < DPL; ++d) o[mt][d] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+
+    // a lane's keys inside a grain: K row l16; V rows 4 lg + j
+    const uint32_t koff = (uint32_t)(l16 * a.k_pos + lg * 16);
+    uint32_t voff[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) voff[j] = (uint32_t)((lg * 4 + j) * a.v_pos + l16 * (DPL * 2));
+    struct Pages {
+        int32_t p[2];
+    };
+    auto look = [&](int32_t kb) {
+        return Pages{{kb < st.end ? grain_page(a, st, kb / 16) : -1, kb < st.end ? grain_page(a, st, kb / 16 + 1) : -1}};
+    };
+    auto sound = [](const Pages& p) { return (p.p[0] | p.p[1]) >= 0; };
+    auto base_of = [&](const char* data, int64_t page_stride, int32_t pos_stride, const Pages& p, int32_t kb, int t) {
+        return data + max(p.p[t], 0) * page_stride +
+               (int64_t)(p.p[t] < 0 ? 0 : grain_in_page(a, st, kb / 16 + t) * 16) * pos_stride;
+    };
+    // Rows of a grain that hold keys: the last one stands in for those behind it (masked below), row 0 of the pool for
+    // all of a grain without a page.
+    auto last_of = [&](const Pages& p, int32_t kb, int t) {
+        return p.p[t] < 0 ? 0 : min(15, st.total - 1 - (kb + t * 16));
+    };
+    auto load_k = [&](int32_t kb, const Pages& p, u32x4 (&kf)[2][DC], auto past) {
+        const bool edge = kb + kKeyBlock > st.total || !sound(p);
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            const char* base = base_of(st.k, a.k_page, a.k_pos, p, kb, t);
+            uint32_t off = koff;
+            if (edge) off = (uint32_t)(min(l16, last_of(p, kb, t)) * a.k_pos + lg * 16);
+#pragma unroll
+            for (int c = 0; c < DC; ++c) kf[t][c] = load16<decltype(past)::value>((const u32x4*)(base + off + c * 64));
+        }
+    };
+    auto load_v = [&](int32_t kb, const Pages& p, uint32_t (&vr)[8][VW], auto masked, auto past) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            const char* base = base_of(st.v, a.v_page, a.v_pos, p, kb, t);
+            const int32_t last = last_of(p, kb, t);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                uint32_t off = voff[j];
+                if constexpr (decltype(masked)::value)
+                    off = (uint32_t)(min(lg * 4 + j, last) * a.v_pos + l16 * (DPL * 2));
+                const char* x = base + off;
+                if constexpr (VW == 2) {
+                    const u32x2 w = *(const SV_GLOBAL u32x2*)x;
+                    vr[t * 4 + j][0] = w.x;
+                    vr[t * 4 + j][1] = w.y;
+                } else {
+#pragma unroll
+                    for (int y = 0; y < VW / 4; ++y) {
+                        const u32x4 w = load16<decltype(past)::value>((const u32x4*)(x + y * 16));
+#pragma unroll
+                        for (int z = 0; z < 4; ++z) vr[t * 4 + j][y * 4 + z] = w[z];
+                    }
+                }
+            }
+        }
+    };
+
+    bool wild = false;  // (uniform) a masked block held a value that is not finite
+    bool far = false;   // (uniform) a reference lies beyond kFarReference
+    int32_t kb = st.begin + wave * kKeyBlock, wild_from = st.end;
+    Pages now = look(kb), next = look(kb + kKeyRound);
+    u32x4 kf[2][DC];  // the block at hand; the next one's is loaded once the scores have taken it
+    auto next_k = [&](int32_t x, const Pages& p) {
+        if (x >= st.end) return;
+        with_policy(st.past, [&](auto past) { load_k(x, p, kf, past); });
+    };
+    auto step = [&](auto masked) {
+        constexpr bool MASKED = decltype(masked)::value;
+        uint32_t vr[8][VW];
+        with_policy(st.past, [&](auto past) { load_v(kb, now, vr, masked, past); });
+        const Pages after = look(kb + 2 * kKeyRound);
+        f32x4 s[2][MT];
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+                s[t][mt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int c = 0; c < DC; ++c) s[t][mt] = mfma_16x16x32<DT>(kf[t][c], qf[mt][c], s[t][mt]);
+            }
+        next_k(kb + kKeyRound, next);
+        if constexpr (MASKED) {
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) {
+                    const uint32_t seen =
+                        now.p[t] < 0 ? 0u : sees4(view[mt], kb + t * 16 + lg * 4 - st.context);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if ((seen >> i & 1u) == 0) s[t][mt][i] = neg_inf();
+                }
+        }
+        // move a reference that a score exceeds by the slack (the first one always does)
+        float top[MT];
+        bool over = false;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+            float x = fmaxf(s[0][mt][0], s[0][mt][1]);
+#pragma unroll
+            for (int i = 2; i < 8; ++i) x = fmaxf(x, s[i / 4][mt][i & 3]);
+            top[mt] = x * a.c;
+            over |= top[mt] > m[mt] + (Reference<DT>::kBelow + Reference<DT>::kSlack);
+        }
+        if (__any(over)) {
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+                float x = top[mt];
+                x = fmaxf(x, __shfl_xor(x, 16, kWave));
+                x = fmaxf(x, __shfl_xor(x, 32, kWave));
+                x = fmaxf(x - Reference<DT>::kBelow, m[mt]);
+                const float f = __builtin_amdgcn_exp2f(m[mt] - x);
+                m[mt] = x;
+                l[mt] *= f;
+#pragma unroll
+                for (int d = 0; d < DPL; ++d) o[mt][d] *= f;
+            }
+            far = far_references<MT>(m);
+        }
+        if (__builtin_expect(far, 0)) {
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) s[i / 4][mt][i & 3] = far_distance(s[i / 4][mt][i & 3], a.c, m[mt]);
+        }
+        const float c = far ? 1.0f : a.c;
+        u32x4 pf[MT];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+            const float ref = far ? 0.0f : m[mt];
+            float p[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i / 4][mt][i & 3], c, -ref));
+                l[mt] += p[i];
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) pf[mt][i] = pack2<DT>(p[2 * i], p[2 * i + 1]);
+        }
+        if constexpr (MASKED) {
+            // none for keys past the last one, or without a page
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const bool there = now.p[j / 4] >= 0 && kb + (j < 4 ? 0 : 12) + lg * 4 + j < st.total;
+#pragma unroll
+                for (int x = 0; x < VW; ++x) vr[j][x] = there ? vr[j][x] : 0u;
+            }
+            // A value that is not finite times the weight 0 of a row that does not see it would be NaN: such values
+            // count as 0 here, and reach the rows that see them after the last block.
+            bool any = false;
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+#pragma unroll
+                for (int x = 0; x < VW; ++x) any |= finite_halves<DT>(vr[j][x]) != vr[j][x];
+            if (__any(any)) {
+                wild = true;
+                wild_from = min(wild_from, kb);
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+#pragma unroll
+                    for (int x = 0; x < VW; ++x) vr[j][x] = finite_halves<DT>(vr[j][x]);
+            }
+        }
+#pragma unroll
+        for (int d = 0; d < DPL; ++d) {
+            u32x4 vf;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                vf[i] = __builtin_amdgcn_perm(vr[2 * i + 1][d / 2], vr[2 * i][d / 2], d & 1 ? 0x07060302u : 0x05040100u);
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) o[mt][d] = mfma_16x16x32<DT>(vf, pf[mt], o[mt][d]);
+        }
+        now = next;
+        next = after;
+        kb += kKeyRound;
+    };
+    next_k(kb, now);
+    while (kb < st.end) {
+        while (kb + kKeyBlock <= st.context && kb < st.end && sound(now)) step(std::false_type{});
+        if (kb < st.end) step(std::true_type{});
+    }
+    if (wild) {
+#pragma unroll 1
+        for (kb = wild_from; kb < st.end; kb += kKeyRound) {
+            const Pages p = look(kb);
+            if (kb + kKeyBlock <= st.context && sound(p)) continue;  // (its values went into the products as they are)
+#pragma unroll 1
+            for (int t = 0; t < 2; ++t) {
+                if (p.p[t] < 0) continue;
+                const char* base = base_of(st.v, a.v_page, a.v_pos, p, kb, t);
+#pragma unroll 1
+                for (int32_t x = 0; x <= last_of(p, kb, t); ++x) {
+                    // accumulator i of tile d holds column (4 lg + i) * DPL + d
+                    const SV_GLOBAL uint32_t* row =
+                        (const SV_GLOBAL uint32_t*)(base + (int64_t)x * a.v_pos + lg * (4 * DPL * 2));
+                    bool see[MT];
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt) see[mt] = sees(view[mt], kb + t * 16 + x - st.context);
+#pragma unroll
+                    for (int e = 0; e < 4 * DPL; e += 2) {
+                        const uint32_t w = row[e / 2], bad = w ^ finite_halves<DT>(w);
+#pragma unroll
+                        for (int y = 0; y < 2; ++y) {
+                            const float v = y ? hi16<DT>(bad) : lo16<DT>(bad);  // 0 where the value was finite
+#pragma unroll
+                            for (int mt = 0; mt < MT; ++mt)
+                                if (see[mt]) o[mt][(e + y) % DPL][(e + y) / DPL] += v;
+                        }
+                    }
+                }
+            }
+        }
+    }
+
+    // ---- join the four waves: a common reference, then o summed in a fixed order
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+        l[mt] += __shfl_xor(l[mt], 16, kWave);
+        l[mt] += __shfl_xor(l[mt], 32, kWave);
+    }
+    float* s_m = s_mem;                                 // [wave][MT * 16]
+    float* s_l = s_m + kAttnWaves * MT * 16;            // [wave][MT * 16]
+    f32x4* s_o = (f32x4*)(s_l + kAttnWaves * MT * 16);  // [2][MT * DPL][64]
+    if (lg == 0) {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+            s_m[(wave * MT + mt) * 16 + l16] = m[mt];
+            s_l[(wave * MT + mt) * 16 + l16] = l[mt];
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+        float x = s_m[mt * 16 + l16];
+#pragma unroll
+        for (int w = 1; w < kAttnWaves; ++w) x = fmaxf(x, s_m[(w * MT + mt) * 16 + l16]);
+        const float f = __builtin_amdgcn_exp2f(m[mt] - x);
+        float sum = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kAttnWaves; ++w)
+            sum += s_l[(w * MT + mt) * 16 + l16] * __builtin_amdgcn_exp2f(s_m[(w * MT + mt) * 16 + l16] - x);
+        m[mt] = x;
+        l[mt] = sum;
+#pragma unroll
+        for (int d = 0; d < DPL; ++d) o[mt][d] *= f;
+    }
+#pragma unroll
+    for (int half = 2; half >= 1; half >>= 1) {
+        if (wave >= half && wave < 2 * half) {
+#pragma unroll
+            for (int i = 0; i < MT * DPL; ++i) s_o[((wave - half) * MT * DPL + i) * kWave + lane] = o[i / DPL][i % DPL];
+        }
+        __syncthreads();
+        if (wave < half) {
+#pragma unroll
+            for (int i = 0; i < MT * DPL; ++i) o[i / DPL][i % DPL] += s_o[(wave * MT * DPL + i) * kWave + lane];
+        }
+        __syncthreads();
+    }
+    if (wave != 0) return;
+    // accumulator i of tile d holds column (4 lg + i) * DPL + d
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+        const int32_t r = r0 + mt * 16 + l16;
+        if (r >= m_total) continue;
+        const int32_t t = r / a.rep, h = st.hk * a.rep + (r - t * a.rep);
+        if (to.whole) {
+            const float inv = l[mt] != 0.0f ? 1.0f / l[mt] : 0.0f;
+            char* dst = a.out + (int64_t)(st.row0 + t) * a.out_row + (int64_t)h * a.out_head + lg * (4 * DPL * 2);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int d = 0; d < DPL; d += 4)
+                    store4<DT>(dst + (i * DPL + d) * 2, o[mt][d][i] * inv, o[mt][d + 1][i] * inv, o[mt][d + 2][i] * inv,
+                               o[mt][d + 3][i] * inv);
+            if (a.lse != nullptr && lg == 0)
+                a.lse[(int64_t)(st.row0 + t) * a.q_heads + h] =
+                    l[mt] != 0.0f ? (m[mt] + __builtin_amdgcn_logf(l[mt])) * 0.69314718055994531f : neg_inf();
+        } else {
+            const int64_t at = to.slot * (MT * 16) + mt * 16 + l16;
+            if (lg == 0) a.ml[at] = float2{m[mt], l[mt]};
+            SV_GLOBAL f32x4* dst = (SV_GLOBAL f32x4*)(a.acc + at * D + lg * 4 * DPL);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int d = 0; d < DPL; d += 4)
+                    dst[(i * DPL + d) / 4] = f32x4{o[mt][d][i], o[mt][d + 1][i], o[mt][d + 2][i], o[mt][d + 3][i]};
+        }
+    }
+}
+
+// ---- many rows per key head: four waves of MT * 16 rows share tiles of 64 keys through LDS, laid out and read as in
+// TileAttention.
+template <int DT, int D, int MT>
+__device__ __forceinline__ void attend_tree_tiles(const TreeArgs& a, const Stretch& st, int32_t tile, const TreeOut& to,
+                                                  const uint32_t* s_view, int32_t* s_wild, char* s_kv)
+{
+    typedef TileAttention<DT, D, MT> TA;
+    constexpr int DC = TA::DC, DT16 = TA::DT16, KT = TA::KT, SUBS = KT / kKeyBlock, GR = KT / 16;
+    static_assert(kWave % TA::CH == 0 || TA::CH % kWave == 0, "a wave's load stays within a grain");
+    const int lane = lane_id(), l16 = lane & 15, lg = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(wave_id());
+    const int32_t m_total = st.nrows * a.rep;
+    const int32_t r0 = tile * TA::ROWS + wave * (MT * 16), t0 = tile * TA::ROWS / a.rep;
+    const bool idle = r0 >= m_total;  // no rows: the wave only moves tiles
+
+    u32x4 qf[MT][DC];
+    const uint32_t* view[MT];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+        const int32_t r = r0 + mt * 16 + l16;
+        const int32_t t = r / a.rep, h = st.hk * a.rep + (r - t * a.rep);
+        const char* qp = a.q + (int64_t)(st.row0 + t) * a.q_row + (int64_t)h * a.q_head + lg * 16;
+#pragma unroll
+        for (int c = 0; c < DC; ++c)
+            qf[mt][c] = r < m_total ? *(const SV_GLOBAL u32x4*)(qp + c * 64) : u32x4{0u, 0u, 0u, 0u};
+        view[mt] = s_view + (r < m_total ? t - t0 : 0) * kTreeWords;
+    }
+    f32x4 o[MT][DT16];
+    float m[MT], l[MT];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+        m[mt] = kNoReference;
+        l[mt] = 0.0f;
+#pragma unroll
+        for (int d = 0; d < DT16; ++d) o[mt][d] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+
+    struct Pages {
+        int32_t p[GR];
+    };
+    auto look = [&](int32_t kb) {
+        Pages p;
+#pragma unroll
+        for (int g = 0; g < GR; ++g) p.p[g] = kb < st.end ? grain_page(a, st, kb / 16 + g) : -1;
+        return p;
+    };
+    auto sound = [](const Pages& p) {
+        int32_t x = 0;
+#pragma unroll
+        for (int g = 0; g < GR; ++g) x |= p.p[g];
+        return x >= 0;
+    };
+    // this thread's chunks of a tile: i-th load, row (i * 256 + thread) / CH; a wave's rows lie in one grain
+    u32x4 kreg[TA::LOADS], vreg[TA::LOADS];
+    auto row_of = [&](int i) { return (i * kAttnThreads + (int32_t)threadIdx.x) / TA::CH; };
+    const uint32_t ch = (uint32_t)threadIdx.x % TA::CH;
+    auto fetch = [&](int32_t kb, const Pages& p) {
+        const bool edge = kb + KT > st.total || !sound(p);
+#pragma unroll
+        for (int i = 0; i < TA::LOADS; ++i) {
+            // (uniform over the wave)
+            const int g = (i * kAttnThreads + wave * kWave) / TA::CH / 16;
+            int32_t page = p.p[0];
+#pragma unroll
+            for (int x = 1; x < GR; ++x) page = g == x ? p.p[x] : page;
+            const int64_t at = page < 0 ? 0 : grain_in_page(a, st, kb / 16 + g) * 16;
+            int32_t row = row_of(i) - g * 16;
+            if (edge) row = min(row, page < 0 ? 0 : min(15, st.total - 1 - (kb + g * 16)));
+            const char* kp = st.k + max(page, 0) * a.k_page + at * a.k_pos;
+            const char* vp = st.v + max(page, 0) * a.v_page + at * a.v_pos;
+            kreg[i] = *(const SV_GLOBAL u32x4*)(kp + (uint32_t)(row * a.k_pos + (int32_t)ch * 16));
+            vreg[i] = *(const SV_GLOBAL u32x4*)(vp + (uint32_t)(row * a.v_pos + (int32_t)ch * 16));
+        }
+    };
+    auto plain = [&](int32_t kb, const Pages& p) { return kb + KT <= st.context && sound(p); };
+    auto keep = [&](int buf, int32_t kb, const Pages& p) {
+        char* dst = s_kv + buf * (2 * TA::TILE);
+        if (!plain(kb, p)) {
+            // No value for keys past the last one or without a page; one that is not finite counts as 0 here (times the
+            // weight 0 of a row that does not see it, it would be NaN) and reaches the rows that see it at the end.
+            bool any = false;
+#pragma unroll
+            for (int i = 0; i < TA::LOADS; ++i) {
+                const int g = (i * kAttnThreads + wave * kWave) / TA::CH / 16;
+                int32_t page = p.p[0];
+#pragma unroll
+                for (int x = 1; x < GR; ++x) page = g == x ? p.p[x] : page;
+                const bool there = page >= 0 && kb + row_of(i) < st.total;
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    const uint32_t w = there ? vreg[i][x] : 0u;
+                    vreg[i][x] = finite_halves<DT>(w);
+                    any |= vreg[i][x] != w;
+                }
+            }
+            if (__any(any) && lane == 0) atomicMin(s_wild, kb);
+        }
+#pragma unroll
+        for (int i = 0; i < TA::LOADS; ++i) {
+            const int32_t row = row_of(i);
+            const int32_t at = row * TA::ROW + (((int32_t)ch ^ (row & TA::MASK)) * 16);
+            *(u32x4*)(dst + at) = kreg[i];
+            *(u32x4*)(dst + TA::TILE + at) = vreg[i];
+        }
+    };
+
+    int32_t kb = st.begin;
+    Pages now = look(kb), next = look(kb + KT);
+    if (threadIdx.x == 0) *s_wild = INT32_MAX;
+    fetch(kb, now);
+    __syncthreads();
+    keep(0, kb, now);
+    __syncthreads();
+    int buf = 0;
+    bool far = false;  // (uniform over the wave) a reference lies beyond kFarReference
+    auto use = [&](auto masked) {
+        constexpr bool MASKED = decltype(masked)::value;
+        const char* s_k = s_kv + buf * (2 * TA::TILE);
+        const char* s_v = s_k + TA::TILE;
+        // The fragments that a group of products needs are read while the group before it runs (the barriers keep the
+        // scheduler from moving a read down to its use, which exposed the LDS latency once per product).
+        auto k_rows = [&](int i, u32x4 (&kf)[DC]) {  // 16 keys
+            const int32_t row = i * 16 + l16;
+#pragma unroll
+            for (int c = 0; c < DC; ++c)
+                kf[c] = *(const u32x4*)(s_k + row * TA::ROW + (((c * 4 + lg) ^ (l16 & TA::MASK)) * 16));
+        };
+        auto v_columns = [&](int u, u32x4 (&vf)[DT16]) {  // 32 keys: four (lg * 4 + l16 / 4) and 8 bytes of columns per
+                                                          // lane before the exchange
+            const int32_t vrow = u * kKeyBlock + lg * 4 + (l16 >> 2);
+#pragma unroll
+            for (int d = 0; d < DT16; ++d) {
+                const int32_t at =
+                    vrow * TA::ROW + (((d * 2 + ((l16 & 3) >> 1)) ^ (vrow & TA::MASK)) * 16) + (l16 & 1) * 8;
+                const u32x2 v0 = lds_read_transposed(s_v + at), v1 = lds_read_transposed(s_v + at + 16 * TA::ROW);
+                vf[d] = u32x4{v0.x, v0.y, v1.x, v1.y};
+            }
+        };
+        f32x4 s[SUBS][2][MT];
+        u32x4 kf[2][DC], vf[DT16];
+        k_rows(0, kf[0]);
+#pragma unroll
+        for (int i = 0; i < 2 * SUBS; ++i) {
+            const int u = i / 2, t = i & 1;
+            if (i + 1 < 2 * SUBS) k_rows(i + 1, kf[(i + 1) & 1]);
+            else v_columns(0, vf);
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) s[u][t][mt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int c = 0; c < DC; ++c)
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) s[u][t][mt] = mfma_16x16x32<DT>(kf[i & 1][c], qf[mt][c], s[u][t][mt]);
+            if constexpr (MASKED) {
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) {
+                    const uint32_t seen = now.p[i] < 0 ? 0u : sees4(view[mt], kb + i * 16 + lg * 4 - st.context);
+#pragma unroll
+                    for (int x = 0; x < 4; ++x)
+                        if ((seen >> x & 1u) == 0) s[u][t][mt][x] = neg_inf();
+                }
+            }
+        }
+        float top[MT];
+        bool over = false;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+            float x = s[0][0][mt][0];
+#pragma unroll
+            for (int i = 1; i < 8 * SUBS; ++i) x = fmaxf(x, s[i / 8][(i / 4) & 1][mt][i & 3]);
+            top[mt] = x * a.c;
+            over |= top[mt] > m[mt] + (Reference<DT>::kBelow + Reference<DT>::kSlack);
+        }
+        if (__any(over)) {
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+                float x = top[mt];
+                x = fmaxf(x, __shfl_xor(x, 16, kWave));
+                x = fmaxf(x, __shfl_xor(x, 32, kWave));
+                x = fmaxf(x - Reference<DT>::kBelow, m[mt]);
+                const float f = __builtin_amdgcn_exp2f(m[mt] - x);
+                m[mt] = x;
+                l[mt] *= f;
+#pragma unroll
+                for (int d = 0; d < DT16; ++d) o[mt][d] *= f;
+            }
+            far = far_references<MT>(m);
+        }
+        if (__builtin_expect(far, 0)) {
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int i = 0; i < 8 * SUBS; ++i) {
+                    f32x4& x = s[i / 8][(i / 4) & 1][mt];
+                    x[i & 3] = far_distance(x[i & 3], a.c, m[mt]);
+                }
+        }
+        const float c = far ? 1.0f : a.c;
+#pragma unroll
+        for (int u = 0; u < SUBS; ++u) {
+            u32x4 pf[MT];
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+                const float ref = far ? 0.0f : m[mt];
+                float p[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[u][i / 4][mt][i & 3], c, -ref));
+                    l[mt] += p[i];
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) pf[mt][i] = pack2<DT>(p[2 * i], p[2 * i + 1]);
+            }
+#pragma unroll
+            for (int d = 0; d < DT16; ++d)
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) o[mt][d] = mfma_16x16x32<DT>(vf[d], pf[mt], o[mt][d]);
+            if (u + 1 < SUBS) v_columns(u + 1, vf);
+        }
+    };
+    while (kb < st.end) {
+        const bool more = kb + KT < st.end;
+        if (more) fetch(kb + KT, next);
+        const Pages after = look(kb + 2 * KT);
+        if (!idle) {
+            if (plain(kb, now)) use(std::false_type{});
+            else use(std::true_type{});
+        }
+        if (more) keep(buf ^ 1, kb + KT, next);
+        __syncthreads();
+        now = next;
+        next = after;
+        kb += KT;
+        buf ^= 1;
+    }
+    const int32_t wild_from = *s_wild;  // (before the last barrier)
+    if (idle) return;
+    if (wild_from != INT32_MAX) {
+#pragma unroll 1
+        for (kb = wild_from; kb < st.end; kb += KT) {
+            const Pages p = look(kb);
+            if (plain(kb, p)) continue;  // (its values went into the products as they are)
+#pragma unroll 1
+            for (int32_t x = 0; x < min(KT, st.total - kb); ++x) {
+                int32_t page = p.p[0];
+#pragma unroll
+                for (int g = 1; g < GR; ++g) page = x / 16 == g ? p.p[g] : page;
+                if (page < 0) continue;
+                const char* row = st.v + page * a.v_page +
+                                  (int64_t)(grain_in_page(a, st, kb / 16 + x / 16) * 16 + x % 16) * a.v_pos;
+                bool see[MT];
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) see[mt] = sees(view[mt], kb + x - st.context);
+                // accumulator i of tile d holds column d * 16 + lg * 4 + i
+#pragma unroll
+                for (int d = 0; d < DT16; ++d) {
+                    const u32x2 w = *(const SV_GLOBAL u32x2*)(row + (d * 16 + lg * 4) * 2);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t bad = w[i / 2] ^ finite_halves<DT>(w[i / 2]);
+                        const float v = i % 2 ? hi16<DT>(bad) : lo16<DT>(bad);
+#pragma unroll
+                        for (int mt = 0; mt < MT; ++mt)
+                            if (see[mt]) o[mt][d][i] += v;
+                    }
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+        l[mt] += __shfl_xor(l[mt], 16, kWave);
+        l[mt] += __shfl_xor(l[mt], 32, kWave);
+        const int32_t r = r0 + mt * 16 + l16;
+        if (r >= m_total) continue;
+        const int32_t t = r / a.rep, h = st.hk * a.rep + (r - t * a.rep);
+        if (to.whole) {
+            const float inv = l[mt] != 0.0f ? 1.0f / l[mt] : 0.0f;
+            char* dst = a.out + (int64_t)(st.row0 + t) * a.out_row + (int64_t)h * a.out_head + lg * 8;
+#pragma unroll
+            for (int d = 0; d < DT16; ++d)
+                store4<DT>(dst + d * 32, o[mt][d][0] * inv, o[mt][d][1] * inv, o[mt][d][2] * inv, o[mt][d][3] * inv);
+            if (a.lse != nullptr && lg == 0)
+                a.lse[(int64_t)(st.row0 + t) * a.q_heads + h] =
+                    l[mt] != 0.0f ? (m[mt] + __builtin_amdgcn_logf(l[mt])) * 0.69314718055994531f : neg_inf();
+        } else {
+            const int64_t at = to.slot * TA::ROWS + wave * (MT * 16) + mt * 16 + l16;
+            if (lg == 0) a.ml[at] = float2{m[mt], l[mt]};
+            SV_GLOBAL f32x4* dst = (SV_GLOBAL f32x4*)(a.acc + at * D + lg * 4);
+#pragma unroll
+            for (int d = 0; d < DT16; ++d) dst[d * 4] = o[mt][d];
+        }
+    }
+}
+
+// Rounds of a pair's keys: what the line counts.
+template <bool TILES>
+constexpr int kTreeRound = TILES ? 64 : kKeyRound;
+
+// The line's length and where a stretch begins, by all threads of the workgroup: thread t sums the sequences t * per
+// .. t * per + per - 1.
+struct TreeStart {
+    int32_t total, stretch;  // rounds of the line, and of one workgroup
+    int32_t b, at;           // the sequence that holds the first round, and the rounds of it before that one
+};
+template <int KB>
+__device__ __forceinline__ TreeStart tree_start(const TreeArgs& a, int32_t group, bool write, int32_t* s_sum,
+                                                int32_t* s_found)
+{
+    const int32_t tid = (int32_t)threadIdx.x, per = (a.batch + kAttnThreads - 1) / kAttnThreads;
+    const int32_t b0 = min(tid * per, a.batch), b1 = min(b0 + per, a.batch);
+    int32_t mine = 0;
+    for (int32_t b = b0; b < b1; ++b) mine += (tree_length(a, b) + KB - 1) / KB * a.kv_heads;
+    const int32_t incl = wave_incl_scan_int(mine);
+    if (lane_id() == kWave - 1) s_sum[wave_id()] = incl;
+    __syncthreads();
+    int32_t before = incl - mine, total = 0;
+#pragma unroll
+    for (int w = 0; w < kAttnWaves; ++w) {
+        const int32_t x = s_sum[w];
+        before += w < wave_id() ? x : 0;
+        total += x;
+    }
+    const int32_t stretch = max(1, (total + a.groups - 1) / a.groups);
+    const int64_t from = (int64_t)group * stretch;
+    if (write) {
+        int32_t sum = before;
+        for (int32_t b = b0; b < b1; ++b) {
+            a.plan[b] = sum;
+            sum += (tree_length(a, b) + KB - 1) / KB * a.kv_heads;
+        }
+        if (tid == 0) {
+            a.plan[a.batch] = total;
+            a.plan[a.batch + 1] = stretch;
+        }
+    }
+    if (from >= before && from < before + mine) {
+        int32_t sum = before, b = b0;
+        while (true) {
+            const int32_t n = (tree_length(a, b) + KB - 1) / KB * a.kv_heads;
+            if (from < sum + n) break;
+            sum += n;
+            ++b;
+        }
+        s_found[0] = b;
+        s_found[1] = (int32_t)(from - sum);
+    }
+    __syncthreads();
+    return TreeStart{total, stretch, s_found[0], s_found[1]};
+}
+
+constexpr double kTreePastCaches = 128e6;  // bytes of keys and values from which they are read past the caches
+
+template <int DT, int D, bool TILES, int MT>
+__global__ __launch_bounds__(kAttnThreads, D == 256 ? 1 : 2) void tree_part_kernel(TreeArgs a)
+{
+    constexpr int ROWS = TILES ? TileAttention<DT, D, MT>::ROWS : MT * 16;
+    constexpr int KB = kTreeRound<TILES>;
+    constexpr size_t kLds = TILES ? (size_t)TileAttention<DT, D, MT>::LDS : tree_rows_lds<D, MT>();
+    // The stretches count on two workgroups per CU: more than a third of the 160 KB keeps a third one out.
+    constexpr size_t kLdsOfTwo = 52 * 1024;
+    __shared__ __align__(16) char s_mem[D != 256 && kLds < kLdsOfTwo ? kLdsOfTwo : kLds];
+    __shared__ uint32_t s_view[ROWS * kTreeWords];
+    __shared__ int32_t s_up[kTreeMostGuesses], s_sum[kAttnWaves], s_found[2], s_wild;
+    // the row tiles of one stretch (the same keys) run on one XCD (workgroups go to the 8 XCDs in turn)
+    const uint32_t x = blockIdx.x & 7u, y = blockIdx.x >> 3;
+    const int32_t group = a.tiles == 1 ? (int32_t)blockIdx.x : (int32_t)(y / (uint32_t)a.tiles * 8u + x);
+    const int32_t tile = a.tiles == 1 ? 0 : (int32_t)(y % (uint32_t)a.tiles);
+    if (group >= a.groups) return;
+    const TreeStart start = tree_start<KB>(a, group, group == 0 && tile == 0, s_sum, s_found);
+    int64_t at = (int64_t)group * start.stretch;
+    if (at >= start.total) return;
+    const int64_t end = min(at + start.stretch, (int64_t)start.total);
+    const bool past = a.tiles == 1 && (double)start.total * (KB * D * 4.0) > kTreePastCaches;
+    int32_t b = __builtin_amdgcn_readfirstlane(start.b);
+    int32_t in = __builtin_amdgcn_readfirstlane(start.at);  // rounds of sequence b before `at`
+    bool first = true;
+    while (at < end) {
+        const int32_t len = __builtin_amdgcn_readfirstlane(tree_length(a, b)), n = (len + KB - 1) / KB;
+        if (in >= n * a.kv_heads) {  // (also the empty sequences)
+            in -= n * a.kv_heads;
+            ++b;
+            continue;
+        }
+        const int32_t hk = in / n, j = in - hk * n;
+        const int32_t take = (int32_t)min((int64_t)(n - j), end - at);
+        Stretch st;
+        st.b = b;
+        st.hk = hk;
+        st.row0 = __builtin_amdgcn_readfirstlane(tree_row(a, b));
+        st.nrows = __builtin_amdgcn_readfirstlane(min(tree_row(a, b + 1) - st.row0, a.kmax + 1));
+        st.total = len;
+        st.context = len - st.nrows;
+        st.begin = j * KB;
+        st.end = min((j + take) * KB, len);
+        st.k = a.k + (int64_t)hk * a.k_head;
+        st.v = a.v + (int64_t)hk * a.v_head;
+        st.table = a.table != nullptr ? a.table + (int64_t)b * a.table_stride : nullptr;
+        st.parents = a.parents != nullptr ? a.parents + (st.row0 - b) : nullptr;
+        st.past = past;
+        if (tile * ROWS < st.nrows * a.rep) {
+            const int32_t t0 = tile * ROWS / a.rep;
+            __syncthreads();  // (the stretch before this one is done with the LDS)
+            if (st.end > st.context) tree_views(st, t0, min(st.nrows, ((tile + 1) * ROWS - 1) / a.rep + 1) - t0, s_up, s_view);
+            const TreeOut to{j == 0 && take == n, ((int64_t)group * 2 + (first ? 0 : 1)) * a.tiles + tile};
+            if constexpr (TILES) attend_tree_tiles<DT, D, MT>(a, st, tile, to, s_view, &s_wild, s_mem);
+            else attend_rows<DT, D, MT>(a, st, tile, to, s_view, (float*)s_mem);
+        }
+        at += take;
+        in += take;
+        first = false;
+    }
+}
+
+// Join of the parts: one wave per (row, head), D / 4 lanes over the columns of a part and kWave / (D / 4) parts side by
+// side.  A pair that one workgroup finished is left alone; rows that see nothing get zeros.
+template <int DT, int D, int ROWS>
+__global__ __launch_bounds__(kThreads) void tree_join_kernel(TreeArgs a)
+{
+    constexpr int LPP = D / 4;        // lanes per part
+    constexpr int PPR = kWave / LPP;  // parts per round
+    const int64_t i = (int64_t)blockIdx.x * kWaves + wave_id();
+    const int32_t heads = a.q_heads;
+    const int64_t ik = i / heads;
+    const int32_t h = (int32_t)(i - ik * heads), b = (int32_t)(ik / (a.kmax + 1)), k = (int32_t)(ik - (int64_t)b * (a.kmax + 1));
+    if (b >= a.batch) return;
+    const int32_t row0 = tree_row(a, b), nrows = min(tree_row(a, b + 1) - row0, a.kmax + 1);
+    if (k >= nrows) return;
+    const int32_t begin = a.plan[b], rounds = (a.plan[b + 1] - begin) / a.kv_heads, stretch = a.plan[a.batch + 1];
+    const int32_t hk = h / a.rep, r = k * a.rep + (h - hk * a.rep), tile = r / ROWS;
+    const int32_t from = begin + hk * rounds;
+    const int32_t g0 = from / stretch, parts = rounds > 0 ? (from + rounds - 1) / stretch - g0 + 1 : 0;
+    if (parts == 1) return;
+    const int lane = lane_id(), col = (lane % LPP) * 4, sub = lane / LPP;
+    // the first part lies in its workgroup's second place if the workgroup began with another pair
+    auto place = [&](int32_t p) {
+        const int64_t slot = (int64_t)(g0 + p) * 2 + (p == 0 && from != g0 * stretch ? 1 : 0);
+        return (slot * a.tiles + tile) * ROWS + (r - tile * ROWS);
+    };
+    float m = kNoReference;
+    for (int32_t p = lane; p < parts; p += kWave) m = fmaxf(m, a.ml[place(p)].x);
+    m = wave_max_dpp(m);
+    float l = 0.0f;
+    f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+    for (int32_t p = sub; p < parts; p += PPR) {
+        const int64_t at = place(p);
+        const float2 ml = a.ml[at];
+        const f32x4 v = *(const SV_GLOBAL f32x4*)(a.acc + at * D + col);
+        if (ml.y == 0.0f) continue;  // nothing in this part (l is NaN where a row sees a NaN)
+        const float w = __builtin_amdgcn_exp2f(ml.x - m);
+        l += ml.y * w;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[e] += v[e] * w;
+    }
+#pragma unroll
+    for (int x = LPP; x < kWave; x <<= 1) {
+        l += __shfl_xor(l, x, kWave);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[e] += __shfl_xor(o[e], x, kWave);
+    }
+    if (sub != 0) return;
+    const float inv = l != 0.0f ? 1.0f / l : 0.0f;
+    store4<DT>(a.out + (int64_t)(row0 + k) * a.out_row + (int64_t)h * a.out_head + col * 2, o.x * inv, o.y * inv, o.z * inv,
+               o.w * inv);
+    if (a.lse != nullptr && lane == 0)
+        a.lse[(int64_t)(row0 + k) * heads + h] =
+            l != 0.0f ? (m + __builtin_amdgcn_logf(l)) * 0.69314718055994531f : neg_inf();
+}
+
+}  // namespace sv

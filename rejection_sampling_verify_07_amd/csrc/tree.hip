@@ -1,5 +1,5 @@
-// C ABI of the calls around the scoring of trees of guesses: edits of logits.
-// Argument checks and kernel launches; the operations are documented in
+// C ABI of the calls around the scoring of trees of guesses: edits of logits and
+// attention over paged caches.  Argument checks, workspace layout and kernel launches; the operations are documented in
 // include/specverify.h.
 #include "specverify.h"
 #include "specverify_profile.h"
@@ -12,8 +12,9 @@
 #include "sv_common.hpp"
 #include "sv_host.hpp"
 #include "sv_adjust.hpp"
+#include "sv_tree_attention.hpp"
 
-static_assert(SV_MAX_DRAFT == sv::kAdjustMost, "draft limit mismatch");
+static_assert(SV_MAX_DRAFT == sv::kAdjustMost && SV_MAX_DRAFT == sv::kTreeMostGuesses, "draft limit mismatch");
 
 namespace {
 
@@ -117,9 +118,195 @@ sv_status_t adjust_logits_common(const sv_adjust_shape_t* sh, const sv_adjust_t*
     });
 }
 
+// ---- attention over paged caches
+
+// Workgroups that the line of keys is dealt to: two per CU, one where the registers hold no second one.
+constexpr int32_t kTreeGroups = 512;
+constexpr int32_t kTreeGroupsWide = 256;
+
+struct TreePlan {
+    bool tiles;
+    int32_t mt, wg_rows, row_tiles, groups, rows, capacity;
+    int64_t grid, join;
+    size_t off_plan, off_ml, off_acc, bytes;
+};
+
+TreePlan tree_plan(const sv_tree_shape_t* sh)
+{
+    TreePlan p{};
+    p.rows = sh->total_draft + sh->batch;
+    p.capacity = sh->max_pages * sh->page_size;
+    const int32_t rep = sh->q_heads / sh->kv_heads;
+    const int64_t rows = (int64_t)(sh->max_draft + 1) * rep;  // of one key head
+    const int32_t most = sh->head_dim == 256 ? 1 : 2;         // 16-row tiles per wave that the registers hold
+    p.tiles = rows > most * 16;
+    p.mt = p.tiles ? (rows <= sv::kAttnWaves * 16 ? 1 : most) : rows <= 16 ? 1 : most;
+    p.wg_rows = p.mt * 16 * (p.tiles ? sv::kAttnWaves : 1);
+    p.row_tiles = (int32_t)((rows + p.wg_rows - 1) / p.wg_rows);
+    const int32_t kb = p.tiles ? sv::kTreeRound<true> : sv::kTreeRound<false>;
+    const int64_t rounds = (int64_t)sh->batch * sh->kv_heads * (((int64_t)p.capacity + kb - 1) / kb);
+    const int64_t target = std::max((sh->head_dim == 256 ? kTreeGroupsWide : kTreeGroups) / p.row_tiles, 1);
+    p.groups = (int32_t)std::min(target, rounds);
+    p.grid = p.row_tiles == 1 ? p.groups : (int64_t)(p.groups + 7) / 8 * 8 * p.row_tiles;
+    p.join = (int64_t)sh->batch * (sh->max_draft + 1) * sh->q_heads;
+    const size_t slots = 2 * (size_t)p.groups * (size_t)p.row_tiles * (size_t)p.wg_rows;
+    p.off_plan = 0;
+    p.off_ml = align_up((size_t)(sh->batch + 2) * 4);
+    p.off_acc = align_up(p.off_ml + slots * sizeof(float2));
+    p.bytes = align_up(p.off_acc + slots * (size_t)sh->head_dim * sizeof(float));
+    return p;
+}
+
+sv_status_t check_tree(const sv_tree_shape_t* sh, float scale)
+{
+    if (sh == nullptr) return SV_ERR_INVALID_ARGUMENT;
+    const int32_t dt = dtype_of(sh);
+    if (dt != SV_DTYPE_F32 && dt != SV_DTYPE_BF16 && dt != SV_DTYPE_F16) return SV_ERR_INVALID_ARGUMENT;
+    if (sh->batch < 1 || sh->max_draft < 0 || sh->total_draft < 0 || sh->q_heads < 1 || sh->kv_heads < 1 ||
+        sh->head_dim < 1 || sh->pages < 1 || sh->page_size < 1 || sh->max_pages < 1)
+        return SV_ERR_INVALID_ARGUMENT;
+    if (sh->q_heads % sh->kv_heads != 0) return SV_ERR_INVALID_ARGUMENT;
+    const int64_t all = (int64_t)sh->batch * sh->max_draft;
+    if (sh->total_draft > all || (sh->cu_draft == nullptr && sh->total_draft != all)) return SV_ERR_INVALID_ARGUMENT;
+    if (sh->page_table == nullptr ? sh->max_pages != 1 || sh->pages < sh->batch
+                                  : sh->batch > 1 && sh->table_stride < sh->max_pages)
+        return SV_ERR_INVALID_ARGUMENT;
+    for (const int32_t* p : {sh->cu_draft, sh->parents, sh->lengths, sh->page_table})
+        if (!aligned(p, 4)) return SV_ERR_INVALID_ARGUMENT;
+    if (!(scale > 0.0f) || !isfinite(scale) || !isfinite((float)((double)scale * 1.4426950408889634)))
+        return SV_ERR_INVALID_ARGUMENT;
+    if (dt == SV_DTYPE_F32) return SV_ERR_UNSUPPORTED;
+    if (sh->head_dim != 64 && sh->head_dim != 128 && sh->head_dim != 256) return SV_ERR_UNSUPPORTED;
+    if (sh->page_table != nullptr && sh->page_size % 16 != 0) return SV_ERR_UNSUPPORTED;
+    if (sh->max_draft > SV_MAX_DRAFT || (int64_t)sh->max_pages * sh->page_size > kMaxPositions)
+        return SV_ERR_UNSUPPORTED;
+    if (((int64_t)sh->total_draft + sh->batch) * sh->q_heads > INT32_MAX / 2) return SV_ERR_UNSUPPORTED;
+    if ((int64_t)(sh->q_heads / sh->kv_heads) * (sh->max_draft + 1) > INT32_MAX / 256) return SV_ERR_UNSUPPORTED;
+    if ((double)sh->batch * sh->kv_heads * ((double)sh->max_pages * sh->page_size / 64 + 1) > (double)INT32_MAX)
+        return SV_ERR_UNSUPPORTED;
+    if (sh->table_stride > INT64_MAX / 8 / sh->batch) return SV_ERR_UNSUPPORTED;
+    const TreePlan p = tree_plan(sh);
+    if (!launchable((double)p.grid, sv::kAttnThreads) || !launchable((double)(p.join / sv::kWaves + 1), sv::kThreads))
+        return SV_ERR_UNSUPPORTED;
+    return SV_OK;
+}
+
+template <int DT, int D, bool TILES, int MT>
+sv_status_t run_tree(const TreePlan& p, const sv::TreeArgs& a, hipStream_t stream, const sv_profile_events_t* prof)
+{
+    launch_stream_nt(prof, sv::tree_part_kernel<DT, D, TILES, MT>, (uint32_t)p.grid, sv::kAttnThreads, stream, a);
+    if (launch_status() != SV_OK) return SV_ERR_HIP;
+    constexpr int ROWS = MT * 16 * (TILES ? sv::kAttnWaves : 1);
+    hipLaunchKernelGGL((sv::tree_join_kernel<DT, D, ROWS>), dim3((uint32_t)((p.join + sv::kWaves - 1) / sv::kWaves)),
+                       dim3(sv::kThreads), 0, stream, a);
+    return launch_status();
+}
+
+sv_status_t tree_attention_common(const sv_tree_shape_t* sh, const void* q, const sv_cache_t* k, const sv_cache_t* v,
+                                  float scale, void* out, float* out_lse, void* workspace, size_t* workspace_bytes,
+                                  hipStream_t stream, const sv_profile_events_t* prof)
+{
+    if (workspace_bytes == nullptr) return SV_ERR_INVALID_ARGUMENT;
+    const sv_status_t st = check_tree(sh, scale);
+    if (st != SV_OK) return st;
+    const TreePlan p = tree_plan(sh);
+    if (workspace == nullptr) {
+        *workspace_bytes = p.bytes;
+        return SV_OK;
+    }
+    if (q == nullptr || out == nullptr || !aligned(q, 16) || !aligned(out, 8) || !aligned(out_lse, 4) ||
+        !aligned(workspace, kAlign))
+        return SV_ERR_INVALID_ARGUMENT;
+    if (sh->q_row_stride < 0 || sh->q_head_stride < 0 || sh->q_row_stride % 8 != 0 || sh->q_head_stride % 8 != 0 ||
+        sh->out_row_stride < 0 || sh->out_head_stride < 0 || sh->out_row_stride % 4 != 0 ||
+        sh->out_head_stride % 4 != 0)
+        return SV_ERR_INVALID_ARGUMENT;
+    if (!distinct_rows(sh->out_row_stride, p.rows, sh->out_head_stride, sh->q_heads, sh->head_dim))
+        return SV_ERR_INVALID_ARGUMENT;
+    if (!cache_ok(k) || !cache_ok(v)) return SV_ERR_INVALID_ARGUMENT;
+    for (const sv_cache_t* c : {k, v})
+        if (c->position_stride * 2 > kMaxPosStride) return SV_ERR_UNSUPPORTED;
+    if (*workspace_bytes < p.bytes) return SV_ERR_WORKSPACE_TOO_SMALL;
+    sv::TreeArgs a{};
+    a.q = static_cast<const char*>(q);
+    a.k = static_cast<const char*>(k->data);
+    a.v = static_cast<const char*>(v->data);
+    a.out = static_cast<char*>(out);
+    a.lse = out_lse;
+    a.q_row = sh->q_row_stride * 2;
+    a.q_head = sh->q_head_stride * 2;
+    a.out_row = sh->out_row_stride * 2;
+    a.out_head = sh->out_head_stride * 2;
+    a.k_page = k->batch_stride * 2;
+    a.k_head = k->head_stride * 2;
+    a.v_page = v->batch_stride * 2;
+    a.v_head = v->head_stride * 2;
+    a.k_pos = (int32_t)(k->position_stride * 2);
+    a.v_pos = (int32_t)(v->position_stride * 2);
+    a.cu = sh->cu_draft;
+    a.parents = sh->total_draft > 0 ? sh->parents : nullptr;
+    a.lengths = sh->lengths;
+    a.table = sh->page_table;
+    a.table_stride = sh->table_stride;
+    a.batch = sh->batch;
+    a.rows = p.rows;
+    a.kmax = sh->max_draft;
+    a.pages = sh->pages;
+    a.capacity = p.capacity;
+    // g / grains as (g * mul) >> shift, exact for g < 2^31: mul = ceil(2^shift / grains) exceeds 2^shift / grains by less
+    // than 1, and 2^shift >= 2^31 * grains
+    a.grains = (uint32_t)std::max(sh->page_size / 16, 1);
+    a.grains_shift = 31;
+    while ((1ull << (a.grains_shift - 31)) < a.grains) ++a.grains_shift;
+    a.grains_mul = (uint32_t)(((1ull << a.grains_shift) + a.grains - 1) / a.grains);
+    a.q_heads = sh->q_heads;
+    a.kv_heads = sh->kv_heads;
+    a.rep = sh->q_heads / sh->kv_heads;
+    a.c = (float)((double)scale * 1.4426950408889634);
+    a.groups = p.groups;
+    a.tiles = p.row_tiles;
+    a.plan = ws_at<int32_t>(workspace, p.off_plan);
+    a.ml = ws_at<float2>(workspace, p.off_ml);
+    a.acc = ws_at<float>(workspace, p.off_acc);
+    const auto by_rows = [&](auto dt, auto dim) -> sv_status_t {
+        constexpr int DT = decltype(dt)::value, D = decltype(dim)::value;
+        if constexpr (DT == sv::DT_F32) {
+            return SV_ERR_UNSUPPORTED;
+        } else if constexpr (D == 256) {
+            return p.tiles ? run_tree<DT, D, true, 1>(p, a, stream, prof) : run_tree<DT, D, false, 1>(p, a, stream, prof);
+        } else {
+            if (p.tiles && p.mt == 2) return run_tree<DT, D, true, 2>(p, a, stream, prof);
+            if (p.tiles) return run_tree<DT, D, true, 1>(p, a, stream, prof);
+            if (p.mt == 2) return run_tree<DT, D, false, 2>(p, a, stream, prof);
+            return run_tree<DT, D, false, 1>(p, a, stream, prof);
+        }
+    };
+    return by_dtype(sh->dtype, [&](auto dt) -> sv_status_t {
+        switch (sh->head_dim) {
+            case 64: return by_rows(dt, std::integral_constant<int, 64>{});
+            case 128: return by_rows(dt, std::integral_constant<int, 128>{});
+            default: return by_rows(dt, std::integral_constant<int, 256>{});
+        }
+    });
+}
+
 }  // namespace
 
 extern "C" {
+
+sv_status_t spec_tree_attention(const sv_tree_shape_t* shape, const void* q, const sv_cache_t* k, const sv_cache_t* v,
+                                float scale, void* out, float* out_lse, void* workspace, size_t* workspace_bytes,
+                                hipStream_t stream)
+{
+    return tree_attention_common(shape, q, k, v, scale, out, out_lse, workspace, workspace_bytes, stream, nullptr);
+}
+
+sv_status_t spec_tree_attention_profiled(const sv_profile_events_t* events, const sv_tree_shape_t* shape, const void* q,
+                                         const sv_cache_t* k, const sv_cache_t* v, float scale, void* out,
+                                         float* out_lse, void* workspace, size_t* workspace_bytes, hipStream_t stream)
+{
+    return tree_attention_common(shape, q, k, v, scale, out, out_lse, workspace, workspace_bytes, stream, events);
+}
 
 sv_status_t spec_adjust_logits(const sv_adjust_shape_t* shape, const sv_adjust_t* adjust, const void* logits, void* out,
                                hipStream_t stream)

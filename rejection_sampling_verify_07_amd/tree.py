@@ -1,6 +1,7 @@
-"""ctypes binding of the calls on trees of guesses (spec_adjust_logits,
-spec_verify_tree_greedy, spec_verify_tree_sample; include/specverify.h): argument
-marshalling only.  Streams, devices and plans are as in beam.py.
+"""ctypes binding of the calls on trees of guesses (spec_tree_attention,
+spec_adjust_logits, spec_verify_tree_greedy, spec_verify_tree_sample;
+include/specverify.h): argument marshalling only.  Streams, devices and plans are
+as in beam.py.
 """
 from __future__ import annotations
 
@@ -10,8 +11,9 @@ from typing import Optional
 import torch
 
 from . import binding as _b
-from .beam import _DevicePlan, _vector, _workspace
+from .beam import CacheT, _DevicePlan, _rows3, _vector, _workspace
 from .binding import _check, _on, load_library
+from .pages import _batch, _table
 
 
 class AdjustShapeT(C.Structure):
@@ -247,3 +249,115 @@ def verify_tree_sample(target_logits: torch.Tensor, draft_ids: torch.Tensor, par
     """
     return TreeSamplePlan(target_logits, draft_ids, parents, cu_draft, temperature, top_k, top_p, seed, offset,
                           max_draft, out, workspace, stream)()
+
+
+class TreeShapeT(C.Structure):
+    """sv_tree_shape_t."""
+    _fields_ = ([(n, C.c_int32) for n in ("batch", "max_draft", "total_draft", "q_heads", "kv_heads", "head_dim", "pages",
+                                          "page_size", "max_pages", "dtype")]
+                + [(n, C.c_int64) for n in ("table_stride", "q_row_stride", "q_head_stride", "out_row_stride",
+                                            "out_head_stride")]
+                + [(n, C.c_void_p) for n in ("cu_draft", "parents", "lengths", "page_table")])
+
+
+def _pages(t, name, q, shape):
+    """The C cache of [pages, page_size, kv_heads, head_dim]."""
+    if t.dtype != q.dtype:
+        raise TypeError(f"{name} is {t.dtype} but q is {q.dtype}")
+    if t.device != q.device:
+        raise ValueError(f"{name} is on {t.device} but q is on {q.device}")
+    if t.dim() != 4 or tuple(t.shape) != shape:
+        raise ValueError(f"{name} is {tuple(t.shape)}; [pages, page_size, kv_heads, head_dim] = {shape} is needed")
+    if t.stride(3) != 1:
+        raise ValueError(f"{name} must have unit stride in its last dimension")
+    return CacheT(t.data_ptr(), *[t.stride(i) if t.shape[i] > 1 else 0 for i in range(3)])
+
+
+class TreeAttentionPlan(_DevicePlan):
+    """spec_tree_attention with every argument marshalled once: __call__ enqueues
+    one call and returns {"out"} and, with return_lse, {"lse"}, the same tensors
+    every time.  See tree_attention."""
+
+    name = "spec_tree_attention"
+
+    def __init__(self, q, k, v, page_table=None, lengths=None, parents=None, cu_draft=None, max_draft=None, scale=None,
+                 return_lse=False, out=None, workspace=None, stream=None):
+        lib = load_library()
+        if q.dim() != 3:
+            raise ValueError("q must be [rows, q_heads, head_dim]")
+        if k.dim() != 4:
+            raise ValueError("k must be [pages, page_size, kv_heads, head_dim]")
+        rows, q_heads, dim = q.shape
+        pages, page_size, kv_heads, _ = k.shape
+        if q.numel() == 0 or k.numel() == 0 or q_heads % kv_heads != 0:
+            raise ValueError(f"{rows} rows, {q_heads} query heads, {pages} pages of {page_size} positions and {kv_heads} "
+                             "key/value heads do not fit together")
+        code = _b._dtype_code(q)
+        dev, dtype = q.device, q.dtype
+        if dev.type != "cuda":
+            raise ValueError("q must be on a GPU")
+        caches = [_pages(t, n, q, (pages, page_size, kv_heads, dim)) for n, t in (("k", k), ("v", v))]
+        # sequences: what tells their number first
+        counts = [("cu_draft", cu_draft, -1), ("page_table", page_table, 0), ("lengths", lengths, 0)]
+        batch = next((t.shape[0] + extra for _, t, extra in counts if t is not None),
+                     rows if parents is None else rows - parents.numel())
+        if batch < 1:
+            raise ValueError(f"{rows} rows do not fit {batch} sequences")
+        kmax, total = _batch(rows, cu_draft, max_draft, batch, stream)
+        if page_table is None:
+            if pages < batch:
+                raise ValueError(f"k holds {pages} sequences; {batch} are needed without a page_table")
+            table, max_pages, stride = None, 1, 1
+        else:
+            table, max_pages, stride = _table(page_table, "page_table", batch, dev)
+        cu, ups, used = [None if t is None else _vector(t, n, c, torch.int32, dev) for n, t, c in (
+            ("cu_draft", cu_draft, batch + 1), ("parents", parents, total), ("lengths", lengths, batch))]
+        with _on(dev, stream):
+            if out is None:
+                out = {"out": torch.empty((rows, q_heads, dim), dtype=dtype, device=dev)}
+            if return_lse and out.get("lse") is None:
+                out = {**out, "lse": torch.empty((rows, q_heads), dtype=torch.float32, device=dev)}
+        o = out["out"]
+        if tuple(o.shape) != (rows, q_heads, dim) or o.dtype != dtype or o.device != dev:
+            raise ValueError(f"out['out'] must be {dtype} [{rows}, {q_heads}, {dim}] on {dev}")
+        lse = None
+        if out.get("lse") is not None:
+            lse = _vector(out["lse"], "out['lse']", rows * q_heads, torch.float32, dev)
+        shape = TreeShapeT(batch, kmax, total, q_heads, kv_heads, dim, pages, page_size, max_pages, code, stride,
+                           *_rows3(q, "q"), *_rows3(o, "out['out']"), cu, ups, used, table)
+        scale = dim ** -0.5 if scale is None else float(scale)
+        args = (C.byref(shape), C.c_void_p(q.data_ptr()), *[C.byref(c) for c in caches], C.c_float(scale),
+                C.c_void_p(o.data_ptr()), lse)
+        need = C.c_size_t(0)
+        _check(lib.spec_tree_attention(*args, None, C.byref(need), None), "spec_tree_attention(workspace query)")
+        with _on(dev, stream):
+            self.workspace = _workspace(workspace, need.value, dev)
+        self.out, self.shape = out, shape
+        self._own(dev, stream, self.workspace, *(t for t in out.values() if t is not None))
+        self.have = C.c_size_t(self.workspace.numel())
+        self._keep = (q, k, v, page_table, lengths, parents, cu_draft, caches)
+        self.args = (*args, C.c_void_p(self.workspace.data_ptr()), C.byref(self.have))
+        self.fn, self.fn_profiled = lib.spec_tree_attention, lib.spec_tree_attention_profiled
+
+
+def tree_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, page_table: Optional[torch.Tensor] = None,
+                   lengths: Optional[torch.Tensor] = None, parents: Optional[torch.Tensor] = None,
+                   cu_draft: Optional[torch.Tensor] = None, max_draft: Optional[int] = None,
+                   scale: Optional[float] = None, return_lse: bool = False, out: Optional[dict] = None,
+                   workspace: Optional[torch.Tensor] = None, stream=None) -> dict:
+    """Attention of every sequence's newest rows over its cache in pages, on the GPU
+    (spec_tree_attention).
+
+    q [sum(K_b + 1), q_heads, D], bfloat16 or float16, rows packed as the target
+    rows of a verify (one row per sequence at a plain decode step); k and v [pages,
+    page_size, kv_heads, D], the newest rows' keys and values written; page_table
+    int32 [batch, max_pages] (page_size a multiple of 16), or None: page b is
+    sequence b's whole cache; lengths int32 [batch], the positions in use with the
+    newest rows (None: all); parents int32 [sum(K_b)], the row (0 .. j) that guess
+    j extends, or None (chains); cu_draft int32 [batch + 1] or None (uniform K);
+    max_draft is read back from the device, on the call's stream, where it is
+    needed and not given.  scale defaults to D ** -0.5.  Returns out [rows, q_heads,
+    D] and, with return_lse, lse [rows, q_heads]; `out` may hold both, or out alone.
+    """
+    return TreeAttentionPlan(q, k, v, page_table, lengths, parents, cu_draft, max_draft, scale, return_lse, out,
+                             workspace, stream)()

@@ -126,3 +126,60 @@ def test_adjust_binding_refusals(T):
         T.adjust_logits(x)
     with pytest.raises(ValueError, match="2-D"):
         T.adjust_logits(x[0], draft_ids=i)
+
+
+# ---- spec_tree_attention
+def _tree(T, lib, q=FAKE, k=(FAKE, 4096, 256, 128), v=(FAKE, 4096, 256, 128), scale=0.1, out=FAKE, lse=None, ws=None, have=0,
+          **kw):
+    d = dict(batch=4, max_draft=5, total_draft=20, q_heads=8, kv_heads=2, head_dim=128, pages=50, page_size=16, max_pages=9,
+             dtype=1, table_stride=9, q_row_stride=1024, q_head_stride=128, out_row_stride=1024, out_head_stride=128,
+             page_table=FAKE)
+    d.update(kw)
+    n = C.c_size_t(have)
+    st = lib.spec_tree_attention(C.byref(T.TreeShapeT(**d)), q, C.byref(T.CacheT(*k)) if k else None,
+                                 C.byref(T.CacheT(*v)) if v else None, scale, out, lse, ws, C.byref(n), None)
+    return st, n.value
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(), 0), (dict(batch=0), 1), (dict(max_draft=-1), 1), (dict(total_draft=19), 1), (dict(total_draft=-1), 1),
+    (dict(total_draft=21, cu_draft=FAKE), 1), (dict(total_draft=7, cu_draft=FAKE), 0), (dict(q_heads=7), 1), (dict(kv_heads=0), 1),
+    (dict(pages=0), 1), (dict(page_size=0), 1), (dict(max_pages=0), 1), (dict(table_stride=8), 1), (dict(batch=1, max_draft=20, table_stride=0), 0),
+    (dict(page_table=None), 1), (dict(page_table=None, max_pages=1, pages=3), 1), (dict(page_table=None, max_pages=1, page_size=77), 0),
+    (dict(page_size=8), 2), (dict(page_size=40), 2), (dict(page_size=48), 0), (dict(dtype=0), 2), (dict(dtype=5), 1), (dict(head_dim=96), 2),
+    (dict(head_dim=0), 1), (dict(max_draft=129, total_draft=516), 2), (dict(max_draft=128, total_draft=512), 0),
+    (dict(max_pages=(1 << 26) + 1, table_stride=1 << 27), 2), (dict(max_pages=1 << 26, table_stride=1 << 26), 0),
+    (dict(max_pages=1 << 26, table_stride=1 << 26, batch=1 << 8, max_draft=0, total_draft=0), 2), (dict(table_stride=1 << 62), 2),
+    (dict(cu_draft=FAKE + 2, total_draft=7), 1), (dict(parents=FAKE + 2), 1), (dict(lengths=FAKE + 1), 1), (dict(page_table=FAKE + 2), 1),
+    (dict(scale=0.0), 1), (dict(scale=-1.0), 1), (dict(scale=float("nan")), 1), (dict(scale=3e38), 1), (dict(q_heads=1 << 24, kv_heads=1), 2)])
+def test_tree_shapes(T, lib, kw, code):
+    st, need = _tree(T, lib, **kw)
+    assert st == code and (code or (need > 0 and need % 256 == 0))
+
+
+def test_tree_workspace_does_not_grow_with_the_caches(T, lib):
+    assert _tree(T, lib, max_pages=1 << 20, table_stride=1 << 20)[1] == _tree(T, lib, max_pages=1 << 14, table_stride=1 << 14)[1]
+
+
+def test_tree_pointers(T, lib):
+    need = _tree(T, lib)[1]
+    ok = dict(ws=FAKE, have=need)
+    for bad in (dict(q=None), dict(q=FAKE + 8), dict(out=None), dict(out=FAKE + 4), dict(lse=FAKE + 2), dict(k=None), dict(v=None),
+                dict(k=(None, 4096, 256, 128)), dict(k=(FAKE + 8, 4096, 256, 128)), dict(v=(FAKE, 4097, 256, 128)),
+                dict(v=(FAKE, 4096, 252, 128)), dict(k=(FAKE, 4096, 256, -128)), dict(q_row_stride=1020), dict(q_head_stride=-8),
+                dict(out_row_stride=1022), dict(out_head_stride=64), dict(out_row_stride=512), dict(ws=FAKE + 128)):
+        assert _tree(T, lib, **{**ok, **bad})[0] == 1, bad
+    assert _tree(T, lib, **ok, k=(FAKE, 1 << 40, 1 << 25, 128))[0] == 2
+    assert _tree(T, lib, ws=FAKE, have=need - 1)[0] == 3
+
+
+def test_tree_binding_refusals(T):
+    q, k = torch.zeros(6, 4, 64, dtype=torch.bfloat16), torch.zeros(9, 16, 2, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="GPU"):
+        T.tree_attention(q, k, k)
+    with pytest.raises(ValueError, match="q must be"):
+        T.tree_attention(q[0], k, k)
+    with pytest.raises(ValueError, match="k must be"):
+        T.tree_attention(q, k[0], k)
+    with pytest.raises(ValueError, match="do not fit"):
+        T.tree_attention(q[:, :3], k, k)

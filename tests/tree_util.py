@@ -191,3 +191,51 @@ def adjust_ref(logits, cu, tokens=None, lengths=None, prompt=None, rep=None, pre
                     bits = np.unpackbits(np.ascontiguousarray(masks[m]).view(np.uint8), bitorder="little")[:V]
                     out[row, bits == 0] = -np.inf
     return out, size
+
+
+# --------------------------------------------------------------------------
+# attention of trees over paged caches, in 64 bits
+# --------------------------------------------------------------------------
+def tree_attention_ref(q, k, v, table, lengths, parents, cu, scale, eps, tiny):
+    """q [rows, Hq, D]; k, v [pages, size, Hk, D] (float64); table [B, most] or None (page b is the cache of b).
+    Returns out, lse and how far a kernel with fp32 scores, weights rounded to the element type and fp32 sums may be
+    off each, with the reasons of beam_util.attention_ref: products exact in fp32 and D of them added there, 4
+    roundings on the way to the exponent, a weight rounded by eps / 2 (or `tiny`), n additions, out rounded once."""
+    rows, Hq, D = q.shape
+    pages, size, Hk, _ = k.shape
+    rep = Hq // Hk
+    out, lse = np.zeros((rows, Hq, D)), np.full((rows, Hq), -np.inf)
+    b_out, b_lse = np.zeros((rows, Hq, D)), np.zeros((rows, Hq))
+    for b in range(len(cu) - 1):
+        n = int(cu[b + 1] - cu[b]) + 1
+        up = [j if parents is None else int(parents[cu[b] + j]) for j in range(n - 1)]
+        up = [u if 0 <= u <= j else 0 for j, u in enumerate(up)]
+        cap = size if table is None else table.shape[1] * size
+        length = cap if lengths is None else min(max(int(lengths[b]), 0), cap)
+        at = np.arange(length)
+        page = np.full(length, b) if table is None else table[b][at // size]
+        there = (page >= 0) & (page < pages)
+        kk = np.where(there[:, None, None], k[np.where(there, page, 0), at % size], 0.0)
+        vv = np.where(there[:, None, None], v[np.where(there, page, 0), at % size], 0.0)
+        for r in range(n):
+            t = int(cu[b]) + b + r
+            way = np.array(way_up(up, r)) + length - n
+            see = there & (at < length - n)
+            see[way[way >= 0]] = there[way[way >= 0]]
+            if not see.any():
+                continue
+            for h in range(Hq):
+                ks, vs = kk[see, h // rep], vv[see, h // rep]
+                a = scale * (ks @ q[t, h])
+                d_s = (D + 4) * 2.0 ** -24 * scale * (np.abs(ks) @ np.abs(q[t, h])).max()
+                m = a.max()
+                w = np.exp(a - m)
+                z = w.sum()
+                w /= z
+                out[t, h], lse[t, h] = w @ vs, m + np.log(z)
+                d = 2 * d_s + 8 * np.abs(a).max() * 2.0 ** -24 + 2.0 ** -22
+                wv, c = w @ np.abs(vs), len(ks)
+                b_out[t, h] = (eps / 2 * np.abs(out[t, h]) + (eps / 2 + d + 2 * c * 2.0 ** -24) * wv
+                               + c * tiny * np.abs(vs).max() + tiny) * 1.01
+                b_lse[t, h] = d + c * 2.0 ** -24 + 4 * 2.0 ** -24 * (1 + np.abs(lse[t, h]))
+    return out, lse, b_out, b_lse
