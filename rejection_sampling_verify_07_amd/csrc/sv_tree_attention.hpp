@@ -15,7 +15,7 @@
 // grow with the caches, and sequences of any mix of lengths keep all CUs busy.
 //
 // Positions come in grains of 16, which never cross a page: a wave finds a
-// grain's page with scalar loads, one step before the keys' own loads.
+// grain's page in a window of the table that its lanes hold (PageWindow).
 //   Few rows per key head (up to 16 or 32): each wave walks its own 32 keys of a
 // round with all rows, K and V straight from memory to registers (attend_rows).
 //   More: the four waves share the rows and take tiles of 64 keys through LDS
@@ -40,7 +40,8 @@ struct TreeArgs {
     int64_t table_stride;
     int32_t batch, rows, kmax, pages, capacity;      // capacity: positions a sequence's pages hold
     int32_t grains_shift;                            // grains per page as a multiplication: (g * mul) >> shift
-    uint32_t grains_mul, grains;
+    uint32_t grains_mul;
+    int32_t grains;                                  // per page (without a table: all of a sequence's)
     int32_t q_heads, kv_heads, rep;
     float c;                                         // scale * log2(e)
     int32_t groups, tiles;                           // stretches of the line; row tiles
@@ -62,10 +63,10 @@ __device__ __forceinline__ int32_t tree_length(const TreeArgs& a, int32_t b)
     return a.lengths != nullptr ? min(max(a.lengths[b], 0), a.capacity) : a.capacity;
 }
 
-// A scalar load: the tables are not written while a kernel reads them.
-__device__ __forceinline__ int32_t scalar_load(const int32_t* p)
+// Number of the page that grain g of a sequence lies in.
+__device__ __forceinline__ int32_t page_of_grain(const TreeArgs& a, int32_t g)
 {
-    return *(const __attribute__((address_space(4))) int32_t*)p;
+    return (int32_t)(((uint64_t)(uint32_t)g * a.grains_mul) >> a.grains_shift);
 }
 
 // What one workgroup works on: a stretch of one (sequence, key head) pair.
@@ -76,25 +77,102 @@ struct Stretch {
     int32_t b, hk, row0, nrows;
     int32_t begin, end;      // keys
     int32_t total;           // positions of the sequence
+    int32_t pages;           // pages that they take
     int32_t context;         // those before the newest rows (below 0 if the newest rows are not all there)
     bool past;               // read past the caches
 };
 
-// The page of grain g (-1: none; keys at or past `total` have none).
-__device__ __forceinline__ int32_t grain_page(const TreeArgs& a, const Stretch& s, int32_t g)
+// The page of grain g, for the few that are looked up one by one (-1: none; keys at or past `total` have none).
+__device__ __forceinline__ int32_t grain_page(const TreeArgs& a, const Stretch& s, int32_t g, int32_t* in_page)
 {
+    const int32_t at = page_of_grain(a, g);
+    *in_page = (g - at * a.grains) * 16;
     if (g * 16 >= s.total) return -1;
-    if (s.table == nullptr) return s.b;
-    const uint32_t at = (uint32_t)(((uint64_t)(uint32_t)g * a.grains_mul) >> a.grains_shift);
-    const int32_t page = scalar_load(s.table + at);
+    const int32_t page = s.table != nullptr ? s.table[at] : s.b;
     return (uint32_t)page < (uint32_t)a.pages ? page : -1;
 }
-__device__ __forceinline__ int32_t grain_in_page(const TreeArgs& a, const Stretch& s, int32_t g)
-{
-    if (s.table == nullptr) return g;
-    const uint32_t at = (uint32_t)(((uint64_t)(uint32_t)g * a.grains_mul) >> a.grains_shift);
-    return g - (int32_t)(at * a.grains);
-}
+
+// The pages that a wave walks through, in rising order: lane i of `held` has page number at + i of the sequence, and
+// `ahead` those from at + 32 on, loaded long before they are needed.  A page is then one v_readlane away.
+struct PageWindow {
+    int32_t at, held, ahead;
+
+    __device__ __forceinline__ int32_t load(const TreeArgs& a, const Stretch& s, int32_t from) const
+    {
+        const int32_t i = from + lane_id();
+        int32_t page = -1;
+        if (i < s.pages) page = s.table != nullptr ? ((const SV_GLOBAL int32_t*)s.table)[i] : s.b;
+        return (uint32_t)page < (uint32_t)a.pages ? page : -1;
+    }
+    __device__ __forceinline__ void start(const TreeArgs& a, const Stretch& s, int32_t i)
+    {
+        at = i;
+        held = load(a, s, i);
+        ahead = load(a, s, i + 32);
+    }
+    // Pages i .. i + 32 can be had; i rises by less than 32 from call to call.
+    __device__ __forceinline__ void reach(const TreeArgs& a, const Stretch& s, int32_t i)
+    {
+        if (i - at < 32) return;
+        at += 32;
+        held = ahead;
+        ahead = load(a, s, at + 32);
+    }
+    __device__ __forceinline__ int32_t page(int32_t i) const { return __builtin_amdgcn_readlane(held, i - at); }
+};
+
+// Where N neighbouring grains lie: page (-1: none) and position in it.
+template <int N>
+struct Grains {
+    int32_t page[N], in[N];
+    __device__ __forceinline__ bool sound() const
+    {
+        int32_t x = 0;
+#pragma unroll
+        for (int g = 0; g < N; ++g) x |= page[g];
+        return x >= 0;
+    }
+};
+
+// Walks grains g, g + STEP, ...: N neighbours each time.
+template <int N, int STEP>
+struct GrainCursor {
+    PageWindow window;
+    int32_t number, rest;  // the next grain's page number, and its place in that page
+    int32_t key;           // its first key
+
+    __device__ __forceinline__ void start(const TreeArgs& a, const Stretch& s, int32_t first_key)
+    {
+        key = first_key;
+        number = page_of_grain(a, key / 16);
+        rest = key / 16 - number * a.grains;
+        window.start(a, s, number);
+    }
+    __device__ __forceinline__ Grains<N> next(const TreeArgs& a, const Stretch& s)
+    {
+        Grains<N> w;
+        window.reach(a, s, number);
+        int32_t n = number, r = rest;
+#pragma unroll
+        for (int g = 0; g < N; ++g) {
+            w.page[g] = key + g * 16 < s.total ? window.page(n) : -1;
+            w.in[g] = r * 16;
+            const bool over = ++r == a.grains;
+            n += over ? 1 : 0;
+            r = over ? 0 : r;
+        }
+        if constexpr (STEP == N) {
+            number = n;
+            rest = r;
+        } else {
+            const int32_t q = page_of_grain(a, rest + STEP);
+            number += q;
+            rest += STEP - q * a.grains;
+        }
+        key += STEP * 16;
+        return w;
+    }
+};
 
 // The rows that rows t0 .. t0 + n - 1 of the sequence see among the newest ones, as
 // bits from the sequence's row 0 on.  All threads of the workgroup call it.
@@ -192,43 +270,31 @@ __device__ __forceinline__ void attend_rows(const TreeArgs& a, const Stretch& st
     uint32_t voff[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) voff[j] = (uint32_t)((lg * 4 + j) * a.v_pos + l16 * (DPL * 2));
-    struct Pages {
-        int32_t p[2];
-    };
-    auto look = [&](int32_t kb) {
-        return Pages{{kb < st.end ? grain_page(a, st, kb / 16) : -1, kb < st.end ? grain_page(a, st, kb / 16 + 1) : -1}};
-    };
-    auto sound = [](const Pages& p) { return (p.p[0] | p.p[1]) >= 0; };
-    auto base_of = [&](const char* data, int64_t page_stride, int32_t pos_stride, const Pages& p, int32_t kb, int t) {
-        return data + max(p.p[t], 0) * page_stride +
-               (int64_t)(p.p[t] < 0 ? 0 : grain_in_page(a, st, kb / 16 + t) * 16) * pos_stride;
-    };
+    typedef Grains<2> Block;  // 32 keys
     // Rows of a grain that hold keys: the last one stands in for those behind it (masked below), row 0 of the pool for
     // all of a grain without a page.
-    auto last_of = [&](const Pages& p, int32_t kb, int t) {
-        return p.p[t] < 0 ? 0 : min(15, st.total - 1 - (kb + t * 16));
+    auto last_of = [&](const Block& p, int32_t kb, int t) {
+        return p.page[t] < 0 ? 0 : min(15, st.total - 1 - (kb + t * 16));
     };
-    auto load_k = [&](int32_t kb, const Pages& p, u32x4 (&kf)[2][DC], auto past) {
-        const bool edge = kb + kKeyBlock > st.total || !sound(p);
+    auto load_k = [&](int32_t kb, const Block& p, u32x4 (&kf)[2][DC], auto edge, auto past) {
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-            const char* base = base_of(st.k, a.k_page, a.k_pos, p, kb, t);
+            const char* base = st.k + max(p.page[t], 0) * a.k_page + (int64_t)(p.page[t] < 0 ? 0 : p.in[t]) * a.k_pos;
             uint32_t off = koff;
-            if (edge) off = (uint32_t)(min(l16, last_of(p, kb, t)) * a.k_pos + lg * 16);
+            if constexpr (decltype(edge)::value) off = (uint32_t)(min(l16, last_of(p, kb, t)) * a.k_pos + lg * 16);
 #pragma unroll
             for (int c = 0; c < DC; ++c) kf[t][c] = load16<decltype(past)::value>((const u32x4*)(base + off + c * 64));
         }
     };
-    auto load_v = [&](int32_t kb, const Pages& p, uint32_t (&vr)[8][VW], auto masked, auto past) {
+    auto load_v = [&](int32_t kb, const Block& p, uint32_t (&vr)[8][VW], auto edge, auto past) {
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-            const char* base = base_of(st.v, a.v_page, a.v_pos, p, kb, t);
-            const int32_t last = last_of(p, kb, t);
+            const char* base = st.v + max(p.page[t], 0) * a.v_page + (int64_t)(p.page[t] < 0 ? 0 : p.in[t]) * a.v_pos;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 uint32_t off = voff[j];
-                if constexpr (decltype(masked)::value)
-                    off = (uint32_t)(min(lg * 4 + j, last) * a.v_pos + l16 * (DPL * 2));
+                if constexpr (decltype(edge)::value)
+                    off = (uint32_t)(min(lg * 4 + j, last_of(p, kb, t)) * a.v_pos + l16 * (DPL * 2));
                 const char* x = base + off;
                 if constexpr (VW == 2) {
                     const u32x2 w = *(const SV_GLOBAL u32x2*)x;
@@ -248,18 +314,32 @@ __device__ __forceinline__ void attend_rows(const TreeArgs& a, const Stretch& st
 
     bool wild = false;  // (uniform) a masked block held a value that is not finite
     bool far = false;   // (uniform) a reference lies beyond kFarReference
-    int32_t kb = st.begin + wave * kKeyBlock, wild_from = st.end;
-    Pages now = look(kb), next = look(kb + kKeyRound);
+    int32_t kb = st.begin + wave * kKeyBlock;
+    GrainCursor<2, kKeyRound / 16> cursor;
+    cursor.start(a, st, kb);
+    Block now = cursor.next(a, st), next = cursor.next(a, st);
     u32x4 kf[2][DC];  // the block at hand; the next one's is loaded once the scores have taken it
-    auto next_k = [&](int32_t x, const Pages& p) {
+    auto next_k = [&](int32_t x, const Block& p) {
         if (x >= st.end) return;
-        with_policy(st.past, [&](auto past) { load_k(x, p, kf, past); });
+        with_policy(st.past, [&](auto past) {
+            if (x + kKeyBlock <= st.total && p.sound()) load_k(x, p, kf, std::false_type{}, past);
+            else load_k(x, p, kf, std::true_type{}, past);
+        });
     };
-    auto step = [&](auto masked) {
-        constexpr bool MASKED = decltype(masked)::value;
+    bool masked = false;  // (uniform) from the first block on that rows see in part, or whose pages are not all there
+    int32_t masked_from = st.end;
+    next_k(kb, now);
+    while (kb < st.end) {
+        if (!masked && (kb + kKeyBlock > st.context || !now.sound())) {
+            masked = true;
+            masked_from = kb;
+        }
         uint32_t vr[8][VW];
-        with_policy(st.past, [&](auto past) { load_v(kb, now, vr, masked, past); });
-        const Pages after = look(kb + 2 * kKeyRound);
+        with_policy(st.past, [&](auto past) {
+            if (!masked) load_v(kb, now, vr, std::false_type{}, past);
+            else load_v(kb, now, vr, std::true_type{}, past);
+        });
+        const Block after = cursor.next(a, st);
         f32x4 s[2][MT];
 #pragma unroll
         for (int t = 0; t < 2; ++t)
@@ -270,13 +350,13 @@ __device__ __forceinline__ void attend_rows(const TreeArgs& a, const Stretch& st
                 for (int c = 0; c < DC; ++c) s[t][mt] = mfma_16x16x32<DT>(kf[t][c], qf[mt][c], s[t][mt]);
             }
         next_k(kb + kKeyRound, next);
-        if constexpr (MASKED) {
+        if (masked) {
 #pragma unroll
             for (int t = 0; t < 2; ++t)
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt) {
                     const uint32_t seen =
-                        now.p[t] < 0 ? 0u : sees4(view[mt], kb + t * 16 + lg * 4 - st.context);
+                        now.page[t] < 0 ? 0u : sees4(view[mt], kb + t * 16 + lg * 4 - st.context);
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
                         if ((seen >> i & 1u) == 0) s[t][mt][i] = neg_inf();
@@ -328,11 +408,11 @@ __device__ __forceinline__ void attend_rows(const TreeArgs& a, const Stretch& st
 #pragma unroll
             for (int i = 0; i < 4; ++i) pf[mt][i] = pack2<DT>(p[2 * i], p[2 * i + 1]);
         }
-        if constexpr (MASKED) {
+        if (masked) {
             // none for keys past the last one, or without a page
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const bool there = now.p[j / 4] >= 0 && kb + (j < 4 ? 0 : 12) + lg * 4 + j < st.total;
+                const bool there = now.page[j / 4] >= 0 && kb + (j < 4 ? 0 : 12) + lg * 4 + j < st.total;
 #pragma unroll
                 for (int x = 0; x < VW; ++x) vr[j][x] = there ? vr[j][x] : 0u;
             }
@@ -345,7 +425,6 @@ __device__ __forceinline__ void attend_rows(const TreeArgs& a, const Stretch& st
                 for (int x = 0; x < VW; ++x) any |= finite_halves<DT>(vr[j][x]) != vr[j][x];
             if (__any(any)) {
                 wild = true;
-                wild_from = min(wild_from, kb);
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
 #pragma unroll
@@ -364,23 +443,18 @@ __device__ __forceinline__ void attend_rows(const TreeArgs& a, const Stretch& st
         now = next;
         next = after;
         kb += kKeyRound;
-    };
-    next_k(kb, now);
-    while (kb < st.end) {
-        while (kb + kKeyBlock <= st.context && kb < st.end && sound(now)) step(std::false_type{});
-        if (kb < st.end) step(std::true_type{});
     }
     if (wild) {
 #pragma unroll 1
-        for (kb = wild_from; kb < st.end; kb += kKeyRound) {
-            const Pages p = look(kb);
-            if (kb + kKeyBlock <= st.context && sound(p)) continue;  // (its values went into the products as they are)
+        for (kb = masked_from; kb < st.end; kb += kKeyRound)
 #pragma unroll 1
             for (int t = 0; t < 2; ++t) {
-                if (p.p[t] < 0) continue;
-                const char* base = base_of(st.v, a.v_page, a.v_pos, p, kb, t);
+                int32_t in;
+                const int32_t page = grain_page(a, st, kb / 16 + t, &in);
+                if (page < 0) continue;
+                const char* base = st.v + page * a.v_page + (int64_t)in * a.v_pos;
 #pragma unroll 1
-                for (int32_t x = 0; x <= last_of(p, kb, t); ++x) {
+                for (int32_t x = 0; x < min(16, st.total - (kb + t * 16)); ++x) {
                     // accumulator i of tile d holds column (4 lg + i) * DPL + d
                     const SV_GLOBAL uint32_t* row =
                         (const SV_GLOBAL uint32_t*)(base + (int64_t)x * a.v_pos + lg * (4 * DPL * 2));
@@ -400,7 +474,6 @@ __device__ __forceinline__ void attend_rows(const TreeArgs& a, const Stretch& st
                     }
                 }
             }
-        }
     }
 
     // ---- join the four waves: a common reference, then o summed in a fixed order
@@ -517,86 +590,84 @@ __device__ __forceinline__ void attend_tree_tiles(const TreeArgs& a, const Stret
         for (int d = 0; d < DT16; ++d) o[mt][d] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     }
 
-    struct Pages {
-        int32_t p[GR];
+    // A tile goes from memory into LDS by itself (a wave's load fills 1 KB in the order of its lanes); the i-th load of a
+    // thread has row (i * 256 + thread) / CH and that place's chunk, which the swizzle has moved.  A wave's rows lie in
+    // one grain.
+    constexpr int RPL = kAttnThreads / TA::CH;  // rows per load
+    const int32_t own_row = (int32_t)threadIdx.x / TA::CH, place = (int32_t)threadIdx.x % TA::CH;
+    const int32_t half = RPL == 32 ? wave / 2 : 0;  // (64 columns: two grains per load)
+    auto pick = [&](const int32_t (&x)[GR], int i) {
+        if constexpr (RPL == 32) return half != 0 ? x[2 * i + 1] : x[2 * i];
+        else return x[i * RPL / 16];
     };
-    auto look = [&](int32_t kb) {
-        Pages p;
+    const int32_t in_grain = RPL == 32 ? own_row - half * 16 : own_row;  // the row in its grain, of the grain's first load
+    uint32_t koff[RPL < 16 ? 2 : 1], voff[RPL < 16 ? 2 : 1];             // (256 columns: two loads per grain)
 #pragma unroll
-        for (int g = 0; g < GR; ++g) p.p[g] = kb < st.end ? grain_page(a, st, kb / 16 + g) : -1;
-        return p;
+    for (int x = 0; x < (RPL < 16 ? 2 : 1); ++x) {
+        const int32_t row = in_grain + x * RPL, ch = place ^ ((own_row + x * RPL) & TA::MASK);
+        koff[x] = (uint32_t)(row * a.k_pos + ch * 16);
+        voff[x] = (uint32_t)(row * a.v_pos + ch * 16);
+    }
+    typedef Grains<GR> Tile;
+    auto plain = [&](int32_t kb, const Tile& p) { return kb + KT <= st.context && p.sound(); };
+    auto to_lds = [&](const char* from, char* to) {
+        __builtin_amdgcn_global_load_lds((const SV_GLOBAL uint32_t*)from, (SV_LDS uint32_t*)to, 16, 0, 0);
     };
-    auto sound = [](const Pages& p) {
-        int32_t x = 0;
-#pragma unroll
-        for (int g = 0; g < GR; ++g) x |= p.p[g];
-        return x >= 0;
-    };
-    // this thread's chunks of a tile: i-th load, row (i * 256 + thread) / CH; a wave's rows lie in one grain
-    u32x4 kreg[TA::LOADS], vreg[TA::LOADS];
-    auto row_of = [&](int i) { return (i * kAttnThreads + (int32_t)threadIdx.x) / TA::CH; };
-    const uint32_t ch = (uint32_t)threadIdx.x % TA::CH;
-    auto fetch = [&](int32_t kb, const Pages& p) {
-        const bool edge = kb + KT > st.total || !sound(p);
-#pragma unroll
-        for (int i = 0; i < TA::LOADS; ++i) {
-            // (uniform over the wave)
-            const int g = (i * kAttnThreads + wave * kWave) / TA::CH / 16;
-            int32_t page = p.p[0];
-#pragma unroll
-            for (int x = 1; x < GR; ++x) page = g == x ? p.p[x] : page;
-            const int64_t at = page < 0 ? 0 : grain_in_page(a, st, kb / 16 + g) * 16;
-            int32_t row = row_of(i) - g * 16;
-            if (edge) row = min(row, page < 0 ? 0 : min(15, st.total - 1 - (kb + g * 16)));
-            const char* kp = st.k + max(page, 0) * a.k_page + at * a.k_pos;
-            const char* vp = st.v + max(page, 0) * a.v_page + at * a.v_pos;
-            kreg[i] = *(const SV_GLOBAL u32x4*)(kp + (uint32_t)(row * a.k_pos + (int32_t)ch * 16));
-            vreg[i] = *(const SV_GLOBAL u32x4*)(vp + (uint32_t)(row * a.v_pos + (int32_t)ch * 16));
-        }
-    };
-    auto plain = [&](int32_t kb, const Pages& p) { return kb + KT <= st.context && sound(p); };
-    auto keep = [&](int buf, int32_t kb, const Pages& p) {
-        char* dst = s_kv + buf * (2 * TA::TILE);
-        if (!plain(kb, p)) {
-            // No value for keys past the last one or without a page; one that is not finite counts as 0 here (times the
-            // weight 0 of a row that does not see it, it would be NaN) and reaches the rows that see it at the end.
-            bool any = false;
+    auto fetch = [&](int buf, int32_t kb, const Tile& p) {
+        char* dst = s_kv + buf * (2 * TA::TILE) + wave * (kWave * 16);
+        if (kb + KT <= st.total && p.sound()) {
 #pragma unroll
             for (int i = 0; i < TA::LOADS; ++i) {
-                const int g = (i * kAttnThreads + wave * kWave) / TA::CH / 16;
-                int32_t page = p.p[0];
-#pragma unroll
-                for (int x = 1; x < GR; ++x) page = g == x ? p.p[x] : page;
-                const bool there = page >= 0 && kb + row_of(i) < st.total;
-#pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    const uint32_t w = there ? vreg[i][x] : 0u;
-                    vreg[i][x] = finite_halves<DT>(w);
-                    any |= vreg[i][x] != w;
-                }
+                const int32_t page = pick(p.page, i);
+                const int64_t in = pick(p.in, i);
+                to_lds(st.k + page * a.k_page + in * a.k_pos + koff[RPL < 16 ? i & 1 : 0], dst + i * (kAttnThreads * 16));
+                to_lds(st.v + page * a.v_page + in * a.v_pos + voff[RPL < 16 ? i & 1 : 0],
+                       dst + TA::TILE + i * (kAttnThreads * 16));
             }
-            if (__any(any) && lane == 0) atomicMin(s_wild, kb);
+        } else {  // the last key stands in for those behind it (masked below), the pool's first for a grain without a page
+#pragma unroll
+            for (int i = 0; i < TA::LOADS; ++i) {
+                const int32_t page = pick(p.page, i), more = RPL < 16 ? i % 2 * RPL : 0;
+                const int32_t start = kb + (i * RPL / 16 + half) * 16;
+                const int64_t row = page < 0 ? 0 : pick(p.in, i) + min(in_grain + more, st.total - 1 - start);
+                const int32_t ch = (place ^ ((own_row + more) & TA::MASK)) * 16;
+                to_lds(st.k + max(page, 0) * a.k_page + row * a.k_pos + ch, dst + i * (kAttnThreads * 16));
+                to_lds(st.v + max(page, 0) * a.v_page + row * a.v_pos + ch, dst + TA::TILE + i * (kAttnThreads * 16));
+            }
         }
+    };
+    // No value for keys past the last one or without a page; one that is not finite counts as 0 here (times the weight 0
+    // of a row that does not see it, it would be NaN) and reaches the rows that see it at the end.
+    auto clear = [&](int buf, int32_t kb, const Tile& p) {
+        u32x4* v = (u32x4*)(s_kv + buf * (2 * TA::TILE) + TA::TILE) + threadIdx.x;
+        bool any = false;
 #pragma unroll
         for (int i = 0; i < TA::LOADS; ++i) {
-            const int32_t row = row_of(i);
-            const int32_t at = row * TA::ROW + (((int32_t)ch ^ (row & TA::MASK)) * 16);
-            *(u32x4*)(dst + at) = kreg[i];
-            *(u32x4*)(dst + TA::TILE + at) = vreg[i];
+            const bool there = pick(p.page, i) >= 0 && kb + i * RPL + own_row < st.total;
+            u32x4 w = v[i * kAttnThreads];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                const uint32_t y = there ? w[x] : 0u;
+                w[x] = finite_halves<DT>(y);
+                any |= w[x] != y;
+            }
+            v[i * kAttnThreads] = w;
         }
+        if (__any(any) && lane == 0) *s_wild = 1;
     };
 
     int32_t kb = st.begin;
-    Pages now = look(kb), next = look(kb + KT);
-    if (threadIdx.x == 0) *s_wild = INT32_MAX;
-    fetch(kb, now);
+    GrainCursor<GR, GR> cursor;
+    cursor.start(a, st, kb);
+    Tile now = cursor.next(a, st), next = cursor.next(a, st);
+    if (threadIdx.x == 0) *s_wild = 0;
+    fetch(0, kb, now);
     __syncthreads();
-    keep(0, kb, now);
-    __syncthreads();
+    bool masked = false;  // (uniform) from the first tile on that rows see in part, or whose pages are not all there
+    int32_t masked_from = st.end;
     int buf = 0;
     bool far = false;  // (uniform over the wave) a reference lies beyond kFarReference
-    auto use = [&](auto masked) {
-        constexpr bool MASKED = decltype(masked)::value;
+    auto use = [&]() {
         const char* s_k = s_kv + buf * (2 * TA::TILE);
         const char* s_v = s_k + TA::TILE;
         // The fragments that a group of products needs are read while the group before it runs (the barriers keep the
@@ -633,10 +704,10 @@ __device__ __forceinline__ void attend_tree_tiles(const TreeArgs& a, const Stret
             for (int c = 0; c < DC; ++c)
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt) s[u][t][mt] = mfma_16x16x32<DT>(kf[i & 1][c], qf[mt][c], s[u][t][mt]);
-            if constexpr (MASKED) {
+            if (masked) {
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt) {
-                    const uint32_t seen = now.p[i] < 0 ? 0u : sees4(view[mt], kb + i * 16 + lg * 4 - st.context);
+                    const uint32_t seen = now.page[i] < 0 ? 0u : sees4(view[mt], kb + i * 16 + lg * 4 - st.context);
 #pragma unroll
                     for (int x = 0; x < 4; ++x)
                         if ((seen >> x & 1u) == 0) s[u][t][mt][x] = neg_inf();
@@ -701,50 +772,46 @@ __device__ __forceinline__ void attend_tree_tiles(const TreeArgs& a, const Stret
         }
     };
     while (kb < st.end) {
-        const bool more = kb + KT < st.end;
-        if (more) fetch(kb + KT, next);
-        const Pages after = look(kb + 2 * KT);
-        if (!idle) {
-            if (plain(kb, now)) use(std::false_type{});
-            else use(std::true_type{});
+        if (kb + KT < st.end) fetch(buf ^ 1, kb + KT, next);
+        const Tile after = cursor.next(a, st);
+        if (!masked && !plain(kb, now)) {
+            masked = true;
+            masked_from = kb;
         }
-        if (more) keep(buf ^ 1, kb + KT, next);
-        __syncthreads();
+        if (masked) {
+            clear(buf, kb, now);
+            __syncthreads();
+        }
+        if (!idle) use();
+        __syncthreads();  // (and the next tile has arrived)
         now = next;
         next = after;
         kb += KT;
         buf ^= 1;
     }
-    const int32_t wild_from = *s_wild;  // (before the last barrier)
+    const bool wild = *s_wild != 0;  // (written before the last barrier)
     if (idle) return;
-    if (wild_from != INT32_MAX) {
+    if (wild) {
 #pragma unroll 1
-        for (kb = wild_from; kb < st.end; kb += KT) {
-            const Pages p = look(kb);
-            if (plain(kb, p)) continue;  // (its values went into the products as they are)
-#pragma unroll 1
-            for (int32_t x = 0; x < min(KT, st.total - kb); ++x) {
-                int32_t page = p.p[0];
+        for (int32_t x = masked_from; x < st.end; ++x) {
+            int32_t in;
+            const int32_t page = grain_page(a, st, x / 16, &in);
+            if (page < 0) continue;
+            const char* row = st.v + page * a.v_page + (int64_t)(in + x % 16) * a.v_pos;
+            bool see[MT];
 #pragma unroll
-                for (int g = 1; g < GR; ++g) page = x / 16 == g ? p.p[g] : page;
-                if (page < 0) continue;
-                const char* row = st.v + page * a.v_page +
-                                  (int64_t)(grain_in_page(a, st, kb / 16 + x / 16) * 16 + x % 16) * a.v_pos;
-                bool see[MT];
+            for (int mt = 0; mt < MT; ++mt) see[mt] = sees(view[mt], x - st.context);
+            // accumulator i of tile d holds column d * 16 + lg * 4 + i
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt) see[mt] = sees(view[mt], kb + x - st.context);
-                // accumulator i of tile d holds column d * 16 + lg * 4 + i
+            for (int d = 0; d < DT16; ++d) {
+                const u32x2 w = *(const SV_GLOBAL u32x2*)(row + (d * 16 + lg * 4) * 2);
 #pragma unroll
-                for (int d = 0; d < DT16; ++d) {
-                    const u32x2 w = *(const SV_GLOBAL u32x2*)(row + (d * 16 + lg * 4) * 2);
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t bad = w[i / 2] ^ finite_halves<DT>(w[i / 2]);
+                    const float v = i % 2 ? hi16<DT>(bad) : lo16<DT>(bad);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const uint32_t bad = w[i / 2] ^ finite_halves<DT>(w[i / 2]);
-                        const float v = i % 2 ? hi16<DT>(bad) : lo16<DT>(bad);
-#pragma unroll
-                        for (int mt = 0; mt < MT; ++mt)
-                            if (see[mt]) o[mt][d][i] += v;
-                    }
+                    for (int mt = 0; mt < MT; ++mt)
+                        if (see[mt]) o[mt][d][i] += v;
                 }
             }
         }
@@ -875,6 +942,7 @@ __global__ __launch_bounds__(kAttnThreads, D == 256 ? 1 : 2) void tree_part_kern
         st.context = len - st.nrows;
         st.begin = j * KB;
         st.end = min((j + take) * KB, len);
+        st.pages = a.table != nullptr ? page_of_grain(a, (len - 1) / 16) + 1 : 1;
         st.k = a.k + (int64_t)hk * a.k_head;
         st.v = a.v + (int64_t)hk * a.v_head;
         st.table = a.table != nullptr ? a.table + (int64_t)b * a.table_stride : nullptr;

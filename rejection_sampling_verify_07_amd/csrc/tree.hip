@@ -255,10 +255,10 @@ sv_status_t tree_attention_common(const sv_tree_shape_t* sh, const void* q, cons
     a.capacity = p.capacity;
     // g / grains as (g * mul) >> shift, exact for g < 2^31: mul = ceil(2^shift / grains) exceeds 2^shift / grains by less
     // than 1, and 2^shift >= 2^31 * grains
-    a.grains = (uint32_t)std::max(sh->page_size / 16, 1);
+    a.grains = sh->page_table != nullptr ? sh->page_size / 16 : kMaxPositions / 16 + 64;
     a.grains_shift = 31;
-    while ((1ull << (a.grains_shift - 31)) < a.grains) ++a.grains_shift;
-    a.grains_mul = (uint32_t)(((1ull << a.grains_shift) + a.grains - 1) / a.grains);
+    while ((1ull << (a.grains_shift - 31)) < (uint64_t)a.grains) ++a.grains_shift;
+    a.grains_mul = (uint32_t)(((1ull << a.grains_shift) + (uint64_t)a.grains - 1) / (uint64_t)a.grains);
     a.q_heads = sh->q_heads;
     a.kv_heads = sh->kv_heads;
     a.rep = sh->q_heads / sh->kv_heads;
