@@ -15,7 +15,7 @@
 // grow with the caches, and sequences of any mix of lengths keep all CUs busy.
 //
 // Positions come in grains of 16, which never cross a page: a wave finds a
-// grain's page in a window of the table that its lanes hold (PageWindow).
+// grain's page with scalar loads, a step before the keys' own loads.
 //   Few rows per key head (up to 16 or 32): each wave walks its own 32 keys of a
 // round with all rows, K and V straight from memory to registers (attend_rows).
 //   More: the four waves share the rows and take tiles of 64 keys through LDS
@@ -92,35 +92,6 @@ __device__ __forceinline__ int32_t grain_page(const TreeArgs& a, const Stretch& 
     return (uint32_t)page < (uint32_t)a.pages ? page : -1;
 }
 
-// The pages that a wave walks through, in rising order: lane i of `held` has page number at + i of the sequence, and
-// `ahead` those from at + 32 on, loaded long before they are needed.  A page is then one v_readlane away.
-struct PageWindow {
-    int32_t at, held, ahead;
-
-    __device__ __forceinline__ int32_t load(const TreeArgs& a, const Stretch& s, int32_t from) const
-    {
-        const int32_t i = from + lane_id();
-        int32_t page = -1;
-        if (i < s.pages) page = s.table != nullptr ? ((const SV_GLOBAL int32_t*)s.table)[i] : s.b;
-        return (uint32_t)page < (uint32_t)a.pages ? page : -1;
-    }
-    __device__ __forceinline__ void start(const TreeArgs& a, const Stretch& s, int32_t i)
-    {
-        at = i;
-        held = load(a, s, i);
-        ahead = load(a, s, i + 32);
-    }
-    // Pages i .. i + 32 can be had; i rises by less than 32 from call to call.
-    __device__ __forceinline__ void reach(const TreeArgs& a, const Stretch& s, int32_t i)
-    {
-        if (i - at < 32) return;
-        at += 32;
-        held = ahead;
-        ahead = load(a, s, at + 32);
-    }
-    __device__ __forceinline__ int32_t page(int32_t i) const { return __builtin_amdgcn_readlane(held, i - at); }
-};
-
 // Where N neighbouring grains lie: page (-1: none) and position in it.
 template <int N>
 struct Grains {
@@ -134,29 +105,27 @@ struct Grains {
     }
 };
 
-// Walks grains g, g + STEP, ...: N neighbours each time.
+// A scalar load: the tables are not written while a kernel reads them.  (A vector load that a loop carries along keeps
+// the compiler from letting the tiles' loads run ahead: it waits for all of them.)
+__device__ __forceinline__ int32_t scalar_load(const int32_t* p)
+{
+    return *(const __attribute__((address_space(4))) int32_t*)p;
+}
+
+// Walks grains g, g + STEP, ...: N neighbours each time.  Their pages are asked for one step before they are needed.
 template <int N, int STEP>
 struct GrainCursor {
-    PageWindow window;
     int32_t number, rest;  // the next grain's page number, and its place in that page
     int32_t key;           // its first key
+    Grains<N> asked;       // those of `key`, as the table says
 
-    __device__ __forceinline__ void start(const TreeArgs& a, const Stretch& s, int32_t first_key)
+    __device__ __forceinline__ void ask(const TreeArgs& a, const Stretch& s)
     {
-        key = first_key;
-        number = page_of_grain(a, key / 16);
-        rest = key / 16 - number * a.grains;
-        window.start(a, s, number);
-    }
-    __device__ __forceinline__ Grains<N> next(const TreeArgs& a, const Stretch& s)
-    {
-        Grains<N> w;
-        window.reach(a, s, number);
         int32_t n = number, r = rest;
 #pragma unroll
         for (int g = 0; g < N; ++g) {
-            w.page[g] = key + g * 16 < s.total ? window.page(n) : -1;
-            w.in[g] = r * 16;
+            asked.page[g] = s.table != nullptr ? scalar_load(s.table + min(n, s.pages - 1)) : s.b;
+            asked.in[g] = r * 16;
             const bool over = ++r == a.grains;
             n += over ? 1 : 0;
             r = over ? 0 : r;
@@ -169,8 +138,69 @@ struct GrainCursor {
             number += q;
             rest += STEP - q * a.grains;
         }
+    }
+    __device__ __forceinline__ void start(const TreeArgs& a, const Stretch& s, int32_t first_key)
+    {
+        key = first_key;
+        number = page_of_grain(a, key / 16);
+        rest = key / 16 - number * a.grains;
+        ask(a, s);
+    }
+    __device__ __forceinline__ Grains<N> next(const TreeArgs& a, const Stretch& s)
+    {
+        Grains<N> w = asked;
+#pragma unroll
+        for (int g = 0; g < N; ++g)
+            if (key + g * 16 >= s.total || (uint32_t)w.page[g] >= (uint32_t)a.pages) w.page[g] = -1;
         key += STEP * 16;
+        ask(a, s);
         return w;
+    }
+};
+
+// Walks all grains of a stretch in order: where the next one's keys and values lie.  Within a page a step is an
+// addition per pointer; the next page's number is asked for a page ahead.  (Scalar work: it runs beside the products in
+// every wave, and with each grain's place worked out anew it was half of the instructions.)
+struct KeyWalk {
+    const char *k, *v;
+    int32_t left;    // grains of the page from here on
+    int32_t page;    // -1: none (the pointers then lie in the pool's first page)
+    int32_t number;  // of the page after this one
+    int32_t asked;   // that page, as the table says
+
+    __device__ __forceinline__ void ask(const Stretch& s)
+    {
+        if (s.table != nullptr) asked = scalar_load(s.table + min(number, s.pages - 1));
+    }
+    __device__ __forceinline__ void open(const TreeArgs& a, const Stretch& s)
+    {
+        page = (uint32_t)asked < (uint32_t)a.pages ? asked : -1;
+        const int64_t at = max(page, 0);
+        k = s.k + at * a.k_page;
+        v = s.v + at * a.v_page;
+        left = a.grains;
+        ++number;
+        ask(s);
+    }
+    __device__ __forceinline__ void start(const TreeArgs& a, const Stretch& s, int32_t key)
+    {
+        number = page_of_grain(a, key / 16);
+        const int32_t in = key / 16 - number * a.grains;
+        asked = s.b;
+        ask(s);
+        open(a, s);
+        k += (int64_t)in * 16 * a.k_pos;
+        v += (int64_t)in * 16 * a.v_pos;
+        left -= in;
+    }
+    __device__ __forceinline__ void step(const TreeArgs& a, const Stretch& s)
+    {
+        if (--left > 0) {
+            k += 16 * a.k_pos;
+            v += 16 * a.v_pos;
+        } else {
+            open(a, s);
+        }
     }
 };
 
@@ -212,6 +242,13 @@ template <int D, int MT>
 constexpr size_t tree_rows_lds()
 {
     return attn_lds_floats(D, MT) * 4;
+}
+
+// All loads of this wave have arrived, in a form that the compiler counts: before a loop, so that it does not wait in
+// every step for what the first one needs.
+__device__ __forceinline__ void loads_done()
+{
+    __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
 }
 
 // Where a finished or partial result of a workgroup goes.
@@ -317,7 +354,7 @@ __device__ __forceinline__ void attend_rows(const TreeArgs& a, const Stretch& st
     int32_t kb = st.begin + wave * kKeyBlock;
     GrainCursor<2, kKeyRound / 16> cursor;
     cursor.start(a, st, kb);
-    Block now = cursor.next(a, st), next = cursor.next(a, st);
+    Block now = cursor.next(a, st);
     u32x4 kf[2][DC];  // the block at hand; the next one's is loaded once the scores have taken it
     auto next_k = [&](int32_t x, const Block& p) {
         if (x >= st.end) return;
@@ -329,6 +366,7 @@ __device__ __forceinline__ void attend_rows(const TreeArgs& a, const Stretch& st
     bool masked = false;  // (uniform) from the first block on that rows see in part, or whose pages are not all there
     int32_t masked_from = st.end;
     next_k(kb, now);
+    loads_done();
     while (kb < st.end) {
         if (!masked && (kb + kKeyBlock > st.context || !now.sound())) {
             masked = true;
@@ -339,7 +377,6 @@ __device__ __forceinline__ void attend_rows(const TreeArgs& a, const Stretch& st
             if (!masked) load_v(kb, now, vr, std::false_type{}, past);
             else load_v(kb, now, vr, std::true_type{}, past);
         });
-        const Block after = cursor.next(a, st);
         f32x4 s[2][MT];
 #pragma unroll
         for (int t = 0; t < 2; ++t)
@@ -349,6 +386,7 @@ __device__ __forceinline__ void attend_rows(const TreeArgs& a, const Stretch& st
 #pragma unroll
                 for (int c = 0; c < DC; ++c) s[t][mt] = mfma_16x16x32<DT>(kf[t][c], qf[mt][c], s[t][mt]);
             }
+        const Block next = cursor.next(a, st);
         next_k(kb + kKeyRound, next);
         if (masked) {
 #pragma unroll
@@ -441,7 +479,6 @@ __device__ __forceinline__ void attend_rows(const TreeArgs& a, const Stretch& st
             for (int mt = 0; mt < MT; ++mt) o[mt][d] = mfma_16x16x32<DT>(vf, pf[mt], o[mt][d]);
         }
         now = next;
-        next = after;
         kb += kKeyRound;
     }
     if (wild) {
@@ -553,33 +590,54 @@ __device__ __forceinline__ void attend_rows(const TreeArgs& a, const Stretch& st
     }
 }
 
-// ---- many rows per key head: four waves of MT * 16 rows share tiles of 64 keys through LDS, laid out and read as in
-// TileAttention.
+// ---- many rows per key head: four waves of MT * 16 rows share tiles of keys through LDS, whose rows lie and are read
+// as in TileAttention.  Four tiles of 16 KB (64 columns: of 64 keys; 128: of 32) are on their way or in use: with two
+// of them a step lasted as long as a read of memory.
+template <int D>
+struct TreeTile {
+    static constexpr int KT = D == 64 ? 64 : 32;           // keys
+    static constexpr int BUFS = 4;
+    static constexpr int ROW = D * 2;                      // bytes per key row
+    static constexpr int CH = ROW / 16;                    // 16-byte chunks per row
+    static constexpr int MASK = CH < 16 ? CH - 1 : 15;     // swizzle
+    static constexpr int TILE = KT * ROW;                  // bytes of K (or V)
+    static constexpr int LOADS = TILE / 16 / kAttnThreads;  // per thread, of K (or V)
+    static constexpr int LDS = BUFS * 2 * TILE;
+};
+
+__device__ __forceinline__ uint32_t lds_address(const char* p) { return (uint32_t)(uintptr_t)(const SV_LDS char*)p; }
+
+// 16 bytes from each lane's place `off` behind `base` into LDS, lane i's at `to` + 16 i (`to`: the wave's).  In assembly, which the compiler
+// does not count among the loads in flight: it would wait for all of them before every transposed read of a tile.
+// arrived() is the wait for them; a wave has none left when its loop over the tiles ends.
+__device__ __forceinline__ void load_to_lds(const char* base, uint32_t off, uint32_t to)
+{
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(to), "v"(off),
+                 "s"((const SV_GLOBAL char*)base)
+                 : "memory", "m0");
+}
+
+// All but the newest N of this wave's loads have arrived, and what it read of LDS; then all waves have come here.
+template <int N>
+__device__ __forceinline__ void arrived()
+{
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+}
+
 template <int DT, int D, int MT>
 __device__ __forceinline__ void attend_tree_tiles(const TreeArgs& a, const Stretch& st, int32_t tile, const TreeOut& to,
                                                   const uint32_t* s_view, int32_t* s_wild, char* s_kv)
 {
-    typedef TileAttention<DT, D, MT> TA;
-    constexpr int DC = TA::DC, DT16 = TA::DT16, KT = TA::KT, SUBS = KT / kKeyBlock, GR = KT / 16;
-    static_assert(kWave % TA::CH == 0 || TA::CH % kWave == 0, "a wave's load stays within a grain");
+    typedef TreeTile<D> TA;
+    constexpr int ROWS = kAttnWaves * MT * 16;
+    constexpr int DC = D / 32, DT16 = D / 16, KT = TA::KT, SUBS = KT / kKeyBlock, GR = KT / 16;
+    static_assert(kWave % TA::CH == 0, "a wave's load stays within a grain");
     const int lane = lane_id(), l16 = lane & 15, lg = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(wave_id());
     const int32_t m_total = st.nrows * a.rep;
-    const int32_t r0 = tile * TA::ROWS + wave * (MT * 16), t0 = tile * TA::ROWS / a.rep;
+    const int32_t r0 = tile * ROWS + wave * (MT * 16), t0 = tile * ROWS / a.rep;
     const bool idle = r0 >= m_total;  // no rows: the wave only moves tiles
 
-    u32x4 qf[MT][DC];
-    const uint32_t* view[MT];
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-        const int32_t r = r0 + mt * 16 + l16;
-        const int32_t t = r / a.rep, h = st.hk * a.rep + (r - t * a.rep);
-        const char* qp = a.q + (int64_t)(st.row0 + t) * a.q_row + (int64_t)h * a.q_head + lg * 16;
-#pragma unroll
-        for (int c = 0; c < DC; ++c)
-            qf[mt][c] = r < m_total ? *(const SV_GLOBAL u32x4*)(qp + c * 64) : u32x4{0u, 0u, 0u, 0u};
-        view[mt] = s_view + (r < m_total ? t - t0 : 0) * kTreeWords;
-    }
     f32x4 o[MT][DT16];
     float m[MT], l[MT];
 #pragma unroll
@@ -595,55 +653,61 @@ __device__ __forceinline__ void attend_tree_tiles(const TreeArgs& a, const Stret
     // one grain.
     constexpr int RPL = kAttnThreads / TA::CH;  // rows per load
     const int32_t own_row = (int32_t)threadIdx.x / TA::CH, place = (int32_t)threadIdx.x % TA::CH;
-    const int32_t half = RPL == 32 ? wave / 2 : 0;  // (64 columns: two grains per load)
-    auto pick = [&](const int32_t (&x)[GR], int i) {
-        if constexpr (RPL == 32) return half != 0 ? x[2 * i + 1] : x[2 * i];
-        else return x[i * RPL / 16];
-    };
+    const int32_t half = RPL == 32 ? wave / 2 : 0;                       // (64 columns: two grains per load)
     const int32_t in_grain = RPL == 32 ? own_row - half * 16 : own_row;  // the row in its grain, of the grain's first load
-    uint32_t koff[RPL < 16 ? 2 : 1], voff[RPL < 16 ? 2 : 1];             // (256 columns: two loads per grain)
+    constexpr int PER = RPL < 16 ? 16 / RPL : 1;                         // (256 columns: two loads per grain)
+    uint32_t koff[PER], voff[PER];
 #pragma unroll
-    for (int x = 0; x < (RPL < 16 ? 2 : 1); ++x) {
+    for (int x = 0; x < PER; ++x) {
         const int32_t row = in_grain + x * RPL, ch = place ^ ((own_row + x * RPL) & TA::MASK);
         koff[x] = (uint32_t)(row * a.k_pos + ch * 16);
         voff[x] = (uint32_t)(row * a.v_pos + ch * 16);
     }
-    typedef Grains<GR> Tile;
-    auto plain = [&](int32_t kb, const Tile& p) { return kb + KT <= st.context && p.sound(); };
-    auto to_lds = [&](const char* from, char* to) {
-        __builtin_amdgcn_global_load_lds((const SV_GLOBAL uint32_t*)from, (SV_LDS uint32_t*)to, 16, 0, 0);
-    };
-    auto fetch = [&](int buf, int32_t kb, const Tile& p) {
-        char* dst = s_kv + buf * (2 * TA::TILE) + wave * (kWave * 16);
-        if (kb + KT <= st.total && p.sound()) {
+    KeyWalk walk;
+    int32_t kb = st.begin, ahead = st.begin;  // the tile in use, the next one to load
+    int32_t bad_from = INT32_MAX;             // the first tile met that has a grain without a page
+    walk.start(a, st, kb);
+    auto load_next = [&](int buf) {
+        if (ahead >= st.end) return;
+        const uint32_t dst = lds_address(s_kv) + (uint32_t)(buf * (2 * TA::TILE) + wave * (kWave * 16));
+        const bool edge = ahead + KT > st.total;
+        int32_t pages = 0;
 #pragma unroll
-            for (int i = 0; i < TA::LOADS; ++i) {
-                const int32_t page = pick(p.page, i);
-                const int64_t in = pick(p.in, i);
-                to_lds(st.k + page * a.k_page + in * a.k_pos + koff[RPL < 16 ? i & 1 : 0], dst + i * (kAttnThreads * 16));
-                to_lds(st.v + page * a.v_page + in * a.v_pos + voff[RPL < 16 ? i & 1 : 0],
-                       dst + TA::TILE + i * (kAttnThreads * 16));
+        for (int i = 0; i < TA::LOADS; ++i) {
+            // this load's grain: pointers before and after a step where it has two
+            const char *k = walk.k, *v = walk.v;
+            pages |= walk.page;
+            if constexpr (RPL == 32) {
+                walk.step(a, st);
+                pages |= walk.page;
+                k = half != 0 ? walk.k : k;
+                v = half != 0 ? walk.v : v;
             }
-        } else {  // the last key stands in for those behind it (masked below), the pool's first for a grain without a page
-#pragma unroll
-            for (int i = 0; i < TA::LOADS; ++i) {
-                const int32_t page = pick(p.page, i), more = RPL < 16 ? i % 2 * RPL : 0;
-                const int32_t start = kb + (i * RPL / 16 + half) * 16;
-                const int64_t row = page < 0 ? 0 : pick(p.in, i) + min(in_grain + more, st.total - 1 - start);
-                const int32_t ch = (place ^ ((own_row + more) & TA::MASK)) * 16;
-                to_lds(st.k + max(page, 0) * a.k_page + row * a.k_pos + ch, dst + i * (kAttnThreads * 16));
-                to_lds(st.v + max(page, 0) * a.v_page + row * a.v_pos + ch, dst + TA::TILE + i * (kAttnThreads * 16));
+            const int x = i % PER;
+            uint32_t ko = koff[x], vo = voff[x];
+            if (edge) {  // the last key stands in for those behind it, the pool's first where a grain has none (masked below)
+                const int32_t first = ahead + (i / PER * (RPL == 32 ? 2 : 1) + half) * 16, last = st.total - 1 - first;
+                const int32_t row = max(min(in_grain + x * RPL, last), 0), ch = place ^ ((own_row + x * RPL) & TA::MASK);
+                ko = (uint32_t)(row * a.k_pos + ch * 16);
+                vo = (uint32_t)(row * a.v_pos + ch * 16);
+                k = last < 0 ? st.k : k;
+                v = last < 0 ? st.v : v;
             }
+            load_to_lds(k, ko, dst + i * (kAttnThreads * 16));
+            load_to_lds(v, vo, dst + TA::TILE + i * (kAttnThreads * 16));
+            if (x == PER - 1) walk.step(a, st);
         }
+        if (pages < 0) bad_from = min(bad_from, ahead);
+        ahead += KT;
     };
     // No value for keys past the last one or without a page; one that is not finite counts as 0 here (times the weight 0
     // of a row that does not see it, it would be NaN) and reaches the rows that see it at the end.
-    auto clear = [&](int buf, int32_t kb, const Tile& p) {
+    auto clear = [&](int buf, int32_t kb, uint32_t pages) {
         u32x4* v = (u32x4*)(s_kv + buf * (2 * TA::TILE) + TA::TILE) + threadIdx.x;
         bool any = false;
 #pragma unroll
         for (int i = 0; i < TA::LOADS; ++i) {
-            const bool there = pick(p.page, i) >= 0 && kb + i * RPL + own_row < st.total;
+            const bool there = (pages >> (i * RPL / 16 + half) & 1u) != 0 && kb + i * RPL + own_row < st.total;
             u32x4 w = v[i * kAttnThreads];
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
@@ -656,63 +720,79 @@ __device__ __forceinline__ void attend_tree_tiles(const TreeArgs& a, const Stret
         if (__any(any) && lane == 0) *s_wild = 1;
     };
 
-    int32_t kb = st.begin;
-    GrainCursor<GR, GR> cursor;
-    cursor.start(a, st, kb);
-    Tile now = cursor.next(a, st), next = cursor.next(a, st);
     if (threadIdx.x == 0) *s_wild = 0;
-    fetch(0, kb, now);
-    __syncthreads();
+#pragma unroll
+    for (int x = 0; x + 1 < TA::BUFS; ++x) load_next(x);
+    u32x4 qf[MT][DC];
+    const uint32_t* view[MT];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+        const int32_t r = r0 + mt * 16 + l16;
+        const int32_t t = r / a.rep, h = st.hk * a.rep + (r - t * a.rep);
+        const char* qp = a.q + (int64_t)(st.row0 + t) * a.q_row + (int64_t)h * a.q_head + lg * 16;
+#pragma unroll
+        for (int c = 0; c < DC; ++c)
+            qf[mt][c] = r < m_total ? *(const SV_GLOBAL u32x4*)(qp + c * 64) : u32x4{0u, 0u, 0u, 0u};
+        view[mt] = s_view + (r < m_total ? t - t0 : 0) * kTreeWords;
+    }
+    loads_done();
+    int buf = 0;
+    uint32_t here = 0;    // a masked tile: which grains have pages
     bool masked = false;  // (uniform) from the first tile on that rows see in part, or whose pages are not all there
     int32_t masked_from = st.end;
-    int buf = 0;
     bool far = false;  // (uniform over the wave) a reference lies beyond kFarReference
-    auto use = [&]() {
-        const char* s_k = s_kv + buf * (2 * TA::TILE);
-        const char* s_v = s_k + TA::TILE;
-        // The fragments that a group of products needs are read while the group before it runs (the barriers keep the
-        // scheduler from moving a read down to its use, which exposed the LDS latency once per product).
-        auto k_rows = [&](int i, u32x4 (&kf)[DC]) {  // 16 keys
-            const int32_t row = i * 16 + l16;
+    // A lane's places in a tile: row l16 (+ 16 per group) of K, its chunk c * 4 + lg behind the swizzle; for the values of
+    // 32 keys, four rows (lg * 4 + l16 / 4) and 8 bytes of columns per lane before the exchange.  Another chunk or
+    // column is an exclusive or away.
+    const uint32_t kplace = (uint32_t)(l16 * TA::ROW + ((lg ^ (l16 & TA::MASK)) * 16));
+    const int32_t vrow = lg * 4 + (l16 >> 2);
+    const uint32_t vplace =
+        (uint32_t)(TA::TILE + vrow * TA::ROW + ((((l16 & 3) >> 1) ^ (vrow & TA::MASK)) * 16) + (l16 & 1) * 8);
+    u32x4 kf[2 * SUBS][DC];  // the keys of the tile that is next in use: read while the one before it is
+    auto read_keys = [&](int buf) {
+        const uint32_t at = (uint32_t)(buf * (2 * TA::TILE)) + kplace;
 #pragma unroll
-            for (int c = 0; c < DC; ++c)
-                kf[c] = *(const u32x4*)(s_k + row * TA::ROW + (((c * 4 + lg) ^ (l16 & TA::MASK)) * 16));
-        };
-        auto v_columns = [&](int u, u32x4 (&vf)[DT16]) {  // 32 keys: four (lg * 4 + l16 / 4) and 8 bytes of columns per
-                                                          // lane before the exchange
-            const int32_t vrow = u * kKeyBlock + lg * 4 + (l16 >> 2);
+        for (int c = 0; c < DC; ++c)
+#pragma unroll
+            for (int i = 0; i < 2 * SUBS; ++i)
+                kf[i][c] = *(const u32x4*)(s_kv + (at ^ (uint32_t)(c * 64)) + i * 16 * TA::ROW);
+    };
+    auto use = [&](bool more) {
+        u32x4 vf[DT16];
+        auto read_values = [&](int u) {
+            const uint32_t at = (uint32_t)(buf * (2 * TA::TILE)) + vplace;
 #pragma unroll
             for (int d = 0; d < DT16; ++d) {
-                const int32_t at =
-                    vrow * TA::ROW + (((d * 2 + ((l16 & 3) >> 1)) ^ (vrow & TA::MASK)) * 16) + (l16 & 1) * 8;
-                const u32x2 v0 = lds_read_transposed(s_v + at), v1 = lds_read_transposed(s_v + at + 16 * TA::ROW);
+                const char* p = s_kv + (at ^ (uint32_t)(d * 32)) + u * kKeyBlock * TA::ROW;
+                const u32x2 v0 = lds_read_transposed(p), v1 = lds_read_transposed(p + 16 * TA::ROW);
                 vf[d] = u32x4{v0.x, v0.y, v1.x, v1.y};
             }
         };
         f32x4 s[SUBS][2][MT];
-        u32x4 kf[2][DC], vf[DT16];
-        k_rows(0, kf[0]);
+        read_values(0);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int i = 0; i < 2 * SUBS; ++i) {
-            const int u = i / 2, t = i & 1;
-            if (i + 1 < 2 * SUBS) k_rows(i + 1, kf[(i + 1) & 1]);
-            else v_columns(0, vf);
-            __builtin_amdgcn_sched_barrier(0);
+        for (int i = 0; i < 2 * SUBS; ++i)
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) s[u][t][mt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            for (int mt = 0; mt < MT; ++mt) s[i / 2][i & 1][mt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-            for (int c = 0; c < DC; ++c)
+        for (int c = 0; c < DC; ++c)
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt) s[u][t][mt] = mfma_16x16x32<DT>(kf[i & 1][c], qf[mt][c], s[u][t][mt]);
-            if (masked) {
+            for (int i = 0; i < 2 * SUBS; ++i)
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+                    s[i / 2][i & 1][mt] = mfma_16x16x32<DT>(kf[i][c], qf[mt][c], s[i / 2][i & 1][mt]);
+        if (more) read_keys((buf + 1) % TA::BUFS);
+        if (masked) {
+#pragma unroll
+            for (int i = 0; i < 2 * SUBS; ++i)
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt) {
-                    const uint32_t seen = now.page[i] < 0 ? 0u : sees4(view[mt], kb + i * 16 + lg * 4 - st.context);
+                    const uint32_t seen = (here >> i & 1u) == 0 ? 0u : sees4(view[mt], kb + i * 16 + lg * 4 - st.context);
 #pragma unroll
                     for (int x = 0; x < 4; ++x)
-                        if ((seen >> x & 1u) == 0) s[u][t][mt][x] = neg_inf();
+                        if ((seen >> x & 1u) == 0) s[i / 2][i & 1][mt][x] = neg_inf();
                 }
-            }
         }
         float top[MT];
         bool over = false;
@@ -768,28 +848,34 @@ __device__ __forceinline__ void attend_tree_tiles(const TreeArgs& a, const Stret
             for (int d = 0; d < DT16; ++d)
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt) o[mt][d] = mfma_16x16x32<DT>(vf[d], pf[mt], o[mt][d]);
-            if (u + 1 < SUBS) v_columns(u + 1, vf);
+            if (u + 1 < SUBS) read_values(u + 1);
         }
     };
+    arrived<0>();  // (the other waves' loads too)
+    if (!idle) read_keys(0);
     while (kb < st.end) {
-        if (kb + KT < st.end) fetch(buf ^ 1, kb + KT, next);
-        const Tile after = cursor.next(a, st);
-        if (!masked && !plain(kb, now)) {
+        // the tile after this one has arrived (the one behind it need not have), and all waves have left the one before
+        // this, whose place the next load takes
+        if (kb + 2 * KT < st.end) arrived<2 * TA::LOADS>();
+        else arrived<0>();
+        load_next((buf + TA::BUFS - 1) % TA::BUFS);
+        if (!masked && (kb + KT > st.context || kb >= bad_from)) {
             masked = true;
             masked_from = kb;
         }
         if (masked) {
-            clear(buf, kb, now);
+            here = 0;
+            int32_t in;
+#pragma unroll
+            for (int g = 0; g < GR; ++g) here |= grain_page(a, st, kb / 16 + g, &in) >= 0 ? 1u << g : 0u;
+            clear(buf, kb, here);
             __syncthreads();
         }
-        if (!idle) use();
-        __syncthreads();  // (and the next tile has arrived)
-        now = next;
-        next = after;
+        if (!idle) use(kb + KT < st.end);
         kb += KT;
-        buf ^= 1;
+        buf = (buf + 1) % TA::BUFS;
     }
-    const bool wild = *s_wild != 0;  // (written before the last barrier)
+    const bool wild = *s_wild != 0;  // (written before a barrier that all waves have passed)
     if (idle) return;
     if (wild) {
 #pragma unroll 1
@@ -833,7 +919,7 @@ __device__ __forceinline__ void attend_tree_tiles(const TreeArgs& a, const Stret
                 a.lse[(int64_t)(st.row0 + t) * a.q_heads + h] =
                     l[mt] != 0.0f ? (m[mt] + __builtin_amdgcn_logf(l[mt])) * 0.69314718055994531f : neg_inf();
         } else {
-            const int64_t at = to.slot * TA::ROWS + wave * (MT * 16) + mt * 16 + l16;
+            const int64_t at = to.slot * ROWS + wave * (MT * 16) + mt * 16 + l16;
             if (lg == 0) a.ml[at] = float2{m[mt], l[mt]};
             SV_GLOBAL f32x4* dst = (SV_GLOBAL f32x4*)(a.acc + at * D + lg * 4);
 #pragma unroll
@@ -903,12 +989,12 @@ constexpr double kTreePastCaches = 128e6;  // bytes of keys and values from whic
 template <int DT, int D, bool TILES, int MT>
 __global__ __launch_bounds__(kAttnThreads, D == 256 ? 1 : 2) void tree_part_kernel(TreeArgs a)
 {
-    constexpr int ROWS = TILES ? TileAttention<DT, D, MT>::ROWS : MT * 16;
+    constexpr int ROWS = MT * 16 * (TILES ? kAttnWaves : 1);
     constexpr int KB = kTreeRound<TILES>;
-    constexpr size_t kLds = TILES ? (size_t)TileAttention<DT, D, MT>::LDS : tree_rows_lds<D, MT>();
+    constexpr size_t kLds = TILES ? (size_t)TreeTile<D>::LDS : tree_rows_lds<D, MT>();
     // The stretches count on two workgroups per CU: more than a third of the 160 KB keeps a third one out.
-    constexpr size_t kLdsOfTwo = 52 * 1024;
-    __shared__ __align__(16) char s_mem[D != 256 && kLds < kLdsOfTwo ? kLdsOfTwo : kLds];
+    constexpr size_t kLdsOfTwo = 52 * 1024, kMem = D != 256 && kLds < kLdsOfTwo ? kLdsOfTwo : kLds;
+    __shared__ __align__(16) char s_mem[kMem];
     __shared__ uint32_t s_view[ROWS * kTreeWords];
     __shared__ int32_t s_up[kTreeMostGuesses], s_sum[kAttnWaves], s_found[2], s_wild;
     // the row tiles of one stretch (the same keys) run on one XCD (workgroups go to the 8 XCDs in turn)
