@@ -114,8 +114,8 @@ sv_status_t cache_compact_common(const sv_compact_shape_t* sh, void* data, const
     return launch_status();
 }
 
-// Counts that one workgroup forms: up to this many table entries and pages.
-constexpr int64_t kForkFused = 1 << 16;
+// Table entries, old and new, that one workgroup counts.
+constexpr int64_t kForkSmall = 1 << 16;
 // Workgroups that copy for one place, at most.
 constexpr int64_t kForkTiles = 64;
 
@@ -198,8 +198,8 @@ sv_status_t page_fork_common(const sv_fork_shape_t* sh, void* data, const int32_
                          ws_at<int32_t>(workspace, p.off_fresh), ws_at<int32_t>(workspace, p.off_left),
                          (int32_t)p.fresh};
     const int64_t entries = ((int64_t)sh->old + sh->batch) * sh->max_pages;
-    if (entries <= kForkFused && sh->pool.pages <= kForkFused) {
-        hipLaunchKernelGGL((sv::fork_plan_kernel<true>), dim3(1), dim3(sv::kPlanThreads), 0, stream, a);
+    if (entries <= kForkSmall && sh->pool.pages <= sv::kPlanPages && sh->batch <= sv::kPlanThreads) {
+        hipLaunchKernelGGL(sv::fork_small_kernel, dim3(1), dim3(sv::kPlanThreads), 0, stream, a);
     } else {
         const auto grid = [](int64_t n) { return dim3((uint32_t)std::min<int64_t>((n + sv::kThreads - 1) / sv::kThreads, 2048)); };
         if (out_refs != refs) {
@@ -208,7 +208,7 @@ sv_status_t page_fork_common(const sv_fork_shape_t* sh, void* data, const int32_
         }
         hipLaunchKernelGGL(sv::fork_count_kernel, grid(entries), dim3(sv::kThreads), 0, stream, a);
         if (launch_status() != SV_OK) return SV_ERR_HIP;
-        hipLaunchKernelGGL((sv::fork_plan_kernel<false>), dim3(1), dim3(sv::kPlanThreads), 0, stream, a);
+        hipLaunchKernelGGL(sv::fork_plan_kernel, dim3(1), dim3(sv::kPlanThreads), 0, stream, a);
     }
     if (launch_status() != SV_OK) return SV_ERR_HIP;
     by_piece(vecb, [&](auto v) {

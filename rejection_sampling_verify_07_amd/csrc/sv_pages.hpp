@@ -107,7 +107,8 @@ __global__ __launch_bounds__(kThreads) void compact_kernel(CompactArgs a)
 // ---------------------------------------------------------------------------
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanWaves = kPlanThreads / kWave;
-constexpr int kListAhead = 8;  // counts in flight per thread while free pages are listed
+constexpr int kListAhead = 8;   // counts in flight per thread while free pages are listed
+constexpr int kCountAhead = 4;  // table entries in flight per thread while they are counted
 
 struct ForkPlace {
     int32_t source;  // the sequence it continues, -1: none
@@ -210,18 +211,107 @@ __device__ __forceinline__ int32_t plan_scan(int32_t v, int32_t* s_wave, int32_t
     return before + incl - v;
 }
 
-// FUSED: the counts are formed here too (few entries: one launch in place of three).
-template <bool FUSED>
+// One of up to `steps` runs of 64 pages per wave from page p0 on: lane i keeps the free ones of the wave's i-th run,
+// `free(page)` says which are; they are listed behind the `listed` found before.  All threads of the workgroup call it.
+template <class Free>
+__device__ __forceinline__ int32_t list_free(const ForkArgs& a, int64_t p0, int32_t steps, int32_t listed, int32_t* s_wave,
+                                             Free free)
+{
+    const int64_t base = p0 + (int64_t)wave_id() * steps * kWave;
+    uint64_t mine = 0;
+    for (int i0 = 0; i0 < steps; i0 += kListAhead) {
+        bool is[kListAhead];
+#pragma unroll
+        for (int j = 0; j < kListAhead; ++j) {
+            const int64_t page = base + (i0 + j) * kWave + lane_id();
+            is[j] = i0 + j < steps && page < a.pool.pages && free((int32_t)page);
+        }
+#pragma unroll
+        for (int j = 0; j < kListAhead; ++j) {
+            const uint64_t m = __ballot(is[j]);
+            if (lane_id() == i0 + j) mine = m;
+        }
+    }
+    int32_t all;
+    int32_t rank = listed + plan_scan(__popcll(mine), s_wave, &all);
+    const int64_t at = base + (int64_t)lane_id() * kWave;
+    for (; mine != 0 && rank < a.fresh_most; mine &= mine - 1, ++rank)
+        a.fresh[rank] = (int32_t)(at + __builtin_ctzll(mine));
+    return all;
+}
+
+// The plan where one workgroup holds all counts in LDS and a place per thread: the counts are formed here too.  Its
+// steps wait for memory three times (parents, lengths, tables): 64 places of 17 pages, 859 pages: 5 us.
+constexpr int kPlanPages = 8192;
+__global__ __launch_bounds__(kPlanThreads) void fork_small_kernel(ForkArgs a)
+{
+    __shared__ int32_t s_refs[kPlanPages], s_first[kPlanPages], s_source[kPlanThreads], s_full[kPlanThreads];
+    __shared__ int32_t s_wave[kPlanWaves];
+    const int32_t tid = (int32_t)threadIdx.x;
+    ForkPlace p{-1, 0, 0, -1, 0, 0, 0, 0};
+    if (tid < a.batch) p.source = fork_source(a, tid);
+    for (int32_t i = tid; i < a.pool.pages; i += kPlanThreads) {
+        s_refs[i] = a.refs[i];
+        s_first[i] = INT32_MAX;
+    }
+    if (p.source >= 0) {
+        const int32_t len = fork_length(a, p.source);
+        p.full = len / a.pool.page_size;
+        p.rest = len - p.full * a.pool.page_size;
+        int64_t want = len;
+        if (a.new_lengths != nullptr) want = max(want, (int64_t)a.new_lengths[tid]);
+        p.need = (int32_t)min((want + a.pool.page_size - 1) / a.pool.page_size, (int64_t)a.max_pages);
+    }
+    s_source[tid] = p.source;
+    s_full[tid] = p.full;
+    __syncthreads();
+    if (p.rest > 0) {
+        const int32_t page = a.table[(int64_t)p.source * a.table_stride + p.full];
+        if ((uint32_t)page < (uint32_t)a.pool.pages) p.open = page;
+    }
+    // the old tables' entries go, those of the shared pages come
+    const uint32_t cols = (uint32_t)a.max_pages, all = cols * (uint32_t)(a.old + a.batch);
+    for (uint32_t i0 = (uint32_t)tid; i0 < all; i0 += kCountAhead * kPlanThreads) {
+        int32_t page[kCountAhead];
+        bool gone[kCountAhead];
+#pragma unroll
+        for (int j = 0; j < kCountAhead; ++j) {
+            const uint32_t i = i0 + j * kPlanThreads, row = i / cols, col = i - row * cols;
+            page[j] = -1;
+            gone[j] = row < (uint32_t)a.old;
+            if (i >= all) continue;
+            const int32_t s = gone[j] ? (int32_t)row : s_source[row - a.old];
+            if (gone[j] || (s >= 0 && (int32_t)col < s_full[row - a.old]))
+                page[j] = a.table[(int64_t)s * a.table_stride + col];
+        }
+#pragma unroll
+        for (int j = 0; j < kCountAhead; ++j)
+            if ((uint32_t)page[j] < (uint32_t)a.pool.pages) atomicAdd(&s_refs[page[j]], gone[j] ? -1 : 1);
+    }
+    if (p.open >= 0) atomicMin(&s_first[p.open], tid);
+    __syncthreads();
+    // a page that is still written stays with the first place that takes it, if nobody else holds it
+    const bool keeps = p.open >= 0 && s_first[p.open] == tid && s_refs[p.open] == 0;
+    p.begin = p.full + (keeps ? 1 : 0);
+    int32_t want;
+    p.start = plan_scan(tid < a.batch ? p.need - p.begin : 0, s_wave, &want);
+    if (keeps) s_refs[p.open] = 1;
+    if (tid < a.batch) a.places[tid] = p;
+    __syncthreads();
+    const int32_t steps = (a.pool.pages + kPlanThreads - 1) / kPlanThreads;
+    const int32_t listed = list_free(a, 0, steps, 0, s_wave, [&](int32_t page) { return s_refs[page] == 0; });
+    for (int32_t i = tid; i < a.pool.pages; i += kPlanThreads) a.out_refs[i] = s_refs[i];
+    if (tid == 0) {
+        *a.out_free = listed - want;
+        *a.left = min(listed, a.fresh_most);
+    }
+}
+
+// The plan of any size, from counts that launches before it have formed.
 __global__ __launch_bounds__(kPlanThreads) void fork_plan_kernel(ForkArgs a)
 {
     __shared__ int32_t s_wave[kPlanWaves];
     const int32_t tid = (int32_t)threadIdx.x;
-    if constexpr (FUSED) {
-        fork_copy_refs(a, tid, kPlanThreads);
-        wait_stores();
-        __syncthreads();
-        fork_count(a, tid, kPlanThreads);
-    }
     for (int32_t w = tid; w < a.batch; w += kPlanThreads) {
         ForkPlace p{fork_source(a, w), 0, 0, -1, 0, 0, 0, 0};
         if (p.source >= 0) {
@@ -274,32 +364,11 @@ __global__ __launch_bounds__(kPlanThreads) void fork_plan_kernel(ForkArgs a)
     }
     wait_stores();
     __syncthreads();
-    // free pages in rising order.  A wave takes `span` pages, 64 at a time; lane i keeps the free ones of the i-th 64.
+    // free pages in rising order
     const int32_t steps = min(kWave, (a.pool.pages + kPlanThreads - 1) / kPlanThreads);
     int32_t listed = 0;
-    for (int64_t p0 = 0; p0 < a.pool.pages; p0 += (int64_t)steps * kPlanThreads) {
-        const int64_t base = p0 + (int64_t)wave_id() * steps * kWave;
-        uint64_t mine = 0;
-        for (int i0 = 0; i0 < steps; i0 += kListAhead) {
-            int32_t held[kListAhead];
-#pragma unroll
-            for (int j = 0; j < kListAhead; ++j) {
-                const int64_t page = base + (i0 + j) * kWave + lane_id();
-                held[j] = i0 + j < steps && page < a.pool.pages ? ld_agent(a.out_refs + page) : 1;
-            }
-#pragma unroll
-            for (int j = 0; j < kListAhead; ++j) {
-                const uint64_t m = __ballot(held[j] == 0);
-                if (lane_id() == i0 + j) mine = m;
-            }
-        }
-        int32_t all;
-        int32_t rank = listed + plan_scan(__popcll(mine), s_wave, &all);
-        const int64_t at = base + (int64_t)lane_id() * kWave;
-        for (; mine != 0 && rank < a.fresh_most; mine &= mine - 1, ++rank)
-            a.fresh[rank] = (int32_t)(at + __builtin_ctzll(mine));
-        listed += all;
-    }
+    for (int64_t p0 = 0; p0 < a.pool.pages; p0 += (int64_t)steps * kPlanThreads)
+        listed += list_free(a, p0, steps, listed, s_wave, [&](int32_t page) { return ld_agent(a.out_refs + page) == 0; });
     if (tid == 0) {
         *a.out_free = listed - want;
         *a.left = min(listed, a.fresh_most);

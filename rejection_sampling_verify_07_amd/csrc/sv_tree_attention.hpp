@@ -609,12 +609,13 @@ __device__ __forceinline__ uint32_t lds_address(const char* p) { return (uint32_
 
 // 16 bytes from each lane's place `off` behind `base` into LDS, lane i's at `to` + 16 i (`to`: the wave's).  In assembly, which the compiler
 // does not count among the loads in flight: it would wait for all of them before every transposed read of a tile.
-// arrived() is the wait for them; a wave has none left when its loop over the tiles ends.
+// arrived() is the wait for them; a wave has none left when its loop over the tiles ends.  (M0 is not kept between
+// instructions that take it: nothing else here does.)
 __device__ __forceinline__ void load_to_lds(const char* base, uint32_t off, uint32_t to)
 {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(to), "v"(off),
                  "s"((const SV_GLOBAL char*)base)
-                 : "memory", "m0");
+                 : "memory");
 }
 
 // All but the newest N of this wave's loads have arrived, and what it read of LDS; then all waves have come here.

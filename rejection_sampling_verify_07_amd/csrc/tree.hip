@@ -22,8 +22,17 @@ constexpr int32_t kMaxTokens = 1 << 30;
 
 // ---- edits of logits
 
-// Tokens of the vocabulary per workgroup.
-constexpr int kAdjustChunk = 8192;
+// Threads of a workgroup, of 8 tokens of the vocabulary each.  320 rows of 151936 bf16 logits with texts of up to 8000
+// tokens: 46 us with 512, 45 with 1024, 51 with 256; with smaller tables in LDS more workgroups stay on a CU, with larger
+// ones fewer of them read the texts.  Calls of few workgroups take 256: one row of 50304 fp32 logits 5.5 us, 7.5 with
+// 1024 threads.
+constexpr int kAdjustThreads = 512;
+constexpr int kAdjustThreadsFew = 256;
+constexpr int kAdjustTokens = 8;
+constexpr int64_t kAdjustFew = 256;  // workgroups below which the rows of a call count as few
+constexpr int kAdjustRows = 4;       // rows in flight together
+// Bias entries that a table of 16 bits can number.
+constexpr int32_t kAdjustFewBiases = 65535;
 // Workgroups that the rows of a sequence are divided for.
 constexpr int64_t kAdjustGroups = 1024;
 
@@ -100,21 +109,32 @@ sv_status_t adjust_logits_common(const sv_adjust_shape_t* sh, const sv_adjust_t*
     a.mask_stride = ad->mask_stride * 4;
     a.num_masks = ad->num_masks;
     a.mask_rows = ad->mask_rows;
-    a.nchunk = (sh->vocab + kAdjustChunk - 1) / kAdjustChunk;
-    const int64_t rows = sh->max_draft + 1, one = (int64_t)sh->batch * a.nchunk;
-    const int64_t runs = std::min(std::max<int64_t>(kAdjustGroups / one, 1), rows);
-    a.run_rows = (int32_t)((rows + runs - 1) / runs);
-    a.runs = (int32_t)((rows + a.run_rows - 1) / a.run_rows);
-    if (!launchable((double)one * a.runs, sv::kThreads)) return SV_ERR_UNSUPPORTED;
-    const uint32_t grid = (uint32_t)(one * a.runs);
-    return by_dtype(sh->dtype, [&](auto dtc) {
-        constexpr int DT = decltype(dtc)::value, CT = kAdjustChunk;
-        const bool bias = a.total_bias > 0;
-        if (logits == out && bias) launch_stream(prof, sv::adjust_kernel<DT, true, true, CT>, grid, stream, a);
-        else if (logits == out) launch_stream(prof, sv::adjust_kernel<DT, true, false, CT>, grid, stream, a);
-        else if (bias) launch_stream(prof, sv::adjust_kernel<DT, false, true, CT>, grid, stream, a);
-        else launch_stream(prof, sv::adjust_kernel<DT, false, false, CT>, grid, stream, a);
+    const int64_t rows = sh->max_draft + 1;
+    const auto launch = [&](auto dt, auto inplace, auto bias, auto threads) -> sv_status_t {
+        constexpr int DT = decltype(dt)::value, NT = decltype(threads)::value, CT = NT * kAdjustTokens;
+        a.nchunk = (sh->vocab + CT - 1) / CT;
+        const int64_t one = (int64_t)sh->batch * a.nchunk;
+        const int64_t runs = std::min(std::max<int64_t>(kAdjustGroups / one, 1), rows);
+        a.run_rows = (int32_t)((rows + runs - 1) / runs);
+        a.runs = (int32_t)((rows + a.run_rows - 1) / a.run_rows);
+        if (!launchable((double)one * a.runs, NT)) return SV_ERR_UNSUPPORTED;
+        launch_stream_nt(prof, sv::adjust_kernel<DT, decltype(inplace)::value, decltype(bias)::value, CT, NT, kAdjustRows>,
+                         (uint32_t)(one * a.runs), NT, stream, a);
         return launch_status();
+    };
+    const bool few =
+        (int64_t)sh->batch * rows * (sh->vocab / (kAdjustThreads * kAdjustTokens) + 1) < kAdjustFew;
+    return by_dtype(sh->dtype, [&](auto dt) {
+        const auto by_size = [&](auto inplace, auto bias) {
+            return few ? launch(dt, inplace, bias, std::integral_constant<int, kAdjustThreadsFew>{})
+                       : launch(dt, inplace, bias, std::integral_constant<int, kAdjustThreads>{});
+        };
+        const auto by_bias = [&](auto inplace) {
+            if (a.total_bias == 0) return by_size(inplace, std::integral_constant<int, sv::BIAS_NONE>{});
+            if (a.total_bias <= kAdjustFewBiases) return by_size(inplace, std::integral_constant<int, sv::BIAS_16>{});
+            return by_size(inplace, std::integral_constant<int, sv::BIAS_32>{});
+        };
+        return logits == out ? by_bias(std::true_type{}) : by_bias(std::false_type{});
     });
 }
 
