@@ -15,11 +15,8 @@
 // grow with the caches, and sequences of any mix of lengths keep all CUs busy.
 //
 // Positions come in grains of 16, which never cross a page: a wave finds a
-// grain's page with scalar loads, a step before the keys' own loads.
-//   Few rows per key head (up to 16 or 32): each wave walks its own 32 keys of a
-// round with all rows, K and V straight from memory to registers (attend_rows).
-//   More: the four waves share the rows and take tiles of 64 keys through LDS
-// (attend_tree_tiles).
+// grain's page with scalar loads, a page ahead.  The four waves of a workgroup share the rows and take tiles of keys through LDS, where loads put them by
+// themselves (attend_tree_tiles).
 #pragma once
 
 #include "sv_attention.hpp"
@@ -45,7 +42,7 @@ struct TreeArgs {
     int32_t q_heads, kv_heads, rep;
     float c;                                         // scale * log2(e)
     int32_t groups, tiles;                           // stretches of the line; row tiles
-    int32_t* plan;                                   // [batch + 1] rounds before each sequence, then the stretch
+    int32_t* plan;                                   // [batch + 1] rounds before each sequence, the stretch, the extra
     float* acc;                                      // [2 * groups][tile][row][D]
     float2* ml;                                      // [2 * groups][tile][row]
 };
@@ -92,71 +89,12 @@ __device__ __forceinline__ int32_t grain_page(const TreeArgs& a, const Stretch& 
     return (uint32_t)page < (uint32_t)a.pages ? page : -1;
 }
 
-// Where N neighbouring grains lie: page (-1: none) and position in it.
-template <int N>
-struct Grains {
-    int32_t page[N], in[N];
-    __device__ __forceinline__ bool sound() const
-    {
-        int32_t x = 0;
-#pragma unroll
-        for (int g = 0; g < N; ++g) x |= page[g];
-        return x >= 0;
-    }
-};
-
 // A scalar load: the tables are not written while a kernel reads them.  (A vector load that a loop carries along keeps
 // the compiler from letting the tiles' loads run ahead: it waits for all of them.)
 __device__ __forceinline__ int32_t scalar_load(const int32_t* p)
 {
     return *(const __attribute__((address_space(4))) int32_t*)p;
 }
-
-// Walks grains g, g + STEP, ...: N neighbours each time.  Their pages are asked for one step before they are needed.
-template <int N, int STEP>
-struct GrainCursor {
-    int32_t number, rest;  // the next grain's page number, and its place in that page
-    int32_t key;           // its first key
-    Grains<N> asked;       // those of `key`, as the table says
-
-    __device__ __forceinline__ void ask(const TreeArgs& a, const Stretch& s)
-    {
-        int32_t n = number, r = rest;
-#pragma unroll
-        for (int g = 0; g < N; ++g) {
-            asked.page[g] = s.table != nullptr ? scalar_load(s.table + min(n, s.pages - 1)) : s.b;
-            asked.in[g] = r * 16;
-            const bool over = ++r == a.grains;
-            n += over ? 1 : 0;
-            r = over ? 0 : r;
-        }
-        if constexpr (STEP == N) {
-            number = n;
-            rest = r;
-        } else {
-            const int32_t q = page_of_grain(a, rest + STEP);
-            number += q;
-            rest += STEP - q * a.grains;
-        }
-    }
-    __device__ __forceinline__ void start(const TreeArgs& a, const Stretch& s, int32_t first_key)
-    {
-        key = first_key;
-        number = page_of_grain(a, key / 16);
-        rest = key / 16 - number * a.grains;
-        ask(a, s);
-    }
-    __device__ __forceinline__ Grains<N> next(const TreeArgs& a, const Stretch& s)
-    {
-        Grains<N> w = asked;
-#pragma unroll
-        for (int g = 0; g < N; ++g)
-            if (key + g * 16 >= s.total || (uint32_t)w.page[g] >= (uint32_t)a.pages) w.page[g] = -1;
-        key += STEP * 16;
-        ask(a, s);
-        return w;
-    }
-};
 
 // Walks all grains of a stretch in order: where the next one's keys and values lie.  Within a page a step is an
 // addition per pointer; the next page's number is asked for a page ahead.  (Scalar work: it runs beside the products in
@@ -216,12 +154,17 @@ __device__ __forceinline__ void tree_views(const Stretch& s, int32_t t0, int32_t
     for (int32_t i = tid; i < n; i += kAttnThreads) {
         uint32_t w[kTreeWords] = {~0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
         int32_t r = t0 + i;
-        while (true) {
+        if (s.parents == nullptr) {  // a chain: all rows up to r
 #pragma unroll
-            for (int x = 0; x < 5; ++x) w[x + 1] |= r / 32 == x ? 1u << (r % 32) : 0u;
-            if (r == 0) break;
-            const int32_t up = s.parents != nullptr ? s_up[r - 1] : r - 1;
-            r = up >= 0 && up < r ? up : 0;
+            for (int x = 0; x < 5; ++x) w[x + 1] = r >= x * 32 + 31 ? ~0u : r >= x * 32 ? (2u << (r % 32)) - 1 : 0u;
+        } else {
+            while (true) {
+#pragma unroll
+                for (int x = 0; x < 5; ++x) w[x + 1] |= r / 32 == x ? 1u << (r % 32) : 0u;
+                if (r == 0) break;
+                const int32_t up = s_up[r - 1];
+                r = up >= 0 && up < r ? up : 0;
+            }
         }
 #pragma unroll
         for (int x = 0; x < kTreeWords; ++x) s_view[i * kTreeWords + x] = w[x];
@@ -237,12 +180,6 @@ __device__ __forceinline__ uint32_t sees4(const uint32_t* w, int32_t e)
     return (uint32_t)((((uint64_t)w[at + 1] << 32) | w[at]) >> (e & 31)) & 15u;
 }
 __device__ __forceinline__ bool sees(const uint32_t* w, int32_t e) { return e < 0 || (sees4(w, e) & 1u) != 0; }
-
-template <int D, int MT>
-constexpr size_t tree_rows_lds()
-{
-    return attn_lds_floats(D, MT) * 4;
-}
 
 // All loads of this wave have arrived, in a form that the compiler counts: before a loop, so that it does not wait in
 // every step for what the first one needs.
@@ -267,330 +204,7 @@ __device__ __forceinline__ void store4(char* p, float x0, float x1, float x2, fl
     *(SV_GLOBAL u32x2*)p = w;
 }
 
-// MT tiles of 16 query rows in every wave, 32 keys of each round per wave.
-template <int DT, int D, int MT>
-__device__ __forceinline__ void attend_rows(const TreeArgs& a, const Stretch& st, int32_t tile, const TreeOut& to,
-                                            const uint32_t* s_view, float* s_mem)
-{
-    constexpr int DC = D / 32;   // 32-wide chunks of the score product
-    constexpr int DPL = D / 16;  // columns of V per lane
-    constexpr int VW = DPL / 2;  // 32-bit words of a lane's V row
-    const int lane = lane_id(), l16 = lane & 15, lg = lane >> 4;
-    const int wave = __builtin_amdgcn_readfirstlane(wave_id());
-    const int32_t m_total = st.nrows * a.rep;
-    const int32_t r0 = tile * (MT * 16), t0 = r0 / a.rep;
-
-    u32x4 qf[MT][DC];  // query rows: column l16 of each tile; rows past the matrix are zero
-    const uint32_t* view[MT];
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-        const int32_t r = r0 + mt * 16 + l16;
-        const int32_t t = r / a.rep, h = st.hk * a.rep + (r - t * a.rep);
-        const char* qp = a.q + (int64_t)(st.row0 + t) * a.q_row + (int64_t)h * a.q_head + lg * 16;
-#pragma unroll
-        for (int c = 0; c < DC; ++c)
-            qf[mt][c] = r < m_total ? *(const SV_GLOBAL u32x4*)(qp + c * 64) : u32x4{0u, 0u, 0u, 0u};
-        view[mt] = s_view + (r < m_total ? t - t0 : 0) * kTreeWords;
-    }
-    f32x4 o[MT][DPL];
-    float m[MT], l[MT];
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-        m[mt] = kNoReference;
-        l[mt] = 0.0f;
-#pragma unroll
-        for (int d = 0; d < DPL; ++d) o[mt][d] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    }
-
-    // a lane's keys inside a grain: K row l16; V rows 4 lg + j
-    const uint32_t koff = (uint32_t)(l16 * a.k_pos + lg * 16);
-    uint32_t voff[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) voff[j] = (uint32_t)((lg * 4 + j) * a.v_pos + l16 * (DPL * 2));
-    typedef Grains<2> Block;  // 32 keys
-    // Rows of a grain that hold keys: the last one stands in for those behind it (masked below), row 0 of the pool for
-    // all of a grain without a page.
-    auto last_of = [&](const Block& p, int32_t kb, int t) {
-        return p.page[t] < 0 ? 0 : min(15, st.total - 1 - (kb + t * 16));
-    };
-    auto load_k = [&](int32_t kb, const Block& p, u32x4 (&kf)[2][DC], auto edge, auto past) {
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            const char* base = st.k + max(p.page[t], 0) * a.k_page + (int64_t)(p.page[t] < 0 ? 0 : p.in[t]) * a.k_pos;
-            uint32_t off = koff;
-            if constexpr (decltype(edge)::value) off = (uint32_t)(min(l16, last_of(p, kb, t)) * a.k_pos + lg * 16);
-#pragma unroll
-            for (int c = 0; c < DC; ++c) kf[t][c] = load16<decltype(past)::value>((const u32x4*)(base + off + c * 64));
-        }
-    };
-    auto load_v = [&](int32_t kb, const Block& p, uint32_t (&vr)[8][VW], auto edge, auto past) {
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            const char* base = st.v + max(p.page[t], 0) * a.v_page + (int64_t)(p.page[t] < 0 ? 0 : p.in[t]) * a.v_pos;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                uint32_t off = voff[j];
-                if constexpr (decltype(edge)::value)
-                    off = (uint32_t)(min(lg * 4 + j, last_of(p, kb, t)) * a.v_pos + l16 * (DPL * 2));
-                const char* x = base + off;
-                if constexpr (VW == 2) {
-                    const u32x2 w = *(const SV_GLOBAL u32x2*)x;
-                    vr[t * 4 + j][0] = w.x;
-                    vr[t * 4 + j][1] = w.y;
-                } else {
-#pragma unroll
-                    for (int y = 0; y < VW / 4; ++y) {
-                        const u32x4 w = load16<decltype(past)::value>((const u32x4*)(x + y * 16));
-#pragma unroll
-                        for (int z = 0; z < 4; ++z) vr[t * 4 + j][y * 4 + z] = w[z];
-                    }
-                }
-            }
-        }
-    };
-
-    bool wild = false;  // (uniform) a masked block held a value that is not finite
-    bool far = false;   // (uniform) a reference lies beyond kFarReference
-    int32_t kb = st.begin + wave * kKeyBlock;
-    GrainCursor<2, kKeyRound / 16> cursor;
-    cursor.start(a, st, kb);
-    Block now = cursor.next(a, st);
-    u32x4 kf[2][DC];  // the block at hand; the next one's is loaded once the scores have taken it
-    auto next_k = [&](int32_t x, const Block& p) {
-        if (x >= st.end) return;
-        with_policy(st.past, [&](auto past) {
-            if (x + kKeyBlock <= st.total && p.sound()) load_k(x, p, kf, std::false_type{}, past);
-            else load_k(x, p, kf, std::true_type{}, past);
-        });
-    };
-    bool masked = false;  // (uniform) from the first block on that rows see in part, or whose pages are not all there
-    int32_t masked_from = st.end;
-    next_k(kb, now);
-    loads_done();
-    while (kb < st.end) {
-        if (!masked && (kb + kKeyBlock > st.context || !now.sound())) {
-            masked = true;
-            masked_from = kb;
-        }
-        uint32_t vr[8][VW];
-        with_policy(st.past, [&](auto past) {
-            if (!masked) load_v(kb, now, vr, std::false_type{}, past);
-            else load_v(kb, now, vr, std::true_type{}, past);
-        });
-        f32x4 s[2][MT];
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-                s[t][mt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                for (int c = 0; c < DC; ++c) s[t][mt] = mfma_16x16x32<DT>(kf[t][c], qf[mt][c], s[t][mt]);
-            }
-        const Block next = cursor.next(a, st);
-        next_k(kb + kKeyRound, next);
-        if (masked) {
-#pragma unroll
-            for (int t = 0; t < 2; ++t)
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt) {
-                    const uint32_t seen =
-                        now.page[t] < 0 ? 0u : sees4(view[mt], kb + t * 16 + lg * 4 - st.context);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if ((seen >> i & 1u) == 0) s[t][mt][i] = neg_inf();
-                }
-        }
-        // move a reference that a score exceeds by the slack (the first one always does)
-        float top[MT];
-        bool over = false;
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-            float x = fmaxf(s[0][mt][0], s[0][mt][1]);
-#pragma unroll
-            for (int i = 2; i < 8; ++i) x = fmaxf(x, s[i / 4][mt][i & 3]);
-            top[mt] = x * a.c;
-            over |= top[mt] > m[mt] + (Reference<DT>::kBelow + Reference<DT>::kSlack);
-        }
-        if (__any(over)) {
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-                float x = top[mt];
-                x = fmaxf(x, __shfl_xor(x, 16, kWave));
-                x = fmaxf(x, __shfl_xor(x, 32, kWave));
-                x = fmaxf(x - Reference<DT>::kBelow, m[mt]);
-                const float f = __builtin_amdgcn_exp2f(m[mt] - x);
-                m[mt] = x;
-                l[mt] *= f;
-#pragma unroll
-                for (int d = 0; d < DPL; ++d) o[mt][d] *= f;
-            }
-            far = far_references<MT>(m);
-        }
-        if (__builtin_expect(far, 0)) {
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                for (int i = 0; i < 8; ++i) s[i / 4][mt][i & 3] = far_distance(s[i / 4][mt][i & 3], a.c, m[mt]);
-        }
-        const float c = far ? 1.0f : a.c;
-        u32x4 pf[MT];
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-            const float ref = far ? 0.0f : m[mt];
-            float p[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i / 4][mt][i & 3], c, -ref));
-                l[mt] += p[i];
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) pf[mt][i] = pack2<DT>(p[2 * i], p[2 * i + 1]);
-        }
-        if (masked) {
-            // none for keys past the last one, or without a page
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const bool there = now.page[j / 4] >= 0 && kb + (j < 4 ? 0 : 12) + lg * 4 + j < st.total;
-#pragma unroll
-                for (int x = 0; x < VW; ++x) vr[j][x] = there ? vr[j][x] : 0u;
-            }
-            // A value that is not finite times the weight 0 of a row that does not see it would be NaN: such values
-            // count as 0 here, and reach the rows that see them after the last block.
-            bool any = false;
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-#pragma unroll
-                for (int x = 0; x < VW; ++x) any |= finite_halves<DT>(vr[j][x]) != vr[j][x];
-            if (__any(any)) {
-                wild = true;
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-#pragma unroll
-                    for (int x = 0; x < VW; ++x) vr[j][x] = finite_halves<DT>(vr[j][x]);
-            }
-        }
-#pragma unroll
-        for (int d = 0; d < DPL; ++d) {
-            u32x4 vf;
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                vf[i] = __builtin_amdgcn_perm(vr[2 * i + 1][d / 2], vr[2 * i][d / 2], d & 1 ? 0x07060302u : 0x05040100u);
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt) o[mt][d] = mfma_16x16x32<DT>(vf, pf[mt], o[mt][d]);
-        }
-        now = next;
-        kb += kKeyRound;
-    }
-    if (wild) {
-#pragma unroll 1
-        for (kb = masked_from; kb < st.end; kb += kKeyRound)
-#pragma unroll 1
-            for (int t = 0; t < 2; ++t) {
-                int32_t in;
-                const int32_t page = grain_page(a, st, kb / 16 + t, &in);
-                if (page < 0) continue;
-                const char* base = st.v + page * a.v_page + (int64_t)in * a.v_pos;
-#pragma unroll 1
-                for (int32_t x = 0; x < min(16, st.total - (kb + t * 16)); ++x) {
-                    // accumulator i of tile d holds column (4 lg + i) * DPL + d
-                    const SV_GLOBAL uint32_t* row =
-                        (const SV_GLOBAL uint32_t*)(base + (int64_t)x * a.v_pos + lg * (4 * DPL * 2));
-                    bool see[MT];
-#pragma unroll
-                    for (int mt = 0; mt < MT; ++mt) see[mt] = sees(view[mt], kb + t * 16 + x - st.context);
-#pragma unroll
-                    for (int e = 0; e < 4 * DPL; e += 2) {
-                        const uint32_t w = row[e / 2], bad = w ^ finite_halves<DT>(w);
-#pragma unroll
-                        for (int y = 0; y < 2; ++y) {
-                            const float v = y ? hi16<DT>(bad) : lo16<DT>(bad);  // 0 where the value was finite
-#pragma unroll
-                            for (int mt = 0; mt < MT; ++mt)
-                                if (see[mt]) o[mt][(e + y) % DPL][(e + y) / DPL] += v;
-                        }
-                    }
-                }
-            }
-    }
-
-    // ---- join the four waves: a common reference, then o summed in a fixed order
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-        l[mt] += __shfl_xor(l[mt], 16, kWave);
-        l[mt] += __shfl_xor(l[mt], 32, kWave);
-    }
-    float* s_m = s_mem;                                 // [wave][MT * 16]
-    float* s_l = s_m + kAttnWaves * MT * 16;            // [wave][MT * 16]
-    f32x4* s_o = (f32x4*)(s_l + kAttnWaves * MT * 16);  // [2][MT * DPL][64]
-    if (lg == 0) {
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-            s_m[(wave * MT + mt) * 16 + l16] = m[mt];
-            s_l[(wave * MT + mt) * 16 + l16] = l[mt];
-        }
-    }
-    __syncthreads();
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-        float x = s_m[mt * 16 + l16];
-#pragma unroll
-        for (int w = 1; w < kAttnWaves; ++w) x = fmaxf(x, s_m[(w * MT + mt) * 16 + l16]);
-        const float f = __builtin_amdgcn_exp2f(m[mt] - x);
-        float sum = 0.0f;
-#pragma unroll
-        for (int w = 0; w < kAttnWaves; ++w)
-            sum += s_l[(w * MT + mt) * 16 + l16] * __builtin_amdgcn_exp2f(s_m[(w * MT + mt) * 16 + l16] - x);
-        m[mt] = x;
-        l[mt] = sum;
-#pragma unroll
-        for (int d = 0; d < DPL; ++d) o[mt][d] *= f;
-    }
-#pragma unroll
-    for (int half = 2; half >= 1; half >>= 1) {
-        if (wave >= half && wave < 2 * half) {
-#pragma unroll
-            for (int i = 0; i < MT * DPL; ++i) s_o[((wave - half) * MT * DPL + i) * kWave + lane] = o[i / DPL][i % DPL];
-        }
-        __syncthreads();
-        if (wave < half) {
-#pragma unroll
-            for (int i = 0; i < MT * DPL; ++i) o[i / DPL][i % DPL] += s_o[(wave * MT * DPL + i) * kWave + lane];
-        }
-        __syncthreads();
-    }
-    if (wave != 0) return;
-    // accumulator i of tile d holds column (4 lg + i) * DPL + d
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-        const int32_t r = r0 + mt * 16 + l16;
-        if (r >= m_total) continue;
-        const int32_t t = r / a.rep, h = st.hk * a.rep + (r - t * a.rep);
-        if (to.whole) {
-            const float inv = l[mt] != 0.0f ? 1.0f / l[mt] : 0.0f;
-            char* dst = a.out + (int64_t)(st.row0 + t) * a.out_row + (int64_t)h * a.out_head + lg * (4 * DPL * 2);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int d = 0; d < DPL; d += 4)
-                    store4<DT>(dst + (i * DPL + d) * 2, o[mt][d][i] * inv, o[mt][d + 1][i] * inv, o[mt][d + 2][i] * inv,
-                               o[mt][d + 3][i] * inv);
-            if (a.lse != nullptr && lg == 0)
-                a.lse[(int64_t)(st.row0 + t) * a.q_heads + h] =
-                    l[mt] != 0.0f ? (m[mt] + __builtin_amdgcn_logf(l[mt])) * 0.69314718055994531f : neg_inf();
-        } else {
-            const int64_t at = to.slot * (MT * 16) + mt * 16 + l16;
-            if (lg == 0) a.ml[at] = float2{m[mt], l[mt]};
-            SV_GLOBAL f32x4* dst = (SV_GLOBAL f32x4*)(a.acc + at * D + lg * 4 * DPL);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int d = 0; d < DPL; d += 4)
-                    dst[(i * DPL + d) / 4] = f32x4{o[mt][d][i], o[mt][d + 1][i], o[mt][d + 2][i], o[mt][d + 3][i]};
-        }
-    }
-}
-
-// ---- many rows per key head: four waves of MT * 16 rows share tiles of keys through LDS, whose rows lie and are read
+// Four waves of MT * 16 rows share tiles of keys through LDS, whose rows lie and are read
 // as in TileAttention.  Four tiles of 16 KB (64 columns: of 64 keys; 128: of 32) are on their way or in use: with two
 // of them a step lasted as long as a read of memory.
 template <int D>
@@ -611,11 +225,17 @@ __device__ __forceinline__ uint32_t lds_address(const char* p) { return (uint32_
 // does not count among the loads in flight: it would wait for all of them before every transposed read of a tile.
 // arrived() is the wait for them; a wave has none left when its loop over the tiles ends.  (M0 is not kept between
 // instructions that take it: nothing else here does.)
+template <bool PAST>
 __device__ __forceinline__ void load_to_lds(const char* base, uint32_t off, uint32_t to)
 {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(to), "v"(off),
-                 "s"((const SV_GLOBAL char*)base)
-                 : "memory");
+    if constexpr (PAST)
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2 nt" ::"s"(to), "v"(off),
+                     "s"((const SV_GLOBAL char*)base)
+                     : "memory");
+    else
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(to), "v"(off),
+                     "s"((const SV_GLOBAL char*)base)
+                     : "memory");
 }
 
 // All but the newest N of this wave's loads have arrived, and what it read of LDS; then all waves have come here.
@@ -627,7 +247,7 @@ __device__ __forceinline__ void arrived()
 
 template <int DT, int D, int MT>
 __device__ __forceinline__ void attend_tree_tiles(const TreeArgs& a, const Stretch& st, int32_t tile, const TreeOut& to,
-                                                  const uint32_t* s_view, int32_t* s_wild, char* s_kv)
+                                                  int32_t* s_up, uint32_t* s_view, int32_t* s_wild, char* s_kv)
 {
     typedef TreeTile<D> TA;
     constexpr int ROWS = kAttnWaves * MT * 16;
@@ -667,20 +287,20 @@ __device__ __forceinline__ void attend_tree_tiles(const TreeArgs& a, const Stret
     KeyWalk walk;
     int32_t kb = st.begin, ahead = st.begin;  // the tile in use, the next one to load
     int32_t bad_from = INT32_MAX;             // the first tile met that has a grain without a page
+    uint32_t there = 0;                       // four bits per buffer: the grains of its tile that have pages
     walk.start(a, st, kb);
-    auto load_next = [&](int buf) {
-        if (ahead >= st.end) return;
+    auto load_tile = [&](int buf, auto past) {
         const uint32_t dst = lds_address(s_kv) + (uint32_t)(buf * (2 * TA::TILE) + wave * (kWave * 16));
         const bool edge = ahead + KT > st.total;
-        int32_t pages = 0;
+        uint32_t pages = 0;
 #pragma unroll
         for (int i = 0; i < TA::LOADS; ++i) {
             // this load's grain: pointers before and after a step where it has two
             const char *k = walk.k, *v = walk.v;
-            pages |= walk.page;
+            pages |= walk.page >= 0 ? 1u << (i * RPL / 16) : 0u;
             if constexpr (RPL == 32) {
                 walk.step(a, st);
-                pages |= walk.page;
+                pages |= walk.page >= 0 ? 2u << (i * 2) : 0u;
                 k = half != 0 ? walk.k : k;
                 v = half != 0 ? walk.v : v;
             }
@@ -694,12 +314,16 @@ __device__ __forceinline__ void attend_tree_tiles(const TreeArgs& a, const Stret
                 k = last < 0 ? st.k : k;
                 v = last < 0 ? st.v : v;
             }
-            load_to_lds(k, ko, dst + i * (kAttnThreads * 16));
-            load_to_lds(v, vo, dst + TA::TILE + i * (kAttnThreads * 16));
+            load_to_lds<decltype(past)::value>(k, ko, dst + i * (kAttnThreads * 16));
+            load_to_lds<decltype(past)::value>(v, vo, dst + TA::TILE + i * (kAttnThreads * 16));
             if (x == PER - 1) walk.step(a, st);
         }
-        if (pages < 0) bad_from = min(bad_from, ahead);
+        if (pages != (1u << GR) - 1) bad_from = min(bad_from, ahead);
+        there = (there & ~(15u << (buf * 4))) | pages << (buf * 4);
         ahead += KT;
+    };
+    auto load_next = [&](int buf) {
+        if (ahead < st.end) with_policy(st.past, [&](auto past) { load_tile(buf, past); });
     };
     // No value for keys past the last one or without a page; one that is not finite counts as 0 here (times the weight 0
     // of a row that does not see it, it would be NaN) and reaches the rows that see it at the end.
@@ -724,6 +348,7 @@ __device__ __forceinline__ void attend_tree_tiles(const TreeArgs& a, const Stret
     if (threadIdx.x == 0) *s_wild = 0;
 #pragma unroll
     for (int x = 0; x + 1 < TA::BUFS; ++x) load_next(x);
+    if (st.end > st.context) tree_views(st, t0, min(st.nrows, ((tile + 1) * ROWS - 1) / a.rep + 1) - t0, s_up, s_view);
     u32x4 qf[MT][DC];
     const uint32_t* view[MT];
 #pragma unroll
@@ -737,6 +362,7 @@ __device__ __forceinline__ void attend_tree_tiles(const TreeArgs& a, const Stret
         view[mt] = s_view + (r < m_total ? t - t0 : 0) * kTreeWords;
     }
     loads_done();
+    const bool younger = blockIdx.x >= gridDim.x / 2;
     int buf = 0;
     uint32_t here = 0;    // a masked tile: which grains have pages
     bool masked = false;  // (uniform) from the first tile on that rows see in part, or whose pages are not all there
@@ -857,18 +483,21 @@ __device__ __forceinline__ void attend_tree_tiles(const TreeArgs& a, const Stret
     while (kb < st.end) {
         // the tile after this one has arrived (the one behind it need not have), and all waves have left the one before
         // this, whose place the next load takes
-        if (kb + 2 * KT < st.end) arrived<2 * TA::LOADS>();
+        if (kb + (TA::BUFS - 2) * KT < st.end) arrived<2 * TA::LOADS * (TA::BUFS - 3)>();
         else arrived<0>();
         load_next((buf + TA::BUFS - 1) % TA::BUFS);
+        // The older of a CU's two workgroups goes first where both could: the younger one leads in three tiles of four,
+        // or it ends 10% later (the line is dealt evenly).  With more rows the products are what counts: no gain.
+        if constexpr (MT == 1 && D != 256) {
+            if (younger && (kb / KT & 3) != 0) __builtin_amdgcn_s_setprio(1);
+            else __builtin_amdgcn_s_setprio(0);
+        }
         if (!masked && (kb + KT > st.context || kb >= bad_from)) {
             masked = true;
             masked_from = kb;
         }
         if (masked) {
-            here = 0;
-            int32_t in;
-#pragma unroll
-            for (int g = 0; g < GR; ++g) here |= grain_page(a, st, kb / 16 + g, &in) >= 0 ? 1u << g : 0u;
+            here = there >> (buf * 4);
             clear(buf, kb, here);
             __syncthreads();
         }
@@ -929,24 +558,26 @@ __device__ __forceinline__ void attend_tree_tiles(const TreeArgs& a, const Stret
     }
 }
 
-// Rounds of a pair's keys: what the line counts.
-template <bool TILES>
-constexpr int kTreeRound = TILES ? 64 : kKeyRound;
+constexpr int kTreeRound = 64;  // keys: what the line of all pairs counts
+// A pair counts this many rounds beyond its own where stretches have at least kTreeExtraFrom: what a stretch's start and
+// end cost.  (16 trees of 32 rows on 9000 positions: 145 us without, 142 with 2, 141 with 4; 48 rows on 1000 to 8000
+// each: 160, 158 and 164.)
+constexpr int kTreeExtra = 2, kTreeExtraFrom = 8;
 
 // The line's length and where a stretch begins, by all threads of the workgroup: thread t sums the sequences t * per
 // .. t * per + per - 1.
 struct TreeStart {
     int32_t total, stretch;  // rounds of the line, and of one workgroup
+    int32_t extra;           // rounds that a pair counts beyond its own
     int32_t b, at;           // the sequence that holds the first round, and the rounds of it before that one
 };
-template <int KB>
 __device__ __forceinline__ TreeStart tree_start(const TreeArgs& a, int32_t group, bool write, int32_t* s_sum,
                                                 int32_t* s_found)
 {
     const int32_t tid = (int32_t)threadIdx.x, per = (a.batch + kAttnThreads - 1) / kAttnThreads;
     const int32_t b0 = min(tid * per, a.batch), b1 = min(b0 + per, a.batch);
     int32_t mine = 0;
-    for (int32_t b = b0; b < b1; ++b) mine += (tree_length(a, b) + KB - 1) / KB * a.kv_heads;
+    for (int32_t b = b0; b < b1; ++b) mine += (tree_length(a, b) + kTreeRound - 1) / kTreeRound * a.kv_heads;
     const int32_t incl = wave_incl_scan_int(mine);
     if (lane_id() == kWave - 1) s_sum[wave_id()] = incl;
     __syncthreads();
@@ -957,23 +588,28 @@ __device__ __forceinline__ TreeStart tree_start(const TreeArgs& a, int32_t group
         before += w < wave_id() ? x : 0;
         total += x;
     }
+    const int32_t extra = total / a.groups >= kTreeExtraFrom ? kTreeExtra * a.kv_heads : 0;  // per sequence
+    before += extra * b0;
+    mine += extra * (b1 - b0);
+    total += extra * a.batch;
     const int32_t stretch = max(1, (total + a.groups - 1) / a.groups);
     const int64_t from = (int64_t)group * stretch;
     if (write) {
         int32_t sum = before;
         for (int32_t b = b0; b < b1; ++b) {
             a.plan[b] = sum;
-            sum += (tree_length(a, b) + KB - 1) / KB * a.kv_heads;
+            sum += (tree_length(a, b) + kTreeRound - 1) / kTreeRound * a.kv_heads + extra;
         }
         if (tid == 0) {
             a.plan[a.batch] = total;
             a.plan[a.batch + 1] = stretch;
+            a.plan[a.batch + 2] = extra / a.kv_heads;
         }
     }
     if (from >= before && from < before + mine) {
         int32_t sum = before, b = b0;
         while (true) {
-            const int32_t n = (tree_length(a, b) + KB - 1) / KB * a.kv_heads;
+            const int32_t n = (tree_length(a, b) + kTreeRound - 1) / kTreeRound * a.kv_heads + extra;
             if (from < sum + n) break;
             sum += n;
             ++b;
@@ -982,17 +618,16 @@ __device__ __forceinline__ TreeStart tree_start(const TreeArgs& a, int32_t group
         s_found[1] = (int32_t)(from - sum);
     }
     __syncthreads();
-    return TreeStart{total, stretch, s_found[0], s_found[1]};
+    return TreeStart{total, stretch, extra / a.kv_heads, s_found[0], s_found[1]};
 }
 
 constexpr double kTreePastCaches = 128e6;  // bytes of keys and values from which they are read past the caches
 
-template <int DT, int D, bool TILES, int MT>
+template <int DT, int D, int MT>
 __global__ __launch_bounds__(kAttnThreads, D == 256 ? 1 : 2) void tree_part_kernel(TreeArgs a)
 {
-    constexpr int ROWS = MT * 16 * (TILES ? kAttnWaves : 1);
-    constexpr int KB = kTreeRound<TILES>;
-    constexpr size_t kLds = TILES ? (size_t)TreeTile<D>::LDS : tree_rows_lds<D, MT>();
+    constexpr int ROWS = MT * 16 * kAttnWaves, KB = kTreeRound;
+    constexpr size_t kLds = TreeTile<D>::LDS;
     // The stretches count on two workgroups per CU: more than a third of the 160 KB keeps a third one out.
     constexpr size_t kLdsOfTwo = 52 * 1024, kMem = D != 256 && kLds < kLdsOfTwo ? kLdsOfTwo : kLds;
     __shared__ __align__(16) char s_mem[kMem];
@@ -1003,7 +638,7 @@ __global__ __launch_bounds__(kAttnThreads, D == 256 ? 1 : 2) void tree_part_kern
     const int32_t group = a.tiles == 1 ? (int32_t)blockIdx.x : (int32_t)(y / (uint32_t)a.tiles * 8u + x);
     const int32_t tile = a.tiles == 1 ? 0 : (int32_t)(y % (uint32_t)a.tiles);
     if (group >= a.groups) return;
-    const TreeStart start = tree_start<KB>(a, group, group == 0 && tile == 0, s_sum, s_found);
+    const TreeStart start = tree_start(a, group, group == 0 && tile == 0, s_sum, s_found);
     int64_t at = (int64_t)group * start.stretch;
     if (at >= start.total) return;
     const int64_t end = min(at + start.stretch, (int64_t)start.total);
@@ -1012,14 +647,14 @@ __global__ __launch_bounds__(kAttnThreads, D == 256 ? 1 : 2) void tree_part_kern
     int32_t in = __builtin_amdgcn_readfirstlane(start.at);  // rounds of sequence b before `at`
     bool first = true;
     while (at < end) {
-        const int32_t len = __builtin_amdgcn_readfirstlane(tree_length(a, b)), n = (len + KB - 1) / KB;
-        if (in >= n * a.kv_heads) {  // (also the empty sequences)
-            in -= n * a.kv_heads;
+        const int32_t len = __builtin_amdgcn_readfirstlane(tree_length(a, b)), n = (len + KB - 1) / KB, pair = n + start.extra;
+        if (in >= pair * a.kv_heads) {  // (also the empty sequences)
+            in -= pair * a.kv_heads;
             ++b;
             continue;
         }
-        const int32_t hk = in / n, j = in - hk * n;
-        const int32_t take = (int32_t)min((int64_t)(n - j), end - at);
+        const int32_t hk = in / pair, j = in - hk * pair;
+        const int32_t step = (int32_t)min((int64_t)(pair - j), end - at), take = min(step, n - j);
         Stretch st;
         st.b = b;
         st.hk = hk;
@@ -1035,72 +670,93 @@ __global__ __launch_bounds__(kAttnThreads, D == 256 ? 1 : 2) void tree_part_kern
         st.table = a.table != nullptr ? a.table + (int64_t)b * a.table_stride : nullptr;
         st.parents = a.parents != nullptr ? a.parents + (st.row0 - b) : nullptr;
         st.past = past;
-        if (tile * ROWS < st.nrows * a.rep) {
-            const int32_t t0 = tile * ROWS / a.rep;
+        if (take > 0 && tile * ROWS < st.nrows * a.rep) {
             __syncthreads();  // (the stretch before this one is done with the LDS)
-            if (st.end > st.context) tree_views(st, t0, min(st.nrows, ((tile + 1) * ROWS - 1) / a.rep + 1) - t0, s_up, s_view);
             const TreeOut to{j == 0 && take == n, ((int64_t)group * 2 + (first ? 0 : 1)) * a.tiles + tile};
-            if constexpr (TILES) attend_tree_tiles<DT, D, MT>(a, st, tile, to, s_view, &s_wild, s_mem);
-            else attend_rows<DT, D, MT>(a, st, tile, to, s_view, (float*)s_mem);
+            attend_tree_tiles<DT, D, MT>(a, st, tile, to, s_up, s_view, &s_wild, s_mem);
         }
-        at += take;
-        in += take;
+        at += step;
+        in += step;
         first = false;
     }
 }
 
-// Join of the parts: one wave per (row, head), D / 4 lanes over the columns of a part and kWave / (D / 4) parts side by
-// side.  A pair that one workgroup finished is left alone; rows that see nothing get zeros.
-template <int DT, int D, int ROWS>
+// Join of the parts: D / 4 lanes over the columns of a (row, head), whose parts come in batches that are on their way at
+// once.  With few rows (SPLIT) the wave's other lanes take parts of the same row, with many another row each.  A pair
+// that one workgroup finished is left alone; rows that see nothing get zeros.
+template <int DT, int D, int ROWS, bool SPLIT>
 __global__ __launch_bounds__(kThreads) void tree_join_kernel(TreeArgs a)
 {
-    constexpr int LPP = D / 4;        // lanes per part
-    constexpr int PPR = kWave / LPP;  // parts per round
-    const int64_t i = (int64_t)blockIdx.x * kWaves + wave_id();
-    const int32_t heads = a.q_heads;
-    const int64_t ik = i / heads;
-    const int32_t h = (int32_t)(i - ik * heads), b = (int32_t)(ik / (a.kmax + 1)), k = (int32_t)(ik - (int64_t)b * (a.kmax + 1));
+    constexpr int LPP = D / 4;                        // lanes per part
+    constexpr int PPR = SPLIT ? kWave / LPP : 1;      // parts side by side
+    constexpr int PER = kWave / LPP / PPR;            // rows per wave
+    const int lane = lane_id(), col = (lane % LPP) * 4, sub = SPLIT ? lane / LPP : 0;
+    const int32_t i = ((int32_t)blockIdx.x * kWaves + wave_id()) * PER + (SPLIT ? 0 : lane / LPP);
+    const int32_t heads = a.q_heads, ik = i / heads, h = i - ik * heads, b = ik / (a.kmax + 1), k = ik - b * (a.kmax + 1);
     if (b >= a.batch) return;
     const int32_t row0 = tree_row(a, b), nrows = min(tree_row(a, b + 1) - row0, a.kmax + 1);
+    const int32_t begin = a.plan[b], pair = (a.plan[b + 1] - begin) / a.kv_heads, stretch = a.plan[a.batch + 1];
+    const int32_t rounds = pair - a.plan[a.batch + 2];
     if (k >= nrows) return;
-    const int32_t begin = a.plan[b], rounds = (a.plan[b + 1] - begin) / a.kv_heads, stretch = a.plan[a.batch + 1];
     const int32_t hk = h / a.rep, r = k * a.rep + (h - hk * a.rep), tile = r / ROWS;
-    const int32_t from = begin + hk * rounds;
+    const int32_t from = begin + hk * pair;
     const int32_t g0 = from / stretch, parts = rounds > 0 ? (from + rounds - 1) / stretch - g0 + 1 : 0;
     if (parts == 1) return;
-    const int lane = lane_id(), col = (lane % LPP) * 4, sub = lane / LPP;
     // the first part lies in its workgroup's second place if the workgroup began with another pair
     auto place = [&](int32_t p) {
         const int64_t slot = (int64_t)(g0 + p) * 2 + (p == 0 && from != g0 * stretch ? 1 : 0);
         return (slot * a.tiles + tile) * ROWS + (r - tile * ROWS);
     };
-    float m = kNoReference;
-    for (int32_t p = lane; p < parts; p += kWave) m = fmaxf(m, a.ml[place(p)].x);
-    m = wave_max_dpp(m);
-    float l = 0.0f;
+    float m = kNoReference, l = 0.0f;
     f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 4
-    for (int32_t p = sub; p < parts; p += PPR) {
-        const int64_t at = place(p);
-        const float2 ml = a.ml[at];
-        const f32x4 v = *(const SV_GLOBAL f32x4*)(a.acc + at * D + col);
-        if (ml.y == 0.0f) continue;  // nothing in this part (l is NaN where a row sees a NaN)
-        const float w = __builtin_amdgcn_exp2f(ml.x - m);
-        l += ml.y * w;
+    auto batch = [&](int32_t p0, auto most) {
+        constexpr int N = decltype(most)::value;
+        float2 ml[N];
+        f32x4 v[N];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o[e] += v[e] * w;
-    }
+        for (int j = 0; j < N; ++j) {
+            const int64_t at = place(min(p0 + j * PPR + sub, parts - 1));
+            ml[j] = a.ml[at];
+            v[j] = *(const SV_GLOBAL f32x4*)(a.acc + at * D + col);
+            if (p0 + j * PPR + sub >= parts) ml[j] = float2{kNoReference, 0.0f};
+        }
+        float top = m;
 #pragma unroll
-    for (int x = LPP; x < kWave; x <<= 1) {
+        for (int j = 0; j < N; ++j) top = fmaxf(top, ml[j].x);
+        const float f = __builtin_amdgcn_exp2f(m - top);
+        m = top;
+        l *= f;
+        o *= f;
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            if (ml[j].y == 0.0f) continue;  // nothing in this part (l is NaN where a row sees a NaN)
+            const float w = __builtin_amdgcn_exp2f(ml[j].x - m);
+            l += ml[j].y * w;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[e] += v[j][e] * w;
+        }
+    };
+    if (parts <= 2 * PPR) batch(0, std::integral_constant<int, 2>{});
+    else if (parts <= 4 * PPR) batch(0, std::integral_constant<int, 4>{});
+    else
+        for (int32_t p0 = 0; p0 < parts; p0 += 8 * PPR) batch(p0, std::integral_constant<int, 8>{});
+#pragma unroll
+    for (int x = LPP; x < LPP * PPR; x <<= 1) {
+        const float top = fmaxf(m, __shfl_xor(m, x, kWave)), f = __builtin_amdgcn_exp2f(m - top);
+        m = top;
+        l *= f;
         l += __shfl_xor(l, x, kWave);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o[e] += __shfl_xor(o[e], x, kWave);
+        for (int e = 0; e < 4; ++e) {
+            o[e] *= f;
+            o[e] += __shfl_xor(o[e], x, kWave);
+        }
     }
     if (sub != 0) return;
     const float inv = l != 0.0f ? 1.0f / l : 0.0f;
     store4<DT>(a.out + (int64_t)(row0 + k) * a.out_row + (int64_t)h * a.out_head + col * 2, o.x * inv, o.y * inv, o.z * inv,
                o.w * inv);
-    if (a.lse != nullptr && lane == 0)
+    if (a.lse != nullptr && col == 0)
         a.lse[(int64_t)(row0 + k) * heads + h] =
             l != 0.0f ? (m + __builtin_amdgcn_logf(l)) * 0.69314718055994531f : neg_inf();
 }

@@ -143,9 +143,11 @@ sv_status_t adjust_logits_common(const sv_adjust_shape_t* sh, const sv_adjust_t*
 // Workgroups that the line of keys is dealt to: two per CU, one where the registers hold no second one.
 constexpr int32_t kTreeGroups = 512;
 constexpr int32_t kTreeGroupsWide = 256;
+// (Row, head)s from which each has D / 4 lanes of a join, not a wave: one row of 32 heads on 32001 positions 40 us with
+// D / 4 lanes, 35 with the wave; 48 ragged trees of up to 9 rows 167 and 168, 64 of 8 rows and 64 columns 95 and 99.
+constexpr int64_t kJoinSplit = 4096;
 
 struct TreePlan {
-    bool tiles;
     int32_t mt, wg_rows, row_tiles, groups, rows, capacity;
     int64_t grid, join;
     size_t off_plan, off_ml, off_acc, bytes;
@@ -159,19 +161,17 @@ TreePlan tree_plan(const sv_tree_shape_t* sh)
     const int32_t rep = sh->q_heads / sh->kv_heads;
     const int64_t rows = (int64_t)(sh->max_draft + 1) * rep;  // of one key head
     const int32_t most = sh->head_dim == 256 ? 1 : 2;         // 16-row tiles per wave that the registers hold
-    p.tiles = rows > most * 16;
-    p.mt = p.tiles ? (rows <= sv::kAttnWaves * 16 ? 1 : most) : rows <= 16 ? 1 : most;
-    p.wg_rows = p.mt * 16 * (p.tiles ? sv::kAttnWaves : 1);
+    p.mt = rows <= sv::kAttnWaves * 16 ? 1 : most;
+    p.wg_rows = p.mt * 16 * sv::kAttnWaves;
     p.row_tiles = (int32_t)((rows + p.wg_rows - 1) / p.wg_rows);
-    const int32_t kb = p.tiles ? sv::kTreeRound<true> : sv::kTreeRound<false>;
-    const int64_t rounds = (int64_t)sh->batch * sh->kv_heads * (((int64_t)p.capacity + kb - 1) / kb);
+    const int64_t rounds = (int64_t)sh->batch * sh->kv_heads * (((int64_t)p.capacity + sv::kTreeRound - 1) / sv::kTreeRound);
     const int64_t target = std::max((sh->head_dim == 256 ? kTreeGroupsWide : kTreeGroups) / p.row_tiles, 1);
     p.groups = (int32_t)std::min(target, rounds);
     p.grid = p.row_tiles == 1 ? p.groups : (int64_t)(p.groups + 7) / 8 * 8 * p.row_tiles;
     p.join = (int64_t)sh->batch * (sh->max_draft + 1) * sh->q_heads;
     const size_t slots = 2 * (size_t)p.groups * (size_t)p.row_tiles * (size_t)p.wg_rows;
     p.off_plan = 0;
-    p.off_ml = align_up((size_t)(sh->batch + 2) * 4);
+    p.off_ml = align_up((size_t)(sh->batch + 3) * 4);
     p.off_acc = align_up(p.off_ml + slots * sizeof(float2));
     p.bytes = align_up(p.off_acc + slots * (size_t)sh->head_dim * sizeof(float));
     return p;
@@ -202,7 +202,7 @@ sv_status_t check_tree(const sv_tree_shape_t* sh, float scale)
         return SV_ERR_UNSUPPORTED;
     if (((int64_t)sh->total_draft + sh->batch) * sh->q_heads > INT32_MAX / 2) return SV_ERR_UNSUPPORTED;
     if ((int64_t)(sh->q_heads / sh->kv_heads) * (sh->max_draft + 1) > INT32_MAX / 256) return SV_ERR_UNSUPPORTED;
-    if ((double)sh->batch * sh->kv_heads * ((double)sh->max_pages * sh->page_size / 64 + 1) > (double)INT32_MAX)
+    if ((double)sh->batch * sh->kv_heads * ((double)sh->max_pages * sh->page_size / sv::kTreeRound + 1 + sv::kTreeExtra) > (double)INT32_MAX)
         return SV_ERR_UNSUPPORTED;
     if (sh->table_stride > INT64_MAX / 8 / sh->batch) return SV_ERR_UNSUPPORTED;
     const TreePlan p = tree_plan(sh);
@@ -211,14 +211,20 @@ sv_status_t check_tree(const sv_tree_shape_t* sh, float scale)
     return SV_OK;
 }
 
-template <int DT, int D, bool TILES, int MT>
+template <int DT, int D, int MT>
 sv_status_t run_tree(const TreePlan& p, const sv::TreeArgs& a, hipStream_t stream, const sv_profile_events_t* prof)
 {
-    launch_stream_nt(prof, sv::tree_part_kernel<DT, D, TILES, MT>, (uint32_t)p.grid, sv::kAttnThreads, stream, a);
+    launch_stream_nt(prof, sv::tree_part_kernel<DT, D, MT>, (uint32_t)p.grid, sv::kAttnThreads, stream, a);
     if (launch_status() != SV_OK) return SV_ERR_HIP;
-    constexpr int ROWS = MT * 16 * (TILES ? sv::kAttnWaves : 1);
-    hipLaunchKernelGGL((sv::tree_join_kernel<DT, D, ROWS>), dim3((uint32_t)((p.join + sv::kWaves - 1) / sv::kWaves)),
-                       dim3(sv::kThreads), 0, stream, a);
+    constexpr int ROWS = MT * 16 * sv::kAttnWaves;
+    const auto join = [&](auto split) {
+        constexpr bool SPLIT = decltype(split)::value;
+        const int64_t per = sv::kWaves * (SPLIT ? 1 : sv::kWave / (D / 4));  // (row, head)s of a workgroup
+        hipLaunchKernelGGL((sv::tree_join_kernel<DT, D, ROWS, SPLIT>), dim3((uint32_t)((p.join + per - 1) / per)),
+                           dim3(sv::kThreads), 0, stream, a);
+    };
+    if (D == 256 || p.join < kJoinSplit) join(std::true_type{});
+    else if constexpr (D != 256) join(std::false_type{});
     return launch_status();
 }
 
@@ -292,13 +298,10 @@ sv_status_t tree_attention_common(const sv_tree_shape_t* sh, const void* q, cons
         constexpr int DT = decltype(dt)::value, D = decltype(dim)::value;
         if constexpr (DT == sv::DT_F32) {
             return SV_ERR_UNSUPPORTED;
-        } else if constexpr (D == 256) {
-            return p.tiles ? run_tree<DT, D, true, 1>(p, a, stream, prof) : run_tree<DT, D, false, 1>(p, a, stream, prof);
         } else {
-            if (p.tiles && p.mt == 2) return run_tree<DT, D, true, 2>(p, a, stream, prof);
-            if (p.tiles) return run_tree<DT, D, true, 1>(p, a, stream, prof);
-            if (p.mt == 2) return run_tree<DT, D, false, 2>(p, a, stream, prof);
-            return run_tree<DT, D, false, 1>(p, a, stream, prof);
+            if constexpr (D != 256)
+                if (p.mt == 2) return run_tree<DT, D, 2>(p, a, stream, prof);
+            return run_tree<DT, D, 1>(p, a, stream, prof);
         }
     };
     return by_dtype(sh->dtype, [&](auto dt) -> sv_status_t {
