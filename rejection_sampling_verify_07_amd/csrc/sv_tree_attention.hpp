@@ -397,7 +397,6 @@ __device__ __forceinline__ void attend_tree_tiles(const TreeArgs& a, const Stret
         };
         f32x4 s[SUBS][2][MT];
         read_values(0);
-        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int i = 0; i < 2 * SUBS; ++i)
 #pragma unroll
@@ -409,6 +408,9 @@ __device__ __forceinline__ void attend_tree_tiles(const TreeArgs& a, const Stret
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt)
                     s[i / 2][i & 1][mt] = mfma_16x16x32<DT>(kf[i][c], qf[mt][c], s[i / 2][i & 1][mt]);
+        // The wave that is past its products goes first, so that one wave of a SIMD multiplies while the other one takes
+        // exponentials (16 trees of 64 rows on 9000 positions: 255 us without, 247 with; fewer rows wait for memory).
+        if constexpr (MT == 2) __builtin_amdgcn_s_setprio(1);
         if (more) read_keys((buf + 1) % TA::BUFS);
         if (masked) {
 #pragma unroll
@@ -471,6 +473,7 @@ __device__ __forceinline__ void attend_tree_tiles(const TreeArgs& a, const Stret
 #pragma unroll
                 for (int i = 0; i < 4; ++i) pf[mt][i] = pack2<DT>(p[2 * i], p[2 * i + 1]);
             }
+            if constexpr (MT == 2) __builtin_amdgcn_s_setprio(0);
 #pragma unroll
             for (int d = 0; d < DT16; ++d)
 #pragma unroll
