@@ -114,10 +114,11 @@ sv_status_t cache_compact_common(const sv_compact_shape_t* sh, void* data, const
     return launch_status();
 }
 
-// Table entries, old and new, that one workgroup counts.
+// Table entries, old and new, that one workgroup counts, in LDS: 4 places 7.7 us, 13.4 with the launches for any size, 64
+// places of 17 pages 22 and 28.
 constexpr int64_t kForkSmall = 1 << 16;
-// Workgroups that copy for one place, at most.
-constexpr int64_t kForkTiles = 64;
+// Workgroups that copy for one place, at most: 64 places of 64 caches 21.4 us with 256, 22.0 with 64, 26.3 with 16.
+constexpr int64_t kForkTiles = 256;
 
 struct ForkPlan {
     size_t off_places, off_first, off_fresh, off_left, bytes;

@@ -116,8 +116,7 @@ __device__ __forceinline__ float edited(float x, uint32_t entry, const Penalty& 
     return x;
 }
 
-// ROWS: rows of the first pass that are in flight together.
-template <int DT, bool INPLACE, int BIAS, int CT, int NT, int ROWS>
+template <int DT, bool INPLACE, int BIAS, int CT, int NT>
 __global__ __launch_bounds__(NT) void adjust_kernel(AdjustArgs a)
 {
     typedef typename RowVec<DT>::type Vec;
@@ -273,65 +272,54 @@ __global__ __launch_bounds__(NT) void adjust_kernel(AdjustArgs a)
     __syncthreads();  // (the list, and the masks' numbers)
 
     if (!INPLACE || a.masks != nullptr) {
-        for (int32_t rb = r0; rb < r1; rb += ROWS) {
-            uint32_t allowed[ROWS][NV];
-            u32x4 raw[ROWS][NV];
-            const int64_t first = (int64_t)k0 + b + rb;
+        for (int32_t r = r0; r < r1; ++r) {
+            const bool masked = a.masks != nullptr && s_mask[r - r0] >= 0;
+            if (INPLACE && !masked) continue;
+            const int64_t at = (int64_t)k0 + b + r;
+            const char* in = a.in + at * a.in_stride + (int64_t)lo * ES;
+            char* out = a.out + at * a.out_stride + (int64_t)lo * ES;
+            uint32_t allowed[NV];
+            u32x4 raw[NV];
 #pragma unroll
-            for (int y = 0; y < ROWS; ++y) {
-                const bool masked = a.masks != nullptr && rb + y < r1 && s_mask[rb + y - r0] >= 0;
-                const SV_GLOBAL uint8_t* mask = masked ? mask_of(rb + y - r0) : nullptr;
-#pragma unroll
-                for (int i = 0; i < NV; ++i) {
-                    const int32_t e = (i * NT + tid) * VEC;
-                    allowed[y][i] = mask != nullptr && e < width ? mask[e / 8] : FULL << (VEC == 8 ? 0 : e % 8);
-                }
+            for (int i = 0; i < NV; ++i) {
+                const int32_t e = (i * NT + tid) * VEC;
+                allowed[i] = masked && e < width ? mask_of(r - r0)[e / 8] : 255u;
             }
 #pragma unroll
-            for (int y = 0; y < ROWS; ++y) {
-                const char* in = a.in + (first + y) * a.in_stride + (int64_t)lo * ES;
-#pragma unroll
-                for (int i = 0; i < NV; ++i) {
-                    const int32_t e = (i * NT + tid) * VEC;
-                    allowed[y][i] = allowed[y][i] >> (VEC == 8 ? 0 : e % 8) & FULL;
-                    raw[y][i] = u32x4{0u, 0u, 0u, 0u};
-                    if (rb + y < r1 && e + VEC <= width && allowed[y][i] != 0 && (!INPLACE || allowed[y][i] != FULL))
-                        raw[y][i] = *(const SV_GLOBAL Vec*)(in + (int64_t)e * ES);
-                }
+            for (int i = 0; i < NV; ++i) {
+                const int32_t e = (i * NT + tid) * VEC;
+                allowed[i] = allowed[i] >> (VEC == 8 ? 0 : e % 8) & FULL;
+                raw[i] = u32x4{0u, 0u, 0u, 0u};
+                if (e + VEC <= width && allowed[i] != 0 && (!INPLACE || allowed[i] != FULL))
+                    raw[i] = *(const SV_GLOBAL Vec*)(in + (int64_t)e * ES);
             }
 #pragma unroll
-            for (int y = 0; y < ROWS; ++y) {
-                if (rb + y >= r1) break;
-                const char* in = a.in + (first + y) * a.in_stride + (int64_t)lo * ES;
-                char* out = a.out + (first + y) * a.out_stride + (int64_t)lo * ES;
+            for (int i = 0; i < NV; ++i) {
+                const int32_t e = (i * NT + tid) * VEC;
+                const uint32_t may = allowed[i];
+                if (e >= width || (INPLACE && may == FULL)) continue;
+                if (e + VEC <= width) {
+                    u32x4 v = raw[i];
 #pragma unroll
-                for (int i = 0; i < NV; ++i) {
-                    const int32_t e = (i * NT + tid) * VEC;
-                    const uint32_t may = allowed[y][i];
-                    if (e >= width || (INPLACE && may == FULL)) continue;
-                    if (e + VEC <= width) {
-                        u32x4 v = raw[y][i];
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            if constexpr (ES == 4) {
-                                if ((may >> q & 1u) == 0) v[q] = 0xff800000u;
-                            } else {
-                                const uint32_t drop = (may >> (2 * q) & 1u ? 0u : 0xffffu) |
-                                                      (may >> (2 * q + 1) & 1u ? 0u : 0xffff0000u);
-                                v[q] = (v[q] & ~drop) | (Dt<DT>::kNegInf * 0x10001u & drop);
-                            }
+                    for (int q = 0; q < 4; ++q) {
+                        if constexpr (ES == 4) {
+                            if ((may >> q & 1u) == 0) v[q] = 0xff800000u;
+                        } else {
+                            const uint32_t drop = (may >> (2 * q) & 1u ? 0u : 0xffffu) |
+                                                  (may >> (2 * q + 1) & 1u ? 0u : 0xffff0000u);
+                            v[q] = (v[q] & ~drop) | (Dt<DT>::kNegInf * 0x10001u & drop);
                         }
-                        *(SV_GLOBAL Vec*)(out + (int64_t)e * ES) = v;
-                    } else {  // the vocabulary ends in this vector
+                    }
+                    *(SV_GLOBAL Vec*)(out + (int64_t)e * ES) = v;
+                } else {  // the vocabulary ends in this vector
 #pragma unroll 1
-                        for (int x = 0; e + x < width; ++x) {
-                            if constexpr (ES == 4)
-                                ((SV_GLOBAL uint32_t*)out)[e + x] =
-                                    may >> x & 1u ? ((const SV_GLOBAL uint32_t*)in)[e + x] : 0xff800000u;
-                            else
-                                ((SV_GLOBAL uint16_t*)out)[e + x] =
-                                    may >> x & 1u ? ((const SV_GLOBAL uint16_t*)in)[e + x] : (uint16_t)Dt<DT>::kNegInf;
-                        }
+                    for (int x = 0; e + x < width; ++x) {
+                        if constexpr (ES == 4)
+                            ((SV_GLOBAL uint32_t*)out)[e + x] =
+                                may >> x & 1u ? ((const SV_GLOBAL uint32_t*)in)[e + x] : 0xff800000u;
+                        else
+                            ((SV_GLOBAL uint16_t*)out)[e + x] =
+                                may >> x & 1u ? ((const SV_GLOBAL uint16_t*)in)[e + x] : (uint16_t)Dt<DT>::kNegInf;
                     }
                 }
             }
@@ -340,11 +328,11 @@ __global__ __launch_bounds__(NT) void adjust_kernel(AdjustArgs a)
     if (!edits) return;
     if (!INPLACE || a.masks != nullptr) __syncthreads();  // (the first pass's stores, which share vectors with the second's)
     const int32_t n = s_listed, all = n * (r1 - r0);
-        constexpr int kItems = 4;  // elements in flight per thread
+    constexpr int kItems = 4;  // elements in flight per thread
     for (int32_t it0 = tid; it0 < all; it0 += kItems * NT) {
         float x[kItems];
         uint32_t token[kItems], may[kItems];  // UINT32_MAX: none, or masked; the mask's byte
-        int32_t at[kItems];      // the row's place in the run
+        int32_t at[kItems];                   // the row's place in the run
         bool guess[kItems];
 #pragma unroll
         for (int j = 0; j < kItems; ++j) {

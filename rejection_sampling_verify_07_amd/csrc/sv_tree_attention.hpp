@@ -76,7 +76,6 @@ struct Stretch {
     int32_t total;           // positions of the sequence
     int32_t pages;           // pages that they take
     int32_t context;         // those before the newest rows (below 0 if the newest rows are not all there)
-    bool past;               // read past the caches
 };
 
 // The page of grain g, for the few that are looked up one by one (-1: none; keys at or past `total` have none).
@@ -289,6 +288,8 @@ __device__ __forceinline__ void attend_tree_tiles(const TreeArgs& a, const Stret
     int32_t bad_from = INT32_MAX;             // the first tile met that has a grain without a page
     uint32_t there = 0;                       // four bits per buffer: the grains of its tile that have pages
     walk.start(a, st, kb);
+    // `past`: where no other row tile reads the same keys they go past the caches (48 ragged trees on up to 8000 positions:
+    // 169 us, 194 through them; nothing was slower).
     auto load_tile = [&](int buf, auto past) {
         const uint32_t dst = lds_address(s_kv) + (uint32_t)(buf * (2 * TA::TILE) + wave * (kWave * 16));
         const bool edge = ahead + KT > st.total;
@@ -323,7 +324,7 @@ __device__ __forceinline__ void attend_tree_tiles(const TreeArgs& a, const Stret
         ahead += KT;
     };
     auto load_next = [&](int buf) {
-        if (ahead < st.end) with_policy(st.past, [&](auto past) { load_tile(buf, past); });
+        if (ahead < st.end) with_policy(a.tiles == 1, [&](auto past) { load_tile(buf, past); });
     };
     // No value for keys past the last one or without a page; one that is not finite counts as 0 here (times the weight 0
     // of a row that does not see it, it would be NaN) and reaches the rows that see it at the end.
@@ -624,8 +625,6 @@ __device__ __forceinline__ TreeStart tree_start(const TreeArgs& a, int32_t group
     return TreeStart{total, stretch, extra / a.kv_heads, s_found[0], s_found[1]};
 }
 
-constexpr double kTreePastCaches = 128e6;  // bytes of keys and values from which they are read past the caches
-
 template <int DT, int D, int MT>
 __global__ __launch_bounds__(kAttnThreads, D == 256 ? 1 : 2) void tree_part_kernel(TreeArgs a)
 {
@@ -645,7 +644,6 @@ __global__ __launch_bounds__(kAttnThreads, D == 256 ? 1 : 2) void tree_part_kern
     int64_t at = (int64_t)group * start.stretch;
     if (at >= start.total) return;
     const int64_t end = min(at + start.stretch, (int64_t)start.total);
-    const bool past = a.tiles == 1 && (double)start.total * (KB * D * 4.0) > kTreePastCaches;
     int32_t b = __builtin_amdgcn_readfirstlane(start.b);
     int32_t in = __builtin_amdgcn_readfirstlane(start.at);  // rounds of sequence b before `at`
     bool first = true;
@@ -672,7 +670,6 @@ __global__ __launch_bounds__(kAttnThreads, D == 256 ? 1 : 2) void tree_part_kern
         st.v = a.v + (int64_t)hk * a.v_head;
         st.table = a.table != nullptr ? a.table + (int64_t)b * a.table_stride : nullptr;
         st.parents = a.parents != nullptr ? a.parents + (st.row0 - b) : nullptr;
-        st.past = past;
         if (take > 0 && tile * ROWS < st.nrows * a.rep) {
             __syncthreads();  // (the stretch before this one is done with the LDS)
             const TreeOut to{j == 0 && take == n, ((int64_t)group * 2 + (first ? 0 : 1)) * a.tiles + tile};

@@ -23,17 +23,14 @@ constexpr int32_t kMaxTokens = 1 << 30;
 // ---- edits of logits
 
 // Threads of a workgroup, of 8 tokens of the vocabulary each.  320 rows of 151936 bf16 logits with texts of up to 8000
-// tokens: 46 us with 512, 45 with 1024, 51 with 256; with smaller tables in LDS more workgroups stay on a CU, with larger
-// ones fewer of them read the texts.  Calls of few workgroups take 256: one row of 50304 fp32 logits 5.5 us, 7.5 with
-// 1024 threads.
+// tokens: 46 us with 512, 45 with 1024, 51 with 256; one row of 50304 fp32 logits 4.9 us, 5.1 with 256, 7.5 with 1024.
+// (With smaller tables in LDS more workgroups stay on a CU, with larger ones fewer of them read the texts.)
 constexpr int kAdjustThreads = 512;
-constexpr int kAdjustThreadsFew = 256;
 constexpr int kAdjustTokens = 8;
-constexpr int64_t kAdjustFew = 256;  // workgroups below which the rows of a call count as few
-constexpr int kAdjustRows = 4;       // rows in flight together
 // Bias entries that a table of 16 bits can number.
 constexpr int32_t kAdjustFewBiases = 65535;
-// Workgroups that the rows of a sequence are divided for.
+// Workgroups that the rows of a sequence are divided for: each counts the text anew.  One sequence of 65 rows of 151936
+// fp32 logits under masks: 30 us with 256, 29.5 with 1024, 48 with 4096; 4 of 9 bf16 rows 12.8, 11.5 and 16.2.
 constexpr int64_t kAdjustGroups = 1024;
 
 sv_status_t check_adjust(const sv_adjust_shape_t* sh, const sv_adjust_t* ad, const void* logits, const void* out)
@@ -110,29 +107,23 @@ sv_status_t adjust_logits_common(const sv_adjust_shape_t* sh, const sv_adjust_t*
     a.num_masks = ad->num_masks;
     a.mask_rows = ad->mask_rows;
     const int64_t rows = sh->max_draft + 1;
-    const auto launch = [&](auto dt, auto inplace, auto bias, auto threads) -> sv_status_t {
-        constexpr int DT = decltype(dt)::value, NT = decltype(threads)::value, CT = NT * kAdjustTokens;
+    const auto launch = [&](auto dt, auto inplace, auto bias) -> sv_status_t {
+        constexpr int DT = decltype(dt)::value, NT = kAdjustThreads, CT = NT * kAdjustTokens;
         a.nchunk = (sh->vocab + CT - 1) / CT;
         const int64_t one = (int64_t)sh->batch * a.nchunk;
         const int64_t runs = std::min(std::max<int64_t>(kAdjustGroups / one, 1), rows);
         a.run_rows = (int32_t)((rows + runs - 1) / runs);
         a.runs = (int32_t)((rows + a.run_rows - 1) / a.run_rows);
         if (!launchable((double)one * a.runs, NT)) return SV_ERR_UNSUPPORTED;
-        launch_stream_nt(prof, sv::adjust_kernel<DT, decltype(inplace)::value, decltype(bias)::value, CT, NT, kAdjustRows>,
+        launch_stream_nt(prof, sv::adjust_kernel<DT, decltype(inplace)::value, decltype(bias)::value, CT, NT>,
                          (uint32_t)(one * a.runs), NT, stream, a);
         return launch_status();
     };
-    const bool few =
-        (int64_t)sh->batch * rows * (sh->vocab / (kAdjustThreads * kAdjustTokens) + 1) < kAdjustFew;
     return by_dtype(sh->dtype, [&](auto dt) {
-        const auto by_size = [&](auto inplace, auto bias) {
-            return few ? launch(dt, inplace, bias, std::integral_constant<int, kAdjustThreadsFew>{})
-                       : launch(dt, inplace, bias, std::integral_constant<int, kAdjustThreads>{});
-        };
         const auto by_bias = [&](auto inplace) {
-            if (a.total_bias == 0) return by_size(inplace, std::integral_constant<int, sv::BIAS_NONE>{});
-            if (a.total_bias <= kAdjustFewBiases) return by_size(inplace, std::integral_constant<int, sv::BIAS_16>{});
-            return by_size(inplace, std::integral_constant<int, sv::BIAS_32>{});
+            if (a.total_bias == 0) return launch(dt, inplace, std::integral_constant<int, sv::BIAS_NONE>{});
+            if (a.total_bias <= kAdjustFewBiases) return launch(dt, inplace, std::integral_constant<int, sv::BIAS_16>{});
+            return launch(dt, inplace, std::integral_constant<int, sv::BIAS_32>{});
         };
         return logits == out ? by_bias(std::true_type{}) : by_bias(std::false_type{});
     });
@@ -140,7 +131,8 @@ sv_status_t adjust_logits_common(const sv_adjust_shape_t* sh, const sv_adjust_t*
 
 // ---- attention over paged caches
 
-// Workgroups that the line of keys is dealt to: two per CU, one where the registers hold no second one.
+// Workgroups that the line of keys is dealt to: two per CU, one where LDS and registers hold no second one.  (48 ragged
+// trees on 1000 to 8000 positions: 169 us with 512, 214 with 256, 178 with 1024.)
 constexpr int32_t kTreeGroups = 512;
 constexpr int32_t kTreeGroupsWide = 256;
 // (Row, head)s from which each has D / 4 lanes of a join, not a wave: one row of 32 heads on 32001 positions 40 us with
@@ -160,7 +152,9 @@ TreePlan tree_plan(const sv_tree_shape_t* sh)
     p.capacity = sh->max_pages * sh->page_size;
     const int32_t rep = sh->q_heads / sh->kv_heads;
     const int64_t rows = (int64_t)(sh->max_draft + 1) * rep;  // of one key head
-    const int32_t most = sh->head_dim == 256 ? 1 : 2;         // 16-row tiles per wave that the registers hold
+    // 16-row tiles per wave: two where 64 rows do not do (and the registers hold them).  48 ragged trees of up to 36 rows a
+    // key head: 169 us with one, 175 with two.
+    const int32_t most = sh->head_dim == 256 ? 1 : 2;
     p.mt = rows <= sv::kAttnWaves * 16 ? 1 : most;
     p.wg_rows = p.mt * 16 * sv::kAttnWaves;
     p.row_tiles = (int32_t)((rows + p.wg_rows - 1) / p.wg_rows);
