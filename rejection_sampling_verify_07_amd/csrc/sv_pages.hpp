@@ -2,7 +2,9 @@
 // tables of sequences that continue others (fork).
 //
 // Both move bytes and are bound by HBM where there are many, by their launches
-// where there are few.
+// where there are few.  compact: 64 sequences of up to 8 taken rows, 64 caches of rows
+// of 2 KB, 66 MB read and written: 14 us, 4.7 TB/s; one sequence 4.8 us.  fork: 64 places
+// on 859 pages, 89 MB: 24 us (plan 5.6, copies 17 at 5.2 TB/s); 4 places 8.3 us.
 #pragma once
 
 #include "sv_common.hpp"

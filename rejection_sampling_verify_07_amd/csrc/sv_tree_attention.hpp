@@ -8,15 +8,28 @@
 // references and fragment orders are used here.
 //
 // Work is dealt by what the lengths say on the device, not by what the tables could
-// hold: the rounds (KB keys) of all (sequence, key head) pairs form one line, and
-// each of a fixed number of workgroups takes an equal stretch of it.  A pair that lies within
-// one stretch is finished there; one that crosses borders leaves parts, at most
-// two per workgroup, which the join adds up.  The workspace therefore does not
-// grow with the caches, and sequences of any mix of lengths keep all CUs busy.
+// hold: the rounds (64 keys) of all (sequence, key head) pairs form one line, and
+// each of a fixed number of workgroups takes an equal stretch of it.  A pair that
+// lies within one stretch is finished there; one that crosses borders leaves parts,
+// at most two per workgroup, which the join adds up.  The workspace therefore does
+// not grow with the caches, and sequences of any mix of lengths keep all CUs busy.
 //
-// Positions come in grains of 16, which never cross a page: a wave finds a
-// grain's page with scalar loads, a page ahead.  The four waves of a workgroup share the rows and take tiles of keys through LDS, where loads put them by
-// themselves (attend_tree_tiles).
+// Positions come in grains of 16, which never cross a page: a wave finds a grain's
+// page with scalar loads, a page ahead.  The four waves of a workgroup share the rows
+// of a pair and take tiles of keys through LDS, where loads put them by themselves
+// (attend_tree_tiles), three tiles ahead of the products.  Rows that one wave alone
+// holds go the same way: the other three only move tiles.  (Each wave walking keys of
+// its own, from memory to registers, took 165 us where this takes 146: 48 single rows
+// of 32/8 heads of 128 on 4500 positions, 885 MB.)
+//
+// Few rows are bound by the read of the caches: those 48 rows 6.0 TB/s, with 9 rows each
+// 5.3, 16 rows of heads of 256 on 16384 positions 6.9; 48 ragged trees on 1000 to 8000
+// positions 169 us, 5.4 TB/s.  There the slowest workgroup ends 15% behind the mean (a
+// CU's older workgroup leads, and of two neighbouring XCDs one): shorter stretches or a
+// second, finer deal cost in parts and starts what they even out.  Many rows are bound by
+// vector and matrix instructions that overlap in part: 16 trees of 64 rows, 32/8 heads
+// of 128, 2048 to 16384 positions 240 us, 675 TFLOP/s.  Few keys are bound by two launches
+// and four trips to memory: 2 rows of 8 heads of 64 on 500 positions 10.6 us (7.6 + 3.2).
 #pragma once
 
 #include "sv_attention.hpp"
@@ -203,9 +216,10 @@ __device__ __forceinline__ void store4(char* p, float x0, float x1, float x2, fl
     *(SV_GLOBAL u32x2*)p = w;
 }
 
-// Four waves of MT * 16 rows share tiles of keys through LDS, whose rows lie and are read
-// as in TileAttention.  Four tiles of 16 KB (64 columns: of 64 keys; 128: of 32) are on their way or in use: with two
-// of them a step lasted as long as a read of memory.
+// Four waves of MT * 16 rows share tiles of keys through LDS, whose rows lie and are read as in TileAttention.  Four
+// tiles (64 columns: of 64 keys, 16 KB; 128: of 32, 16 KB; 256: of 32, 32 KB) are on their way or in use: with two of them
+// a step lasted as long as a read of memory.  One workgroup per CU with eight buffers, or with tiles of twice the keys,
+// instead of two with four: 200 and 157 us, not 150, on 48 single rows of 4500 positions.
 template <int D>
 struct TreeTile {
     static constexpr int KT = D == 64 ? 64 : 32;           // keys
@@ -220,10 +234,10 @@ struct TreeTile {
 
 __device__ __forceinline__ uint32_t lds_address(const char* p) { return (uint32_t)(uintptr_t)(const SV_LDS char*)p; }
 
-// 16 bytes from each lane's place `off` behind `base` into LDS, lane i's at `to` + 16 i (`to`: the wave's).  In assembly, which the compiler
-// does not count among the loads in flight: it would wait for all of them before every transposed read of a tile.
-// arrived() is the wait for them; a wave has none left when its loop over the tiles ends.  (M0 is not kept between
-// instructions that take it: nothing else here does.)
+// 16 bytes from each lane's place `off` behind `base` into LDS, lane i's at `to` + 16 i (`to`: the wave's).  In assembly,
+// which the compiler does not count among the loads in flight: it would wait for all of them before every transposed
+// read of a tile.  arrived() is the wait for them; a wave has none left when its loop over the tiles ends.  (M0 is not
+// kept between instructions that take it: nothing else here does.)
 template <bool PAST>
 __device__ __forceinline__ void load_to_lds(const char* base, uint32_t off, uint32_t to)
 {
