@@ -588,14 +588,21 @@ struct TreeStart {
     int32_t total, stretch;  // rounds of the line, and of one workgroup
     int32_t extra;           // rounds that a pair counts beyond its own
     int32_t b, at;           // the sequence that holds the first round, and the rounds of it before that one
+    int32_t len, row0, row1;  // its length, its first row and the next sequence's
 };
 __device__ __forceinline__ TreeStart tree_start(const TreeArgs& a, int32_t group, bool write, int32_t* s_sum,
                                                 int32_t* s_found)
 {
     const int32_t tid = (int32_t)threadIdx.x, per = (a.batch + kAttnThreads - 1) / kAttnThreads;
     const int32_t b0 = min(tid * per, a.batch), b1 = min(b0 + per, a.batch);
-    int32_t mine = 0;
-    for (int32_t b = b0; b < b1; ++b) mine += (tree_length(a, b) + kTreeRound - 1) / kTreeRound * a.kv_heads;
+    int32_t mine = 0, len = 0, row0 = 0, row1 = 0;
+    if (b0 < b1) {  // (asked for together: one trip to memory where every thread has one sequence)
+        len = tree_length(a, b0);
+        row0 = tree_row(a, b0);
+        row1 = tree_row(a, b0 + 1);
+        mine = (len + kTreeRound - 1) / kTreeRound * a.kv_heads;
+    }
+    for (int32_t b = b0 + 1; b < b1; ++b) mine += (tree_length(a, b) + kTreeRound - 1) / kTreeRound * a.kv_heads;
     const int32_t incl = wave_incl_scan_int(mine);
     if (lane_id() == kWave - 1) s_sum[wave_id()] = incl;
     __syncthreads();
@@ -616,7 +623,7 @@ __device__ __forceinline__ TreeStart tree_start(const TreeArgs& a, int32_t group
         int32_t sum = before;
         for (int32_t b = b0; b < b1; ++b) {
             a.plan[b] = sum;
-            sum += (tree_length(a, b) + kTreeRound - 1) / kTreeRound * a.kv_heads + extra;
+            if (b + 1 < b1) sum += (tree_length(a, b) + kTreeRound - 1) / kTreeRound * a.kv_heads + extra;
         }
         if (tid == 0) {
             a.plan[a.batch] = total;
@@ -627,28 +634,30 @@ __device__ __forceinline__ TreeStart tree_start(const TreeArgs& a, int32_t group
     if (from >= before && from < before + mine) {
         int32_t sum = before, b = b0;
         while (true) {
-            const int32_t n = (tree_length(a, b) + kTreeRound - 1) / kTreeRound * a.kv_heads + extra;
+            const int32_t n = (len + kTreeRound - 1) / kTreeRound * a.kv_heads + extra;
             if (from < sum + n) break;
             sum += n;
-            ++b;
+            len = tree_length(a, ++b);
+            row0 = row1;
+            row1 = tree_row(a, b + 1);
         }
         s_found[0] = b;
         s_found[1] = (int32_t)(from - sum);
+        s_found[2] = len;
+        s_found[3] = row0;
+        s_found[4] = row1;
     }
     __syncthreads();
-    return TreeStart{total, stretch, extra / a.kv_heads, s_found[0], s_found[1]};
+    return TreeStart{total, stretch, extra / a.kv_heads, s_found[0], s_found[1], s_found[2], s_found[3], s_found[4]};
 }
 
 template <int DT, int D, int MT>
 __global__ __launch_bounds__(kAttnThreads, D == 256 ? 1 : 2) void tree_part_kernel(TreeArgs a)
 {
     constexpr int ROWS = MT * 16 * kAttnWaves, KB = kTreeRound;
-    constexpr size_t kLds = TreeTile<D>::LDS;
-    // The stretches count on two workgroups per CU: more than a third of the 160 KB keeps a third one out.
-    constexpr size_t kLdsOfTwo = 52 * 1024, kMem = D != 256 && kLds < kLdsOfTwo ? kLdsOfTwo : kLds;
-    __shared__ __align__(16) char s_mem[kMem];
+    __shared__ __align__(16) char s_mem[TreeTile<D>::LDS];
     __shared__ uint32_t s_view[ROWS * kTreeWords];
-    __shared__ int32_t s_up[kTreeMostGuesses], s_sum[kAttnWaves], s_found[2], s_wild;
+    __shared__ int32_t s_up[kTreeMostGuesses], s_sum[kAttnWaves], s_found[5], s_wild;
     // the row tiles of one stretch (the same keys) run on one XCD (workgroups go to the 8 XCDs in turn)
     const uint32_t x = blockIdx.x & 7u, y = blockIdx.x >> 3;
     const int32_t group = a.tiles == 1 ? (int32_t)blockIdx.x : (int32_t)(y / (uint32_t)a.tiles * 8u + x);
@@ -660,12 +669,17 @@ __global__ __launch_bounds__(kAttnThreads, D == 256 ? 1 : 2) void tree_part_kern
     const int64_t end = min(at + start.stretch, (int64_t)start.total);
     int32_t b = __builtin_amdgcn_readfirstlane(start.b);
     int32_t in = __builtin_amdgcn_readfirstlane(start.at);  // rounds of sequence b before `at`
+    int32_t len = __builtin_amdgcn_readfirstlane(start.len), row0 = __builtin_amdgcn_readfirstlane(start.row0),
+            row1 = __builtin_amdgcn_readfirstlane(start.row1);
     bool first = true;
     while (at < end) {
-        const int32_t len = __builtin_amdgcn_readfirstlane(tree_length(a, b)), n = (len + KB - 1) / KB, pair = n + start.extra;
+        const int32_t n = (len + KB - 1) / KB, pair = n + start.extra;
         if (in >= pair * a.kv_heads) {  // (also the empty sequences)
             in -= pair * a.kv_heads;
             ++b;
+            len = __builtin_amdgcn_readfirstlane(tree_length(a, b));
+            row0 = row1;
+            row1 = __builtin_amdgcn_readfirstlane(tree_row(a, b + 1));
             continue;
         }
         const int32_t hk = in / pair, j = in - hk * pair;
@@ -673,8 +687,8 @@ __global__ __launch_bounds__(kAttnThreads, D == 256 ? 1 : 2) void tree_part_kern
         Stretch st;
         st.b = b;
         st.hk = hk;
-        st.row0 = __builtin_amdgcn_readfirstlane(tree_row(a, b));
-        st.nrows = __builtin_amdgcn_readfirstlane(min(tree_row(a, b + 1) - st.row0, a.kmax + 1));
+        st.row0 = row0;
+        st.nrows = min(row1 - row0, a.kmax + 1);
         st.total = len;
         st.context = len - st.nrows;
         st.begin = j * KB;
