@@ -13,6 +13,7 @@
 // lies within one stretch is finished there; one that crosses borders leaves parts,
 // at most two per workgroup, which the join adds up.  The workspace therefore does
 // not grow with the caches, and sequences of any mix of lengths keep all CUs busy.
+// Where the tables hold few positions a pair is one workgroup's, and nothing is dealt.
 //
 // Positions come in grains of 16, which never cross a page: a wave finds a grain's
 // page with scalar loads, a page ahead.  The four waves of a workgroup share the rows
@@ -55,6 +56,7 @@ struct TreeArgs {
     int32_t q_heads, kv_heads, rep;
     float c;                                         // scale * log2(e)
     int32_t groups, tiles;                           // stretches of the line; row tiles
+    bool whole;                                      // a stretch is a pair: no parts, no join
     int32_t* plan;                                   // [batch + 1] rounds before each sequence, the stretch, the extra
     float* acc;                                      // [2 * groups][tile][row][D]
     float2* ml;                                      // [2 * groups][tile][row]
@@ -663,17 +665,32 @@ __global__ __launch_bounds__(kAttnThreads, D == 256 ? 1 : 2) void tree_part_kern
     const int32_t group = a.tiles == 1 ? (int32_t)blockIdx.x : (int32_t)(y / (uint32_t)a.tiles * 8u + x);
     const int32_t tile = a.tiles == 1 ? 0 : (int32_t)(y % (uint32_t)a.tiles);
     if (group >= a.groups) return;
-    const TreeStart start = tree_start(a, group, group == 0 && tile == 0, s_sum, s_found);
-    int64_t at = (int64_t)group * start.stretch;
-    if (at >= start.total) return;
-    const int64_t end = min(at + start.stretch, (int64_t)start.total);
-    int32_t b = __builtin_amdgcn_readfirstlane(start.b);
-    int32_t in = __builtin_amdgcn_readfirstlane(start.at);  // rounds of sequence b before `at`
-    int32_t len = __builtin_amdgcn_readfirstlane(start.len), row0 = __builtin_amdgcn_readfirstlane(start.row0),
-            row1 = __builtin_amdgcn_readfirstlane(start.row1);
+    int64_t at, end;
+    int32_t b, in, extra, len, row0, row1;  // in: rounds of sequence b before `at`
+    if (a.whole) {                          // one pair per workgroup (an empty one counts a round)
+        b = group / a.kv_heads;
+        len = __builtin_amdgcn_readfirstlane(tree_length(a, b));
+        row0 = __builtin_amdgcn_readfirstlane(tree_row(a, b));
+        row1 = __builtin_amdgcn_readfirstlane(tree_row(a, b + 1));
+        extra = len == 0 ? 1 : 0;
+        at = 0;
+        end = (len + KB - 1) / KB + extra;
+        in = (group - b * a.kv_heads) * (int32_t)end;
+    } else {
+        const TreeStart start = tree_start(a, group, group == 0 && tile == 0, s_sum, s_found);
+        at = (int64_t)group * start.stretch;
+        if (at >= start.total) return;
+        end = min(at + start.stretch, (int64_t)start.total);
+        b = __builtin_amdgcn_readfirstlane(start.b);
+        in = __builtin_amdgcn_readfirstlane(start.at);
+        extra = start.extra;
+        len = __builtin_amdgcn_readfirstlane(start.len);
+        row0 = __builtin_amdgcn_readfirstlane(start.row0);
+        row1 = __builtin_amdgcn_readfirstlane(start.row1);
+    }
     bool first = true;
     while (at < end) {
-        const int32_t n = (len + KB - 1) / KB, pair = n + start.extra;
+        const int32_t n = (len + KB - 1) / KB, pair = n + extra;
         if (in >= pair * a.kv_heads) {  // (also the empty sequences)
             in -= pair * a.kv_heads;
             ++b;
@@ -698,7 +715,7 @@ __global__ __launch_bounds__(kAttnThreads, D == 256 ? 1 : 2) void tree_part_kern
         st.v = a.v + (int64_t)hk * a.v_head;
         st.table = a.table != nullptr ? a.table + (int64_t)b * a.table_stride : nullptr;
         st.parents = a.parents != nullptr ? a.parents + (st.row0 - b) : nullptr;
-        if (take > 0 && tile * ROWS < st.nrows * a.rep) {
+        if ((take > 0 || a.whole) && tile * ROWS < st.nrows * a.rep) {
             __syncthreads();  // (the stretch before this one is done with the LDS)
             const TreeOut to{j == 0 && take == n, ((int64_t)group * 2 + (first ? 0 : 1)) * a.tiles + tile};
             attend_tree_tiles<DT, D, MT>(a, st, tile, to, s_up, s_view, &s_wild, s_mem);

@@ -139,7 +139,13 @@ constexpr int32_t kTreeGroupsWide = 256;
 // D / 4 lanes, 35 with the wave; 48 ragged trees of up to 9 rows 167 and 168, 64 of 8 rows and 64 columns 95 and 99.
 constexpr int64_t kJoinSplit = 4096;
 
+// Columns of a pair's cache up to which one workgroup takes the whole pair, without a deal and a join: so many for any
+// call, twice as many from 64 workgroups on, four times from 256.  64 rows of 32/8 heads of 128 on up to 512 positions:
+// 27 us dealt, 19.5 whole, on 256 22 and 12.6, on 1024 34 and 35; one row on 112 11.5 and 8.6, on 512 11.3 and 17.8.
+constexpr int64_t kTreeWhole = 1 << 14;
+
 struct TreePlan {
+    bool whole;
     int32_t mt, wg_rows, row_tiles, groups, rows, capacity;
     int64_t grid, join;
     size_t off_plan, off_ml, off_acc, bytes;
@@ -160,10 +166,12 @@ TreePlan tree_plan(const sv_tree_shape_t* sh)
     p.row_tiles = (int32_t)((rows + p.wg_rows - 1) / p.wg_rows);
     const int64_t rounds = (int64_t)sh->batch * sh->kv_heads * (((int64_t)p.capacity + sv::kTreeRound - 1) / sv::kTreeRound);
     const int64_t target = std::max((sh->head_dim == 256 ? kTreeGroupsWide : kTreeGroups) / p.row_tiles, 1);
-    p.groups = (int32_t)std::min(target, rounds);
+    const int64_t pairs = (int64_t)sh->batch * sh->kv_heads, workgroups = pairs * p.row_tiles;
+    p.whole = (int64_t)p.capacity * sh->head_dim <= kTreeWhole * (workgroups >= 256 ? 4 : workgroups >= 64 ? 2 : 1);
+    p.groups = p.whole ? (int32_t)pairs : (int32_t)std::min(target, rounds);
     p.grid = p.row_tiles == 1 ? p.groups : (int64_t)(p.groups + 7) / 8 * 8 * p.row_tiles;
     p.join = (int64_t)sh->batch * (sh->max_draft + 1) * sh->q_heads;
-    const size_t slots = 2 * (size_t)p.groups * (size_t)p.row_tiles * (size_t)p.wg_rows;
+    const size_t slots = p.whole ? 0 : 2 * (size_t)p.groups * (size_t)p.row_tiles * (size_t)p.wg_rows;
     p.off_plan = 0;
     p.off_ml = align_up((size_t)(sh->batch + 3) * 4);
     p.off_acc = align_up(p.off_ml + slots * sizeof(float2));
@@ -210,6 +218,7 @@ sv_status_t run_tree(const TreePlan& p, const sv::TreeArgs& a, hipStream_t strea
 {
     launch_stream_nt(prof, sv::tree_part_kernel<DT, D, MT>, (uint32_t)p.grid, sv::kAttnThreads, stream, a);
     if (launch_status() != SV_OK) return SV_ERR_HIP;
+    if (p.whole) return SV_OK;
     constexpr int ROWS = MT * 16 * sv::kAttnWaves;
     const auto join = [&](auto split) {
         constexpr bool SPLIT = decltype(split)::value;
@@ -284,6 +293,7 @@ sv_status_t tree_attention_common(const sv_tree_shape_t* sh, const void* q, cons
     a.rep = sh->q_heads / sh->kv_heads;
     a.c = (float)((double)scale * 1.4426950408889634);
     a.groups = p.groups;
+    a.whole = p.whole;
     a.tiles = p.row_tiles;
     a.plan = ws_at<int32_t>(workspace, p.off_plan);
     a.ml = ws_at<float2>(workspace, p.off_ml);

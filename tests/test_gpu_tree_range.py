@@ -109,3 +109,57 @@ def test_logits_past_32_bits(sv, dtype):
     for call in (lambda x: sv.verify_tree_greedy(x, ids, ups), lambda x: sv.verify_tree_sample(x, ids, ups, seed=4)):
         a, b = call(logits), call(ref)
         assert all(torch.equal(a[k], b[k]) for k in b)
+
+
+@pytest.mark.parametrize("context,drafts,q_heads,kv_heads,dim,size,dtype,form", [
+    ([100, 37, 0, 5], [0, 3, 1, 7], 8, 2, 128, 16, "bf16", "paged"),
+    ([180, 0, 13], [4, 0, 9], 6, 3, 64, 48, "f16", "paged"),
+    ([40, 30], [3, 2], 8, 2, 256, 16, "bf16", "paged"),
+    ([100, 20], [19, 5], 8, 2, 128, 0, "f16", "piece"),
+    ([90, 1], [128, 100], 4, 2, 64, 16, "bf16", "chain"),                      # three row tiles
+    (list(range(3, 240, 12)), [k % 4 for k in range(20)], 8, 4, 128, 16, "f16", "paged"),  # 80 workgroups
+    (list(range(0, 960, 12)), [k % 3 for k in range(80)], 4, 4, 64, 32, "bf16", "paged"),  # 320
+    (list(range(0, 240, 3)), [0] * 80, 4, 4, 256, 16, "bf16", "paged"),
+])
+def test_pairs_of_one_workgroup(sv, context, drafts, q_heads, kv_heads, dim, size, dtype, form):
+    """Tables that hold few positions: a workgroup per pair and no parts, also for empty sequences, pages that are none and
+    values that are not finite."""
+    c = Case(context, drafts, q_heads, kv_heads, dim, size, dtype, form != "chain", seed=dim + len(context))
+    plan = sv.TreeAttentionPlan(c.q, c.k, c.v, **c.kw())
+    assert plan.workspace.numel() < 65536  # (no parts)
+    plan.out["out"].fill_(7), plan.out["lse"].fill_(7)
+    c.check(plan())
+    # in the graph's replays too, with other lengths in the same tensor
+    graph = torch.cuda.CUDAGraph()
+    lengths = ints(c.lengths)
+    held = sv.TreeAttentionPlan(c.q, c.k, c.v, **c.kw(lengths=lengths))
+    with torch.cuda.graph(graph):
+        held()
+    for cut in (3, 0, 10 ** 6):
+        c.lengths = np.maximum(c.lengths - cut, 0)
+        c.lengths[0] = 0
+        lengths.copy_(ints(c.lengths))
+        held.out["out"].fill_(7)
+        graph.replay()
+        torch.cuda.synchronize()
+        c.check(held.out)
+    assert not held.out["out"].any() and bool((held.out["lse"] == -float("inf")).all())
+
+
+def test_pairs_of_one_workgroup_with_holes(sv):
+    c = Case([70, 50, 90], [4, 9, 0], 4, 2, 128, 16, "bf16", seed=3)
+    c.table[0, 1], c.table[1, 2], c.table[2, :] = -1, c.k.shape[0], -7
+    assert sv.TreeAttentionPlan(c.q, c.k, c.v, **c.kw()).workspace.numel() < 65536
+    c.check(c.run(sv))
+    # values that are not finite behind the lengths and in other pages reach nobody; in a guess's row the rows that see it
+    ref = c.run(sv)
+    spare = sorted(set(range(c.k.shape[0])) - set(c.table.reshape(-1).tolist()))
+    for t in (c.k, c.v):
+        t[spare] = float("nan")
+    page, at = int(c.table[1, (c.lengths[1] - 1) // 16]), int((c.lengths[1] - 1) % 16)
+    c.v[page, at] = float("inf")  # the last guess's
+    c.k[page, at + 1:], c.v[page, at + 1:] = float("nan"), float("inf")
+    got = c.run(sv)
+    last = int(c.cu[2]) + 1  # its row
+    assert torch.equal(got["out"][:last], ref["out"][:last]) and torch.equal(got["out"][last + 1:], ref["out"][last + 1:])
+    assert bool(got["out"][last].isinf().all())
