@@ -579,9 +579,9 @@ __device__ __forceinline__ void attend_tree_tiles(const TreeArgs& a, const Stret
 }
 
 constexpr int kTreeRound = 64;  // keys: what the line of all pairs counts
-// A pair counts this many rounds beyond its own where stretches have at least kTreeExtraFrom: what a stretch's start and
-// end cost.  (16 trees of 32 rows on 9000 positions: 145 us without, 142 with 2, 141 with 4; 48 rows on 1000 to 8000
-// each: 160, 158 and 164.)
+// A pair counts this many rounds beyond its own, for each 16-row tile of a wave, where stretches have at least
+// kTreeExtraFrom: what a stretch's start and end cost (6 and 13 us at 2.4 and 2.9 us a round).  48 single rows on 1000 to
+// 8000 positions: 160 us without, 158 with 2, 164 with 4; 16 trees of 64 rows on 8192: 201 with 2, 195 with 4, 201 with 6.
 constexpr int kTreeExtra = 2, kTreeExtraFrom = 8;
 
 // The line's length and where a stretch begins, by all threads of the workgroup: thread t sums the sequences t * per
@@ -592,7 +592,7 @@ struct TreeStart {
     int32_t b, at;           // the sequence that holds the first round, and the rounds of it before that one
     int32_t len, row0, row1;  // its length, its first row and the next sequence's
 };
-__device__ __forceinline__ TreeStart tree_start(const TreeArgs& a, int32_t group, bool write, int32_t* s_sum,
+__device__ __forceinline__ TreeStart tree_start(const TreeArgs& a, int32_t group, int32_t per_pair, bool write, int32_t* s_sum,
                                                 int32_t* s_found)
 {
     const int32_t tid = (int32_t)threadIdx.x, per = (a.batch + kAttnThreads - 1) / kAttnThreads;
@@ -615,7 +615,7 @@ __device__ __forceinline__ TreeStart tree_start(const TreeArgs& a, int32_t group
         before += w < wave_id() ? x : 0;
         total += x;
     }
-    const int32_t extra = total / a.groups >= kTreeExtraFrom ? kTreeExtra * a.kv_heads : 0;  // per sequence
+    const int32_t extra = total / a.groups >= kTreeExtraFrom ? per_pair * a.kv_heads : 0;  // per sequence
     before += extra * b0;
     mine += extra * (b1 - b0);
     total += extra * a.batch;
@@ -677,7 +677,7 @@ __global__ __launch_bounds__(kAttnThreads, D == 256 ? 1 : 2) void tree_part_kern
         end = (len + KB - 1) / KB + extra;
         in = (group - b * a.kv_heads) * (int32_t)end;
     } else {
-        const TreeStart start = tree_start(a, group, group == 0 && tile == 0, s_sum, s_found);
+        const TreeStart start = tree_start(a, group, MT * kTreeExtra, group == 0 && tile == 0, s_sum, s_found);
         at = (int64_t)group * start.stretch;
         if (at >= start.total) return;
         end = min(at + start.stretch, (int64_t)start.total);

@@ -204,8 +204,8 @@ sv_status_t check_tree(const sv_tree_shape_t* sh, float scale)
         return SV_ERR_UNSUPPORTED;
     if (((int64_t)sh->total_draft + sh->batch) * sh->q_heads > INT32_MAX / 2) return SV_ERR_UNSUPPORTED;
     if ((int64_t)(sh->q_heads / sh->kv_heads) * (sh->max_draft + 1) > INT32_MAX / 256) return SV_ERR_UNSUPPORTED;
-    if ((double)sh->batch * sh->kv_heads * ((double)sh->max_pages * sh->page_size / sv::kTreeRound + 1 + sv::kTreeExtra) > (double)INT32_MAX)
-        return SV_ERR_UNSUPPORTED;
+    const double rounds = (double)sh->max_pages * sh->page_size / sv::kTreeRound + 1 + 2 * sv::kTreeExtra;
+    if ((double)sh->batch * sh->kv_heads * rounds > (double)INT32_MAX) return SV_ERR_UNSUPPORTED;
     if (sh->table_stride > INT64_MAX / 8 / sh->batch) return SV_ERR_UNSUPPORTED;
     const TreePlan p = tree_plan(sh);
     if (!launchable((double)p.grid, sv::kAttnThreads) || !launchable((double)(p.join / sv::kWaves + 1), sv::kThreads))
