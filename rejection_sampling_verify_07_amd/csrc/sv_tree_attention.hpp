@@ -615,7 +615,8 @@ __device__ __forceinline__ TreeStart tree_start(const TreeArgs& a, int32_t group
         before += w < wave_id() ? x : 0;
         total += x;
     }
-    const int32_t extra = total / a.groups >= kTreeExtraFrom ? per_pair * a.kv_heads : 0;  // per sequence
+    const int32_t more = total >= kTreeExtraFrom * a.groups ? per_pair : 0;  // (a.groups: 512 at most here)
+    const int32_t extra = more * a.kv_heads;                                  // per sequence
     before += extra * b0;
     mine += extra * (b1 - b0);
     total += extra * a.batch;
@@ -630,7 +631,7 @@ __device__ __forceinline__ TreeStart tree_start(const TreeArgs& a, int32_t group
         if (tid == 0) {
             a.plan[a.batch] = total;
             a.plan[a.batch + 1] = stretch;
-            a.plan[a.batch + 2] = extra / a.kv_heads;
+            a.plan[a.batch + 2] = more;
         }
     }
     if (from >= before && from < before + mine) {
@@ -650,7 +651,7 @@ __device__ __forceinline__ TreeStart tree_start(const TreeArgs& a, int32_t group
         s_found[4] = row1;
     }
     __syncthreads();
-    return TreeStart{total, stretch, extra / a.kv_heads, s_found[0], s_found[1], s_found[2], s_found[3], s_found[4]};
+    return TreeStart{total, stretch, more, s_found[0], s_found[1], s_found[2], s_found[3], s_found[4]};
 }
 
 template <int DT, int D, int MT>
