@@ -19,10 +19,10 @@
 // a workspace.
 //
 // 320 rows of 151936 bf16 logits, texts of up to 8000 tokens, three of four sequences
-// under masks, in place: 54 us with the logits in HBM, 46 with them in the caches.  The
-// masks alone take 23 (almost every line of a masked row is written), the penalties
+// under masks, in place: 45 us with the logits in the caches, 49 with them in memory.
+// The masks alone take 21 (almost every line of a masked row is written), the penalties
 // alone 30: elements scattered over lines, and before them the chain of the text's read,
-// the counts and the list.  43 ragged rows of 32003 fp16 logits, apart: 8.8 us; one row of
+// the counts and the list.  43 ragged rows of 32003 fp16 logits, apart: 9.0 us; one row of
 // 50304 fp32 logits, in place: 4.8 us, a launch and that chain.
 //
 // Arithmetic is fp32, each step rounded, the result rounded to the element type once.
@@ -80,6 +80,7 @@ struct AdjustArgs {
     int64_t mask_stride;   // bytes
     int32_t num_masks;
     const int32_t* mask_rows;
+    bool past;  // whole vectors are stored past the caches
 };
 
 // 16 bytes of a row, aligned to its elements only.
@@ -278,7 +279,7 @@ __global__ __launch_bounds__(NT) void adjust_kernel(AdjustArgs a)
     }
     __syncthreads();  // (the list, and the masks' numbers)
 
-    if (!INPLACE || a.masks != nullptr) {
+    const auto vectors = [&](auto past) {
         for (int32_t r = r0; r < r1; ++r) {
             const bool masked = a.masks != nullptr && s_mask[r - r0] >= 0;
             if (INPLACE && !masked) continue;
@@ -317,7 +318,9 @@ __global__ __launch_bounds__(NT) void adjust_kernel(AdjustArgs a)
                             v[q] = (v[q] & ~drop) | (Dt<DT>::kNegInf * 0x10001u & drop);
                         }
                     }
-                    *(SV_GLOBAL Vec*)(out + (int64_t)e * ES) = v;
+                    SV_GLOBAL Vec* to = (SV_GLOBAL Vec*)(out + (int64_t)e * ES);
+                    if constexpr (decltype(past)::value) __builtin_nontemporal_store((Vec)v, to);
+                    else *to = v;
                 } else {  // the vocabulary ends in this vector
 #pragma unroll 1
                     for (int x = 0; e + x < width; ++x) {
@@ -331,6 +334,10 @@ __global__ __launch_bounds__(NT) void adjust_kernel(AdjustArgs a)
                 }
             }
         }
+    };
+    if (!INPLACE || a.masks != nullptr) {
+        if (a.past) vectors(std::true_type{});
+        else vectors(std::false_type{});
     }
     if (!edits) return;
     if (!INPLACE || a.masks != nullptr) __syncthreads();  // (the first pass's stores, which share vectors with the second's)

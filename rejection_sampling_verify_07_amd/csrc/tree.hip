@@ -33,6 +33,10 @@ constexpr int32_t kAdjustFewBiases = 65535;
 // fp32 logits under masks: 30 us with 256, 29.5 with 1024, 48 with 4096; 4 of 9 bf16 rows 12.8, 11.5 and 16.2.
 constexpr int64_t kAdjustGroups = 1024;
 
+// Bytes of logits from which whole vectors are stored past the caches: 320 rows of 151936 bf16, four sets in turn, 59 us
+// and 62.5 through them (copied 70 and 75), 320 of 128256 fp32 copied 68 and 78; 43 rows of 32003 fp16 copied 9.4 and 9.2.
+constexpr double kAdjustPast = 64e6;
+
 sv_status_t check_adjust(const sv_adjust_shape_t* sh, const sv_adjust_t* ad, const void* logits, const void* out)
 {
     if (sh == nullptr || ad == nullptr) return SV_ERR_INVALID_ARGUMENT;
@@ -106,6 +110,7 @@ sv_status_t adjust_logits_common(const sv_adjust_shape_t* sh, const sv_adjust_t*
     a.mask_stride = ad->mask_stride * 4;
     a.num_masks = ad->num_masks;
     a.mask_rows = ad->mask_rows;
+    a.past = ((double)sh->total_draft + sh->batch) * sh->vocab * (double)es >= kAdjustPast;
     const int64_t rows = sh->max_draft + 1;
     const auto launch = [&](auto dt, auto inplace, auto bias) -> sv_status_t {
         constexpr int DT = decltype(dt)::value, NT = kAdjustThreads, CT = NT * kAdjustTokens;

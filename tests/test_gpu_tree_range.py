@@ -163,3 +163,30 @@ def test_pairs_of_one_workgroup_with_holes(sv):
     last = int(c.cu[2]) + 1  # its row
     assert torch.equal(got["out"][:last], ref["out"][:last]) and torch.equal(got["out"][last + 1:], ref["out"][last + 1:])
     assert bool(got["out"][last].isinf().all())
+
+
+@pytest.mark.parametrize("dtype,V", [(torch.float32, 140001), (torch.bfloat16, 280003), (torch.float16, 280000)])
+def test_edits_of_many_bytes(sv, dtype, V):
+    """Logits of more than 64 MB, in place and apart: what the same sequences get in calls of fewer."""
+    rng = np.random.default_rng(6)
+    B, K = 30, 3
+    rows = B * (K + 1)
+    assert rows * V * torch.finfo(dtype).bits // 8 > 64e6 > rows // 2 * V * torch.finfo(dtype).bits // 8
+    logits = torch.randn(rows, V, generator=torch.Generator(DEV).manual_seed(2), device=DEV).to(dtype)
+    text, ids = rng.integers(0, V, (B, 700)), rng.integers(0, V, B * K)
+    ups = np.concatenate([random_tree(rng, K) for _ in range(B)])
+    bits = torch.rand(rows, (V + 31) // 32, 32, generator=torch.Generator(DEV).manual_seed(3), device=DEV)
+    bits = bits < torch.tensor([0.02, 0.98, 1.0], device=DEV)[torch.arange(rows, device=DEV) % 3][:, None, None]
+    words = (bits.long() << torch.arange(32, device=DEV)).sum(2)
+    masks = torch.where(words >= 2 ** 31, words - 2 ** 32, words).int()
+    rep = 1 + torch.rand(B, device=DEV)
+
+    def call(b0, b1, x, out=None):
+        r = slice(b0 * (K + 1), b1 * (K + 1))
+        return sv.adjust_logits(x[r], ints(text[b0:b1]), repetition=rep[b0:b1], frequency=rep[b0:b1], masks=masks[r],
+                                draft_ids=ints(ids[b0 * K:b1 * K]), parents=ints(ups[b0 * K:b1 * K]), out=out)
+
+    want = torch.cat([call(i, i + B // 2, logits) for i in (0, B // 2)])
+    assert torch.equal(call(0, B, logits), want)
+    call(0, B, logits, out=logits)
+    assert torch.equal(logits, want)
