@@ -34,6 +34,7 @@
 #pragma once
 
 #include "sv_attention.hpp"
+#include "sv_tree_deal.hpp"
 
 namespace sv {
 
@@ -746,13 +747,10 @@ __global__ __launch_bounds__(kThreads) void tree_join_kernel(TreeArgs a)
     if (k >= nrows) return;
     const int32_t hk = h / a.rep, r = k * a.rep + (h - hk * a.rep), tile = r / ROWS;
     const int32_t from = begin + hk * pair;
-    const int32_t g0 = from / stretch, parts = rounds > 0 ? (from + rounds - 1) / stretch - g0 + 1 : 0;
+    const PairParts held = pair_parts(from, rounds, stretch);
+    const int32_t parts = held.count;
     if (parts == 1) return;
-    // the first part lies in its workgroup's second place if the workgroup began with another pair
-    auto place = [&](int32_t p) {
-        const int64_t slot = (int64_t)(g0 + p) * 2 + (p == 0 && from != g0 * stretch ? 1 : 0);
-        return (slot * a.tiles + tile) * ROWS + (r - tile * ROWS);
-    };
+    auto place = [&](int32_t p) { return (part_place(held, p) * a.tiles + tile) * ROWS + (r - tile * ROWS); };
     float m = kNoReference, l = 0.0f;
     f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
     auto batch = [&](int32_t p0, auto most) {
@@ -761,7 +759,7 @@ __global__ __launch_bounds__(kThreads) void tree_join_kernel(TreeArgs a)
         f32x4 v[N];
 #pragma unroll
         for (int j = 0; j < N; ++j) {
-            const int64_t at = place(min(p0 + j * PPR + sub, parts - 1));
+            const int64_t at = place(join_part(parts, p0 + j * PPR + sub));
             ml[j] = a.ml[at];
             v[j] = *(const SV_GLOBAL f32x4*)(a.acc + at * D + col);
             if (p0 + j * PPR + sub >= parts) ml[j] = float2{kNoReference, 0.0f};
@@ -782,9 +780,11 @@ __global__ __launch_bounds__(kThreads) void tree_join_kernel(TreeArgs a)
             for (int e = 0; e < 4; ++e) o[e] += v[j][e] * w;
         }
     };
-    if (parts <= 2 * PPR) batch(0, std::integral_constant<int, 2>{});
-    else if (parts <= 4 * PPR) batch(0, std::integral_constant<int, 4>{});
-    else
+    // (an empty sequence has no parts, and nothing of the workspace is its own: it is not read)
+    const int32_t most = join_batch(parts, PPR);
+    if (most == 2) batch(0, std::integral_constant<int, 2>{});
+    else if (most == 4) batch(0, std::integral_constant<int, 4>{});
+    else if (most == 8)
         for (int32_t p0 = 0; p0 < parts; p0 += 8 * PPR) batch(p0, std::integral_constant<int, 8>{});
 #pragma unroll
     for (int x = LPP; x < LPP * PPR; x <<= 1) {
