@@ -587,7 +587,7 @@ SV_API sv_status_t spec_verify_tree_sample(const sv_shape_t* shape,
  *   counts.  out overlaps no other input.  repetition > 0.
  * Errors: SV_ERR_INVALID_ARGUMENT (null or misaligned pointer, counts or strides as in spec_verify_sample,
  * token_stride < max_tokens, a mask_stride or num_masks too small, logits and out that
- * overlap), SV_ERR_UNSUPPORTED (limits as in spec_verify_sample, more than 2^30
+ * overlap), SV_ERR_UNSUPPORTED (limits as in spec_verify_sample, 2^30 or more
  * tokens of a sequence, more than 2^32 threads), SV_ERR_HIP.  Execution as for
  * spec_verify_sample; no workspace.
  */

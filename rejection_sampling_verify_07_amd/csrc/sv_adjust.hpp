@@ -33,7 +33,7 @@
 namespace sv {
 
 constexpr int kAdjustMost = 128;  // guesses of a sequence
-// A table entry: how often the token was written (below 2^30), and
+// A table entry: how often the token was written (below 2^30: the entry points refuse longer texts), and
 constexpr uint32_t kSeen = 0x80000000u;    // it is in the prompt
 constexpr uint32_t kBiased = 0x40000000u;  // it has a bias
 

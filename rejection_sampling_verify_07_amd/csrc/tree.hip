@@ -18,7 +18,7 @@ static_assert(SV_MAX_DRAFT == sv::kAdjustMost && SV_MAX_DRAFT == sv::kTreeMostGu
 
 namespace {
 
-constexpr int32_t kMaxTokens = 1 << 30;
+constexpr int32_t kMaxTokens = (1 << 30) - 1;  // a text's count of one token stays below the table entry's flags
 
 // ---- edits of logits
 

@@ -115,6 +115,14 @@ def test_adjust_refusals(T, lib, kw, code):
     assert _adjust(T, lib, **kw) == code
 
 
+def test_adjust_longest_text(T, lib):
+    """A count of 2^30 would be a table entry's flag.  (Logits that overlap the output are what the longest text that is
+    taken is refused for: nothing is launched.)"""
+    for n, code in (((1 << 30) - 1, 1), (1 << 30, 2), ((1 << 31) - 1, 2)):
+        assert _adjust(T, lib, out=FAKE + 2, max_tokens=n, token_stride=1 << 31) == code
+    assert _adjust(T, lib, out=FAKE + 2, tokens=None, max_tokens=1 << 30) == 1
+
+
 def test_adjust_null(T, lib):
     assert lib.spec_adjust_logits(None, C.byref(T.AdjustT()), FAKE, FAKE, None) == 1
     assert lib.spec_adjust_logits(C.byref(T.AdjustShapeT()), None, FAKE, FAKE, None) == 1
