@@ -360,8 +360,11 @@ sv_status_t prefix_attention_common(const sv_attention_shape_t* sh, const void* 
         sk = suffix_k;
         svc = suffix_v;
     }
-    for (const sv_cache_t* c : {pk, pv, sk, svc})
-        if (c->position_stride * 2 > kMaxPosStride) return SV_ERR_UNSUPPORTED;
+    if (!cache_fits(pk, sh->groups, sh->kv_heads) || !cache_fits(pv, sh->groups, sh->kv_heads) ||
+        !cache_fits(sk, sh->batch, sh->kv_heads) || !cache_fits(svc, sh->batch, sh->kv_heads) ||
+        !stride_ok(sh->q_row_stride, p.rows) || !stride_ok(sh->q_head_stride, sh->q_heads) ||
+        !stride_ok(sh->out_row_stride, p.rows) || !stride_ok(sh->out_head_stride, sh->q_heads))
+        return SV_ERR_UNSUPPORTED;
     if (*workspace_bytes < p.bytes) return SV_ERR_WORKSPACE_TOO_SMALL;
     sv::AttnArgs a{};
     a.q = static_cast<const char*>(q);

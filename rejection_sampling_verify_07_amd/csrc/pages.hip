@@ -96,7 +96,8 @@ sv_status_t cache_compact_common(const sv_compact_shape_t* sh, void* data, const
         int64_t bytes;
     } inputs[] = {{lengths, sh->batch * 4ll}, {path, rows * 4}, {num_accepted, sh->batch * 4ll},
                   {sh->cu_draft, (sh->batch + 1ll) * 4},
-                  {sh->page_table, table_bytes(sh->batch, sh->table_stride, sh->max_pages)}};
+                  {sh->page_table,
+                   sh->page_table != nullptr ? table_bytes(sh->batch, sh->table_stride, sh->max_pages) : 0}};
     for (const auto& in : inputs)
         if (overlap(in.p, in.bytes, data, extent) || overlap(in.p, in.bytes, out_lengths, sh->batch * 4ll))
             return SV_ERR_INVALID_ARGUMENT;

@@ -126,6 +126,16 @@ inline bool cache_ok(const sv_cache_t* c)
            c->head_stride % 8 == 0 && c->position_stride % 8 == 0;
 }
 
+// Whether `count` places this far apart (elements) stay within what 64 bits count, in bytes of any element type.
+inline bool stride_ok(int64_t stride, int64_t count) { return stride <= INT64_MAX / 16 / count; }
+
+// The limits of a cache of 2-byte elements: `outer` groups, sequences or pages of `heads` heads.
+inline bool cache_fits(const sv_cache_t* c, int64_t outer, int64_t heads)
+{
+    return c->position_stride <= kMaxPosStride / 2 && stride_ok(c->batch_stride, outer) &&
+           stride_ok(c->head_stride, heads);
+}
+
 // Whether rows of `width` elements at two strides lie apart.
 inline bool distinct_rows(int64_t s0, int64_t n0, int64_t s1, int64_t n1, int64_t width)
 {

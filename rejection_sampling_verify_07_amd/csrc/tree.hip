@@ -107,7 +107,7 @@ sv_status_t adjust_logits_common(const sv_adjust_shape_t* sh, const sv_adjust_t*
     a.cu_bias = ad->cu_bias;
     a.total_bias = ad->total_bias;
     a.masks = reinterpret_cast<const uint8_t*>(ad->masks);
-    a.mask_stride = ad->mask_stride * 4;
+    a.mask_stride = ad->masks != nullptr ? ad->mask_stride * 4 : 0;
     a.num_masks = ad->num_masks;
     a.mask_rows = ad->mask_rows;
     a.past = ((double)sh->total_draft + sh->batch) * sh->vocab * (double)es >= kAdjustPast;
@@ -258,8 +258,10 @@ sv_status_t tree_attention_common(const sv_tree_shape_t* sh, const void* q, cons
     if (!distinct_rows(sh->out_row_stride, p.rows, sh->out_head_stride, sh->q_heads, sh->head_dim))
         return SV_ERR_INVALID_ARGUMENT;
     if (!cache_ok(k) || !cache_ok(v)) return SV_ERR_INVALID_ARGUMENT;
-    for (const sv_cache_t* c : {k, v})
-        if (c->position_stride * 2 > kMaxPosStride) return SV_ERR_UNSUPPORTED;
+    if (!cache_fits(k, sh->pages, sh->kv_heads) || !cache_fits(v, sh->pages, sh->kv_heads) ||
+        !stride_ok(sh->q_row_stride, p.rows) || !stride_ok(sh->q_head_stride, sh->q_heads) ||
+        !stride_ok(sh->out_row_stride, p.rows) || !stride_ok(sh->out_head_stride, sh->q_heads))
+        return SV_ERR_UNSUPPORTED;
     if (*workspace_bytes < p.bytes) return SV_ERR_WORKSPACE_TOO_SMALL;
     sv::TreeArgs a{};
     a.q = static_cast<const char*>(q);

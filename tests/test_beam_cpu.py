@@ -249,6 +249,22 @@ def test_attention_position_stride_limit(B, lib):
             assert _attend(B, lib, _attn_shape(B), ws=FAKE, have=need - 1, caches={i: c})[0] == code
 
 
+def test_attention_strides_that_64_bits_do_not_hold(B, lib):
+    need = _attend(B, lib, _attn_shape(B))[1]
+    for far in (1 << 62, (1 << 63) - 8, 1 << 58):
+        for i in range(4):
+            for at in range(3):
+                strides = [1024, 256, 128]
+                strides[at] = far
+                got = _attend(B, lib, _attn_shape(B), ws=FAKE, have=need - 1, caches={i: B.CacheT(FAKE, *strides)})
+                assert got[0] == 2, (i, at, far)
+        for name in ("q_row_stride", "q_head_stride", "out_row_stride", "out_head_stride"):
+            assert _attend(B, lib, _attn_shape(B, **{name: far}), ws=FAKE, have=need - 1)[0] == 2, (name, far)
+    c = B.CacheT(FAKE, 1 << 50, 256, 1 << 50)
+    sh = _attn_shape(B, q_row_stride=1 << 50, out_head_stride=1 << 50)
+    assert _attend(B, lib, sh, ws=FAKE, have=need - 1, caches={0: c, 3: c})[0] == 3
+
+
 def test_attention_row_limit(B, lib):
     """max_group * (max_draft + 1) rows of a key head may be far more than the batch holds."""
     kw = dict(groups=1, batch=1 << 19, max_group=1 << 19, max_draft=128, total_draft=0, q_heads=64, kv_heads=1,

@@ -181,6 +181,27 @@ def test_tree_pointers(T, lib):
     assert _tree(T, lib, ws=FAKE, have=need - 1)[0] == 3
 
 
+def test_tree_strides_that_64_bits_do_not_hold(T, lib):
+    """Counted in bytes they would wrap.  (The workspace is too small: nothing is launched.)"""
+    need = _tree(T, lib)[1]
+    short = dict(ws=FAKE, have=need - 1)
+    for far in (1 << 62, (1 << 63) - 8, 1 << 58):
+        for at in range(3):
+            cache = [4096, 256, 128]
+            cache[at] = far
+            for name in ("k", "v"):
+                assert _tree(T, lib, **short, **{name: (FAKE, *cache)})[0] == 2, (name, at, far)
+        for name in ("q_row_stride", "q_head_stride", "out_row_stride", "out_head_stride"):
+            assert _tree(T, lib, **short, **{name: far})[0] == 2, (name, far)
+    # what is still counted
+    for name in ("q_row_stride", "q_head_stride", "out_row_stride", "out_head_stride"):
+        assert _tree(T, lib, **short, **{name: 1 << 50})[0] == 3
+    for at, stride in ((0, 1 << 50), (1, 1 << 24), (2, 1 << 50)):
+        cache = [4096, 256, 128]
+        cache[at] = stride
+        assert _tree(T, lib, **short, k=(FAKE, *cache))[0] == 3
+
+
 def test_tree_binding_refusals(T):
     q, k = torch.zeros(6, 4, 64, dtype=torch.bfloat16), torch.zeros(9, 16, 2, 64, dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="GPU"):
