@@ -621,7 +621,7 @@ __device__ __forceinline__ TreeStart tree_start(const TreeArgs& a, int32_t group
     before += extra * b0;
     mine += extra * (b1 - b0);
     total += extra * a.batch;
-    const int32_t stretch = max(1, (total + a.groups - 1) / a.groups);
+    const int32_t stretch = deal_stretch(total, a.groups);
     const int64_t from = (int64_t)group * stretch;
     if (write) {
         int32_t sum = before;

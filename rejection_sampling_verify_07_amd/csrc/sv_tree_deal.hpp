@@ -12,6 +12,9 @@
 
 namespace sv {
 
+// Rounds of a stretch where `total` (up to 2^31 - 1) are dealt to `groups` workgroups.
+constexpr int32_t deal_stretch(int32_t total, int32_t groups) { return total > 0 ? (total - 1) / groups + 1 : 1; }
+
 struct PairParts {
     int32_t group;  // the workgroup that has the first of them
     int32_t count;  // 0: the pair has no rounds

@@ -12,11 +12,15 @@ ROUND = 64  # keys
 
 
 @pytest.fixture(scope="module")
-def places(tmp_path_factory):
-    exe = str(tmp_path_factory.mktemp("deal") / "tree_deal")
-    subprocess.run(["g++", "-std=c++17", "-O1", "-Wall", "-Werror", "-I", CSRC, "-o", exe,
+def exe(tmp_path_factory):
+    out = str(tmp_path_factory.mktemp("deal") / "tree_deal")
+    subprocess.run(["g++", "-std=c++17", "-O1", "-Wall", "-Werror", "-I", CSRC, "-o", out,
                     os.path.join(HERE, "tree_deal_helper.cpp")], check=True, capture_output=True)
+    return out
 
+
+@pytest.fixture(scope="module")
+def places(exe):
     def run(rows):
         text = "".join("%d %d %d %d\n" % r for r in rows)
         out = subprocess.run([exe], input=text, capture_output=True, text=True, check=True).stdout
@@ -67,6 +71,15 @@ BATCHES = [
 @pytest.mark.parametrize("lengths,heads,groups,extra", BATCHES)
 def test_places_of_batches_with_empty_sequences(places, lengths, heads, groups, extra):
     check(places, lengths, heads, groups, extra)
+
+
+def test_stretches_of_the_longest_line(exe):
+    """Up to the 2^31 - 1 rounds that the entry point admits."""
+    rows = [(t, g) for g in (1, 2, 7, 8, 511, 512) for t in (0, 1, 2, g, g + 1, 10 ** 6, 2 ** 31 - g, 2 ** 31 - 2, 2 ** 31 - 1)
+            if t < 2 ** 31]
+    out = subprocess.run([exe, "stretch"], input="".join("%d %d\n" % r for r in rows), capture_output=True, text=True,
+                         check=True).stdout
+    assert [int(x) for x in out.split()] == [max(1, -(-t // g)) for t, g in rows]
 
 
 def test_places_of_random_batches(places):

@@ -1,11 +1,14 @@
 // The places that the join of spec_tree_attention reads, by the library's own arithmetic.  Per line of input
 // "from rounds stretch side" a line of output: the pair's parts, then each place read, in the order of the join's lanes.
+// With an argument: per line "total groups" the stretch.
 #include <cstdio>
 
 #include "sv_tree_deal.hpp"
 
-int main()
+int main(int argc, char**)
 {
+    int total, groups;
+    while (argc > 1 && std::scanf("%d %d", &total, &groups) == 2) std::printf("%d\n", sv::deal_stretch(total, groups));
     int from, rounds, stretch, side;
     while (std::scanf("%d %d %d %d", &from, &rounds, &stretch, &side) == 4) {
         const sv::PairParts parts = sv::pair_parts(from, rounds, stretch);
