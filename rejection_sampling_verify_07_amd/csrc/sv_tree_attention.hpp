@@ -63,10 +63,9 @@ struct TreeArgs {
     float2* ml;                                      // [2 * groups][tile][row]
 };
 
-// First packed row of sequence b; entries of cu outside the batch are clamped.
+// First packed row of sequence b (b = batch: the end of the last one's); entries of cu outside the batch are clamped.
 __device__ __forceinline__ int32_t tree_row(const TreeArgs& a, int32_t b)
 {
-    if (b >= a.batch) return a.rows;
     if (a.cu == nullptr) return b * (a.kmax + 1);
     return min(max(a.cu[b], 0), a.rows - a.batch) + b;
 }
