@@ -452,7 +452,8 @@ SV_API sv_status_t spec_state_reorder(const sv_state_shape_t* shape,
  * Errors as for spec_verify_sample; SV_ERR_INVALID_ARGUMENT also for q_heads
  * no multiple of kv_heads and for rows of out that overlap; SV_ERR_UNSUPPORTED
  * also for fp32, another head_dim, more than 2^30 positions, positions more
- * than 32 MB apart, strides whose extents 64 bits do not count, or more than 2^32 threads.  A query, key or value that is
+ * than 32 MB apart, strides whose extents 64 bits do not count, or more than
+ * 2^32 threads.  A query, key or value that is
  * not finite reaches only the rows that see it, where a NaN gives NaN (a value
  * in its column alone) and an infinite value itself, or NaN under a weight that
  * dtype rounds to 0.  Data preconditions: cu_draft and cu_groups prefix
@@ -666,9 +667,9 @@ SV_API sv_status_t spec_adjust_logits(const sv_adjust_shape_t* shape,
  * Errors as for spec_verify_sample; SV_ERR_INVALID_ARGUMENT also for q_heads no
  * multiple of kv_heads and for rows of out that overlap; SV_ERR_UNSUPPORTED also
  * for fp32, another head_dim, a page_size with a page_table that is no multiple of 16, more than 2^30 positions of a
- * sequence, positions more than 32 MB apart, strides whose extents 64 bits do not count, batch * kv_heads * positions / 64 of
- * 2^31 or more, or more than 2^32 threads.  out may be q
- * itself; it may not overlap the inputs otherwise.
+ * sequence, positions more than 32 MB apart, strides whose extents 64 bits do not
+ * count, batch * kv_heads * positions / 64 of 2^31 or more, or more than 2^32
+ * threads.  out may be q itself; it may not overlap the inputs otherwise.
  */
 typedef struct {
     int32_t batch;             /* B >= 1                                      */
@@ -807,8 +808,8 @@ SV_API sv_status_t spec_cache_compact(const sv_compact_shape_t* shape,
  * Memory, execution, workspace and errors as for spec_verify_sample;
  * SV_ERR_INVALID_ARGUMENT also as for spec_cache_compact, and for beams > 0 with batch or
  * old no multiple of it; SV_ERR_UNSUPPORTED also for more than 2^31 - 1 table entries,
- * old or new, more than 2^30 positions of a sequence, and pools as for
- * spec_cache_compact.
+ * old or new, more than 2^30 positions of a sequence, a page of all slabs and heads
+ * of more than 2^31 - 1 pieces, and more than 2^32 threads.
  */
 typedef struct {
     sv_pool_t pool;

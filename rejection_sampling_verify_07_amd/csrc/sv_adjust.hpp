@@ -19,10 +19,11 @@
 // a workspace.
 //
 // 320 rows of 151936 bf16 logits, texts of up to 8000 tokens, three of four sequences
-// under masks, in place: 45 us with the logits in the caches, 49 with them in memory.
-// The masks alone take 21 (almost every line of a masked row is written), the penalties
-// alone 30: elements scattered over lines, and before them the chain of the text's read,
-// the counts and the list.  43 ragged rows of 32003 fp16 logits, apart: 9.0 us; one row of
+// under masks, in place (97 MB): 45 us where the 256 MB cache holds the logits, 49 with
+// three such sets in turn, 59 with four.  The masks alone take 21 and 28 of the 45 and 59
+// (almost every line of a masked row is written), the penalties and biases alone 32 and
+// 34: elements scattered over lines, and before them the chain of the text's read, the
+// counts and the list.  43 ragged rows of 32003 fp16 logits, apart: 9.0 us; one row of
 // 50304 fp32 logits, in place: 4.8 us, a launch and that chain.
 //
 // Arithmetic is fp32, each step rounded, the result rounded to the element type once.

@@ -28,9 +28,11 @@
 // positions 169 us, 5.4 TB/s.  There the slowest workgroup ends 15% behind the mean (a
 // CU's older workgroup leads, and of two neighbouring XCDs one): shorter stretches or a
 // second, finer deal cost in parts and starts what they even out.  Many rows are bound by
-// vector and matrix instructions that overlap in part: 16 trees of 64 rows, 32/8 heads
-// of 128, 2048 to 16384 positions 240 us, 675 TFLOP/s.  Few keys are bound by two launches
-// and four trips to memory: 2 rows of 8 heads of 64 on 500 positions 10.6 us (7.6 + 3.2).
+// what lies between the products: 16 trees of 64 rows, 32/8 heads of 128, 2048 to 16384
+// positions 238 us, 680 TFLOP/s, the matrix cores busy for a third of the time, vector
+// instructions issued in two fifths of it; 16/4 heads of 256 411 us, 390 TFLOP/s (a wave
+// reads all of a tile from LDS for 16 rows).  Few keys are bound by two launches and four
+// trips to memory: 2 rows of 8 heads of 64 on 500 positions 10.4 us (7.5 + 3.0).
 #pragma once
 
 #include "sv_attention.hpp"

@@ -33,8 +33,11 @@ constexpr int32_t kAdjustFewBiases = 65535;
 // fp32 logits under masks: 30 us with 256, 29.5 with 1024, 48 with 4096; 4 of 9 bf16 rows 12.8, 11.5 and 16.2.
 constexpr int64_t kAdjustGroups = 1024;
 
-// Bytes of logits from which whole vectors are stored past the caches: 320 rows of 151936 bf16, four sets in turn, 59 us
-// and 62.5 through them (copied 70 and 75), 320 of 128256 fp32 copied 68 and 78; 43 rows of 32003 fp16 copied 9.4 and 9.2.
+// Bytes of logits (of all rows; in place only masked vectors are stored whole) from which whole vectors are stored past the
+// caches.  Past them and through them, bf16 rows of 151936, three of four sequences under masks: 320 rows in place 45 and 45
+// us with one set of logits, which the 256 MB cache holds, 48 and 54 with three in turn, 59 and 63 with four; four sets in
+// turn of 210 rows (64 MB) in place 36 and 37, apart 52 and 55; of 80 rows (24 MB) 23 and 23, apart 24 and 25.  Between
+// these, calls apart would gain too: 130 rows 29 and 36.
 constexpr double kAdjustPast = 64e6;
 
 sv_status_t check_adjust(const sv_adjust_shape_t* sh, const sv_adjust_t* ad, const void* logits, const void* out)

@@ -1,7 +1,8 @@
 """ctypes binding of the calls on trees of guesses (spec_tree_attention,
 spec_adjust_logits, spec_verify_tree_greedy, spec_verify_tree_sample;
 include/specverify.h): argument marshalling only.  Streams, devices and plans are
-as in beam.py.
+as in beam.py.  A cu_draft may end before the rows do (a step of fixed size that
+holds fewer guesses): rows behind the last sequence's are left as they were.
 """
 from __future__ import annotations
 
