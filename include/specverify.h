@@ -508,9 +508,9 @@ SV_API sv_status_t spec_prefix_attention(const sv_attention_shape_t* shape,
  * comes before its guesses.  parents (device int32 [total_draft]) NULL is the chain
  * (parent j).  Rows are laid out as in spec_verify_sample; the row after a guess
  * scores what follows it.
- *   In the calls on trees cu_draft[B] may be less than total_draft (a step of fixed size
- * that holds fewer guesses): rows and slots behind the last sequence's are left as they
- * were.
+ *   In this and the calls below cu_draft[B] may be less than total_draft (a step of fixed
+ * size that holds fewer guesses): rows and slots behind the last sequence's are left as
+ * they were.
  *   Every row r has its own token y_r.  From row 0 on, the first guess (lowest j)
  * that extends the row and equals y of the row is accepted and its row is next; at
  * a row without one the walk ends, and y of that row is the new token.
